@@ -260,7 +260,7 @@ def prepare(c, seed):
             from dictionary_sparse_kv_gb300 import fadkv as F
             s["plan"] = F.paged_params(s["q"], s["out"], s["k_pages"], c["pool"], s["table"], window=c["window"], sinks=c["sinks"])
             ask = F.paged_attend_workspace_bytes if c["op"] == "decode" else F.paged_prefill_workspace_bytes
-            s["workspace"] = torch.empty(max(1, ask(s["plan"])), dtype=torch.uint8, device=DEV)
+            s["workspace"] = torch.zeros(max(1, ask(s["plan"])), dtype=torch.uint8, device=DEV)
     return s
 
 
