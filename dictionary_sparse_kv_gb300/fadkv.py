@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(_PKG, "_build", "libfadkv.so")
 
 F16 = 0
 F32 = 1
+BF16 = 2                                  # the paged-cache calls only
 STATS_FIELDS = 8
 STATS_NAMES = ("encoded", "replaced", "flagged", "overflow", "nonfinite", "topn_slow_path", "status", "reserved")
 DEV_NONFINITE_INPUT = 0x1
@@ -72,6 +73,32 @@ class AttnParams(C.Structure):
     ]
 
 
+class PageParams(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("B", "page_size", "num_pages", "max_pages", "max_tokens")]
+
+
+class RopeParams(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("d", "rotary_dim", "interleaved", "scaling")] + [
+        (n, C.c_double) for n in ("base", "factor", "original", "slow", "fast", "amplitude")]
+
+
+class Rope(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("d", "rotary_dim", "interleaved")] + [
+        ("amplitude", C.c_float), ("turns", C.c_uint64 * 64)]
+
+
+class QkParams(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("T", "Hq", "Hkv", "d", "dtype", "q_dtype", "kv_dtype", "page_size",
+                                         "num_pages")] + [("eps", C.c_float)] + [
+        (n, C.c_int64) for n in ("q_stride", "k_stride", "v_stride", "page_stride", "head_stride", "token_stride")]
+
+
+class PagedParams(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("B", "T", "Hq", "Hkv", "d", "dtype", "page_size", "num_pages", "max_pages",
+                                         "window", "sinks")] + [("scale", C.c_float)] + [
+        (n, C.c_int64) for n in ("q_stride", "out_stride", "page_stride", "head_stride", "token_stride")]
+
+
 def params(num_dicts, N, d, n, s, dtype=F16, max_batch=1, lambda_abs=1e-4, lambda_rel=0.20) -> Params:
     """Handle parameters; the ridge defaults are Table 5's 1e-4 + 0.20 diag(G)."""
     return Params(num_dicts, N, d, n, s, lambda_abs, lambda_rel, dtype, max_batch)
@@ -112,6 +139,13 @@ _SIGS = {
     "fadkv_attend": ([C.POINTER(AttnParams), C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
                       C.c_void_p, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p], C.c_int),
     "fadkv_attend_workspace_bytes": ([C.POINTER(AttnParams), C.POINTER(C.c_size_t)], C.c_int),
+    "fadkv_page_plan": ([C.POINTER(PageParams)] + [C.c_void_p] * 12, C.c_int),
+    "fadkv_rope_init": ([C.POINTER(RopeParams), C.POINTER(Rope)], C.c_int),
+    "fadkv_qk_norm_rope": ([C.POINTER(QkParams), C.POINTER(Rope)] + [C.c_void_p] * 12, C.c_int),
+    "fadkv_paged_attend": ([C.POINTER(PagedParams)] + [C.c_void_p] * 8 + [C.c_size_t, C.c_void_p], C.c_int),
+    "fadkv_paged_attend_workspace_bytes": ([C.POINTER(PagedParams), C.POINTER(C.c_size_t)], C.c_int),
+    "fadkv_paged_prefill": ([C.POINTER(PagedParams)] + [C.c_void_p] * 9 + [C.c_size_t, C.c_void_p], C.c_int),
+    "fadkv_paged_prefill_workspace_bytes": ([C.POINTER(PagedParams), C.POINTER(C.c_size_t)], C.c_int),
     "fadkv_profile_enable": ([C.c_void_p, C.c_int32], C.c_int),
     "fadkv_profile_select": ([C.c_void_p, C.c_uint32], C.c_int),
     "fadkv_profile_read": ([C.c_void_p, C.POINTER(C.c_int64), C.POINTER(C.c_double), C.c_int32], C.c_int),
@@ -264,6 +298,137 @@ def attend(p: AttnParams, dict_k, dict_v, cache_k, cache_v, lengths, q, out, wor
     _check("fadkv_attend", lib().fadkv_attend(C.byref(p), _addr(dict_k), _addr(dict_v), _addr(cache_k),
                                               _addr(cache_v), _addr(lengths), _addr(q), _addr(out),
                                               _addr(workspace), nbytes, st))
+
+
+# --- the paged cache of full key/value vectors ---
+
+ROPE_SCALING = {"plain": 0, "linear": 1, "stretch": 2, "parts": 3}
+
+
+def _dtype(t) -> int:
+    import torch
+    return {torch.float16: F16, torch.float32: F32, torch.bfloat16: BF16}[t.dtype]
+
+
+def _pool(pages, layout):
+    """(Hkv, page size, page stride, head stride, token stride) of a pool [pages][Hkv][page size][d] (layout
+    "head") or [pages][page size][Hkv][d] ("token"); any strides with the last dimension contiguous."""
+    if layout not in ("head", "token"):
+        raise ValueError(f"unknown pool layout {layout!r}")
+    h, t = (1, 2) if layout == "head" else (2, 1)
+    if pages.dim() != 4 or pages.stride(3) != 1:
+        raise ValueError("a pool has four dimensions, the last one contiguous")
+    return pages.shape[h], pages.shape[t], pages.stride(0), pages.stride(h), pages.stride(t)
+
+
+def page_params(B: int, page_size: int, num_pages: int, max_pages: int, max_tokens: int) -> PageParams:
+    return PageParams(B, page_size, num_pages, max_pages, max_tokens)
+
+
+def page_plan(p: PageParams, add, lengths, block_table, free_pages, free_count, lengths_out, free_count_out, starts,
+              positions, slots, refused, stream=None) -> None:
+    """Pages, positions and slots of one step's new tokens (see fadkv_page_plan)."""
+    st = _stream(stream, lengths)
+    _check("fadkv_page_plan", lib().fadkv_page_plan(C.byref(p), _addr(add), _addr(lengths), _addr(block_table),
+                                                    _addr(free_pages), _addr(free_count), _addr(lengths_out),
+                                                    _addr(free_count_out), _addr(starts), _addr(positions),
+                                                    _addr(slots), _addr(refused), st))
+
+
+def rope_init(d: int, rotary_dim: int, interleaved: bool = False, base: float = 10000.0, scaling: str = "plain",
+              factor: float = 1.0, original: float = 8192.0, slow: float = 1.0, fast: float = 4.0,
+              amplitude: float = 1.0) -> Rope:
+    """The rotation of positions as fadkv_qk_norm_rope takes it; kept by the caller."""
+    rp = RopeParams(d, rotary_dim, 1 if interleaved else 0, ROPE_SCALING[scaling], base, factor, original, slow, fast,
+                    amplitude)
+    out = Rope()
+    _check("fadkv_rope_init", lib().fadkv_rope_init(C.byref(rp), C.byref(out)))
+    return out
+
+
+def qk_params(q, k, v, q_out, k_pages, layout: str = "head", eps: float = 1e-6, kv_dtype=None) -> QkParams:
+    """Parameters of qk_norm_rope from tensors q [T][Hq][d], k, v [T][Hkv][d] (heads contiguous, rows at any
+    stride), q_out and a pool.  Without a pool (k_pages None) kv_dtype says the type of k_out."""
+    for x in (q, k, v):
+        if x.dim() != 3 or x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2]):
+            raise ValueError("q, k and v are [rows][heads][d] with the heads back to back")
+    if not q.dtype == k.dtype == v.dtype:
+        raise ValueError("q, k and v have one type")
+    T, Hq, d = q.shape
+    if k_pages is None:
+        hkv, ps, pages, strides = k.shape[1], 8, 0, (0, 0, 0)
+        kvt = _dtype(k) if kv_dtype is None else kv_dtype
+    else:
+        hkv, ps, *strides = _pool(k_pages, layout)
+        pages, kvt = k_pages.shape[0], _dtype(k_pages)
+    if k.shape != (T, hkv, d) or v.shape != k.shape:
+        raise ValueError("k and v are [T][Hkv][d], Hkv as in the pool")
+    return QkParams(T, Hq, hkv, d, _dtype(q), _dtype(q_out), kvt, ps, pages, eps, q.stride(0), k.stride(0), v.stride(0),
+                    *strides)
+
+
+def qk_norm_rope(p: QkParams, rope: Rope, q, k, v, wq, wk, positions, slots, q_out, k_out, k_pages, v_pages,
+                 stream=None) -> None:
+    """Norm and rotation of queries and keys, keys and values appended to the pools (see fadkv_qk_norm_rope)."""
+    st = _stream(stream, q, q_out)
+    _check("fadkv_qk_norm_rope", lib().fadkv_qk_norm_rope(C.byref(p), C.byref(rope), _addr(q), _addr(k), _addr(v),
+                                                          _addr(wq), _addr(wk), _addr(positions), _addr(slots),
+                                                          _addr(q_out), _addr(k_out), _addr(k_pages),
+                                                          _addr(v_pages), st))
+
+
+def paged_params(q, out, k_pages, layout: str = "head", block_table=None, window: int = 0, sinks: int = 0,
+                 scale=None, B=None, max_pages=None) -> PagedParams:
+    """Parameters of paged_attend / paged_prefill from tensors q, out [T][Hq][d] (heads contiguous), a pool and the
+    block tables [B][max_pages]."""
+    for x in (q, out):
+        if x.dim() != 3 or x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2]):
+            raise ValueError("q and out are [rows][heads][d] with the heads back to back")
+    if q.shape != out.shape or q.dtype != out.dtype or q.dtype != k_pages.dtype or k_pages.shape[3] != q.shape[2]:
+        raise ValueError("q, out and the pool have one type and head dimension, q and out one shape")
+    T, Hq, d = q.shape
+    hkv, ps, *strides = _pool(k_pages, layout)
+    if block_table is not None:
+        B, max_pages = block_table.shape
+        if not block_table.is_contiguous():
+            raise ValueError("block tables are contiguous")
+    return PagedParams(B, T, Hq, hkv, d, _dtype(q), ps, k_pages.shape[0], max_pages, window, sinks,
+                       d ** -0.5 if scale is None else scale, q.stride(0), out.stride(0), *strides)
+
+
+def paged_attend_workspace_bytes(p: PagedParams) -> int:
+    out = C.c_size_t(0)
+    _check("fadkv_paged_attend_workspace_bytes", lib().fadkv_paged_attend_workspace_bytes(C.byref(p), C.byref(out)))
+    return out.value
+
+
+def paged_prefill_workspace_bytes(p: PagedParams) -> int:
+    out = C.c_size_t(0)
+    _check("fadkv_paged_prefill_workspace_bytes", lib().fadkv_paged_prefill_workspace_bytes(C.byref(p), C.byref(out)))
+    return out.value
+
+
+def _nbytes(workspace) -> int:
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def paged_attend(p: PagedParams, k_pages, v_pages, block_table, lengths, q, out, lse, workspace, stream=None) -> None:
+    """Attention of one new token per request over the pages (see fadkv_paged_attend).  The workspace is
+    zero-filled before its first use."""
+    st = _stream(stream, q, out)
+    _check("fadkv_paged_attend", lib().fadkv_paged_attend(C.byref(p), _addr(k_pages), _addr(v_pages),
+                                                          _addr(block_table), _addr(lengths), _addr(q), _addr(out),
+                                                          _addr(lse), _addr(workspace), _nbytes(workspace), st))
+
+
+def paged_prefill(p: PagedParams, k_pages, v_pages, block_table, lengths, starts, q, out, lse=None, workspace=None,
+                  stream=None) -> None:
+    """Attention of each request's last tokens over the pages (see fadkv_paged_prefill)."""
+    st = _stream(stream, q, out)
+    _check("fadkv_paged_prefill", lib().fadkv_paged_prefill(C.byref(p), _addr(k_pages), _addr(v_pages),
+                                                            _addr(block_table), _addr(lengths), _addr(starts),
+                                                            _addr(q), _addr(out), _addr(lse), _addr(workspace),
+                                                            _nbytes(workspace), st))
 
 
 def reconstruct(h: int, V: int, idx, coef, repl_id, repl_coef, xhat, stream=None) -> None:

@@ -81,7 +81,9 @@ typedef enum {
     FADKV_ERR_WORKSPACE = 5      /* workspace too small */
 } fadkv_status;
 
-typedef enum { FADKV_F16 = 0, FADKV_F32 = 1 } fadkv_dtype;
+/* FADKV_BF16 is taken by the paged-cache calls only; dictionaries and codes
+   are binary16 or binary32. */
+typedef enum { FADKV_F16 = 0, FADKV_F32 = 1, FADKV_BF16 = 2 } fadkv_dtype;
 
 /* Device status word bits (per dictionary, see fadkv_dict_stats). */
 #define FADKV_DEV_NONFINITE_INPUT 0x1   /* an input held a NaN or infinity */
@@ -382,6 +384,204 @@ fadkv_status fadkv_attend(const fadkv_attn_params* params, const void* dict_k, c
    round_up(N, 16) bytes and a little more; binary32 dictionaries: 0 (the
    workspace may then be NULL).  Errors: INVALID_ARG, UNSUPPORTED. */
 fadkv_status fadkv_attend_workspace_bytes(const fadkv_attn_params* params, size_t* bytes);
+
+/* ---------------------------------------------------------------------------
+   The paged cache of full key/value vectors: what a decode loop keeps of the
+   vectors that are not coded (a prompt before its encode, the recent window
+   and the first tokens, or the whole cache in a full-KV run).  Handle-free:
+   every call works on caller-owned buffers only, asynchronously on `stream`,
+   and can be captured into a CUDA graph.
+
+   A pool holds num_pages pages of page_size tokens (a power of two, 8 ..
+   1024) for every key/value head; keys and values are two pools of one
+   layout.  Element (page, head, token in page, i) of a pool is at
+     page * page_stride + head * head_stride + token * token_stride + i
+   (strides in elements, multiples of 8; the pools 16-byte aligned).  Row b
+   of the block table [B][max_pages] int32 lists the pages of request b in
+   token order.  The slot of a token is page * page_size + token in page.
+   --------------------------------------------------------------------------- */
+#define FADKV_MAX_REQUESTS 16384   /* largest B of the paged-cache calls */
+
+typedef struct {
+    int32_t B;            /* requests, 0 .. FADKV_MAX_REQUESTS */
+    int32_t page_size;    /* tokens per page */
+    int32_t num_pages;    /* pages of a pool; num_pages * page_size < 2^31 */
+    int32_t max_pages;    /* block-table entries per request */
+    int32_t max_tokens;   /* rows of positions and slots */
+} fadkv_page_params;
+
+/* Plan of one step: gives the new tokens of every request their pages,
+   positions and slots, and takes back the pages of requests that ended.
+     add         [B] int32: new tokens of each request in this step; 0: none;
+                 negative: the request ends
+     lengths     [B] int32: tokens each request has cached (clamped to
+                 [0, max_pages * page_size])
+     block_table [B][max_pages] int32, in/out: entries of pages taken now are
+                 written, all others left as they are
+     free_pages  [num_pages] int32, in/out: the free pages are its first
+                 free_count entries
+     free_count  [1] int32 (clamped to [0, num_pages])
+     lengths_out [B] int32, free_count_out [1] int32: their values after the
+                 step; may be lengths and free_count themselves.  Kept apart,
+                 the call can be repeated on the same inputs.
+     starts      [B+1] int32: the requests' first rows among the step's tokens
+                 (exclusive prefix sum of max(add, 0), saturated at 2^31 - 1)
+     positions, slots  [max_tokens] int32: of every new token, request by
+                 request; -1 for the rows past starts[B] and for requests
+                 that are refused
+     refused     [1] int32: requests refused in this step
+   Order: first the ceil(lengths / page_size) pages of each ended request go
+   to the end of the free list (ascending request, then page; what would pass
+   num_pages is dropped), lengths_out = 0.  Then requests are served in
+   ascending order; page m taken in this step is entry F - 1 - m of the free
+   list, F its length after the returns.  A request is refused, and keeps its
+   length, when its tokens would pass max_pages * page_size, when its rows
+   would pass max_tokens, or when its pages and those that the requests
+   before it asked for are more than F.
+   All pointers are device pointers, 4-byte aligned.
+   Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+fadkv_status fadkv_page_plan(const fadkv_page_params* params, const int32_t* add, const int32_t* lengths,
+                             int32_t* block_table, int32_t* free_pages, const int32_t* free_count,
+                             int32_t* lengths_out, int32_t* free_count_out, int32_t* starts,
+                             int32_t* positions, int32_t* slots, int32_t* refused, void* stream);
+
+/* Rotation of positions.  Pair i of the rotated part (its first rotary_dim
+   elements) turns by position * f_i, f_i = base^(-2 i / rotary_dim) before
+   scaling for long contexts:
+     FADKV_ROPE_PLAIN    f_i
+     FADKV_ROPE_LINEAR   f_i / factor
+     FADKV_ROPE_STRETCH  f_i of the base base * factor^(rotary_dim / (rotary_dim - 2))
+     FADKV_ROPE_PARTS    with r = original * f_i / (2 pi) turns over the original
+                         length and g = clamp((r - slow) / (fast - slow), 0, 1):
+                         f_i * (g + (1 - g) / factor)
+   The rotated part is multiplied by amplitude (1 for none). */
+#define FADKV_ROPE_MAX_PAIRS 64
+typedef enum {
+    FADKV_ROPE_PLAIN = 0,
+    FADKV_ROPE_LINEAR = 1,
+    FADKV_ROPE_STRETCH = 2,
+    FADKV_ROPE_PARTS = 3
+} fadkv_rope_scaling;
+
+typedef struct {
+    int32_t d;            /* head dimension: 64 or 128 */
+    int32_t rotary_dim;   /* rotated elements: 0 (none) or a multiple of 16, <= d */
+    int32_t interleaved;  /* pairs (2i, 2i+1) if set, (i, i + rotary_dim/2) if not */
+    int32_t scaling;      /* fadkv_rope_scaling */
+    double base;          /* > 1 */
+    double factor;        /* >= 1 (LINEAR, STRETCH, PARTS) */
+    double original;      /* > 0, trained length (PARTS) */
+    double slow, fast;    /* slow < fast (PARTS) */
+    double amplitude;     /* finite */
+} fadkv_rope_params;
+
+/* The rotation as the kernel reads it: a plain host struct, filled by
+   fadkv_rope_init and kept by the caller. */
+typedef struct {
+    int32_t d, rotary_dim, interleaved;
+    float amplitude;
+    uint64_t turns[FADKV_ROPE_MAX_PAIRS];   /* f_i / (2 pi) in units of 2^-64 turns a position */
+} fadkv_rope;
+
+/* Host-only.  Errors: INVALID_ARG, UNSUPPORTED. */
+fadkv_status fadkv_rope_init(const fadkv_rope_params* params, fadkv_rope* out);
+
+typedef struct {
+    int32_t T;            /* rows (new tokens of the step) */
+    int32_t Hq, Hkv;      /* query and key/value heads */
+    int32_t d;            /* head dimension: 64 or 128 */
+    int32_t dtype;        /* of q, k, v and the norms' weights */
+    int32_t q_dtype;      /* of q_out */
+    int32_t kv_dtype;     /* of k_out and the pools */
+    int32_t page_size, num_pages;
+    float eps;            /* of the norms */
+    int64_t q_stride, k_stride, v_stride;   /* elements from one token to the next, multiples of 8 */
+    int64_t page_stride, head_stride, token_stride;   /* of the pools */
+} fadkv_qk_params;
+
+/* Norm, rotation and append of one step's keys, queries and values, in one
+   pass.  Every query and key head-vector x becomes
+     rotate(x / sqrt(mean(x^2) + eps) * w)
+   in 32 bits, rounded once on storing; a null w leaves the norm out.
+     q, k, v     rows of Hq (Hkv) heads of d elements, heads back to back, rows
+                 q_stride (k_stride, v_stride) apart (three parts of one
+                 projection's output, say); 16-byte aligned
+     wq, wk      [d] or null
+     positions   [T] int32; a row with a negative position is empty: its
+                 q_out and k_out are 0 and nothing of it enters the pools
+     slots       [T] int32: where row t's key and value go in the pools; slots
+                 outside [0, num_pages * page_size) are skipped.  A slot may
+                 appear once at most.  Null: nothing is appended.
+     q_out       [T][Hq][d], e.g. binary32 for fadkv_attend
+     k_out       [T][Hkv][d] or null: the keys as fadkv_encode takes them
+                 (v = t * Hkv + h) with kv_dtype the dictionary's type
+     k_pages, v_pages  pools (null with null slots)
+   16-byte aligned throughout (positions, slots 4).  rope->d must equal d.
+   Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+fadkv_status fadkv_qk_norm_rope(const fadkv_qk_params* params, const fadkv_rope* rope, const void* q,
+                                const void* k, const void* v, const void* wq, const void* wk,
+                                const int32_t* positions, const int32_t* slots, void* q_out, void* k_out,
+                                void* k_pages, void* v_pages, void* stream);
+
+typedef struct {
+    int32_t B;            /* requests, 0 .. FADKV_MAX_REQUESTS */
+    int32_t T;            /* query rows of all requests */
+    int32_t Hq;           /* query heads (a multiple of Hkv); head h reads KV head h / (Hq / Hkv) */
+    int32_t Hkv;
+    int32_t d;            /* head dimension: 64 or 128 */
+    int32_t dtype;        /* of q, the pools and out: FADKV_F16 or FADKV_BF16 */
+    int32_t page_size, num_pages, max_pages;
+    int32_t window;       /* a query sees its last `window` tokens, itself among them; 0: all */
+    int32_t sinks;        /* first tokens that stay visible beside the window */
+    float scale;          /* score scale, 1/sqrt(d) for standard attention */
+    int64_t q_stride, out_stride;   /* elements from one row of q (out) to the next; heads back to back */
+    int64_t page_stride, head_stride, token_stride;   /* of the pools */
+} fadkv_paged_params;
+
+/* Attention of one new token per request over the paged cache (T = B):
+     out[b][h] = sum_j p_j v_j,  p = softmax_j(scale <q[b][h], k_j>),
+     lse[b][h] = log sum_j exp(scale <q[b][h], k_j>),
+   over the tokens j < lengths[b] that the query at position lengths[b] - 1
+   sees: all, or with a window those with j > position - window or j < sinks.
+   Tokens on pages outside [0, num_pages) are not seen.  A query that sees
+   nothing gets out = 0 and lse = -inf.
+     lengths     [B] int32, the new token included, clamped to
+                 [0, max_pages * page_size]
+     q           rows of Hq heads, 16-byte aligned; out likewise
+     lse         [T][Hq] float32, or null
+     workspace   >= fadkv_paged_attend_workspace_bytes bytes, 256-byte aligned,
+                 ZERO-FILLED before its first use (each call leaves it fit for
+                 the next, whatever that call's parameters); not to be shared
+                 by calls that may run concurrently
+   Scores, softmax and sums in 32 bits; the probabilities enter the product
+   with the values as two 16-bit terms each.
+   Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+fadkv_status fadkv_paged_attend(const fadkv_paged_params* params, const void* k_pages, const void* v_pages,
+                                const int32_t* block_table, const int32_t* lengths, const void* q, void* out,
+                                float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Device workspace fadkv_paged_attend needs (host-only; writes *bytes).
+   Errors: INVALID_ARG, UNSUPPORTED. */
+fadkv_status fadkv_paged_attend_workspace_bytes(const fadkv_paged_params* params, size_t* bytes);
+
+/* The same attention for several new tokens per request (a prompt, or a chunk
+   of it on top of cached tokens): rows starts[b] .. starts[b+1]-1 of q are
+   the last tokens of request b, row i of its n at position lengths[b] - n + i.
+   Keys and values of the new tokens are in the pools already.
+     starts      [B+1] int32 as fadkv_page_plan writes them: 0, ascending; rows
+                 at and past T are left out.  Rows of q past starts[B] are not
+                 read and their out and lse not written.
+   Rows at a negative position see nothing (out = 0, lse = -inf).  What the
+   pools hold where no row sees it is never used; a value that is not finite
+   and that one row sees may reach other rows of its request.  The
+   probabilities enter the product with the values in the type of the pools.
+   Other arguments and errors as for fadkv_paged_attend; the workspace
+   (fadkv_paged_prefill_workspace_bytes) may be null where 0 bytes are asked. */
+fadkv_status fadkv_paged_prefill(const fadkv_paged_params* params, const void* k_pages, const void* v_pages,
+                                 const int32_t* block_table, const int32_t* lengths, const int32_t* starts,
+                                 const void* q, void* out, float* lse, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+fadkv_status fadkv_paged_prefill_workspace_bytes(const fadkv_paged_params* params, size_t* bytes);
 
 /* Kernel classes reported by fadkv_profile_read. */
 #define FADKV_PROFILE_KERNELS 8
