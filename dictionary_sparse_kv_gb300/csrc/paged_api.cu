@@ -37,7 +37,7 @@ int log2_exact(int v)
 
 bool page_size_ok(int ps) { return ps >= 8 && ps <= 1024 && (ps & (ps - 1)) == 0; }
 
-bool stride_ok(int64_t s, int64_t least) { return s >= least && s % 8 == 0 && s < ((int64_t)1 << 40); }
+bool stride_ok(int64_t s, int64_t least) { return s >= least && s % 8 == 0 && s < ((int64_t)1 << 38); }
 
 // Pool shape: sizes and strides.
 fadkv_status check_pool(int page_size, int num_pages, int d, int64_t page_stride, int64_t head_stride,
@@ -54,6 +54,7 @@ fadkv_status check_paged(const fadkv_paged_params* p)
 {
     if (!p) return FADKV_ERR_INVALID_ARG;
     if (p->B < 0 || p->T < 0 || p->Hq < 1 || p->Hkv < 1 || p->Hq % p->Hkv != 0 || p->max_pages < 1 ||
+        p->num_pages < 1 ||
         p->window < 0 || p->sinks < 0 || !isfinite(p->scale))
         return FADKV_ERR_INVALID_ARG;
     if (p->dtype != FADKV_F16 && p->dtype != FADKV_F32 && p->dtype != FADKV_BF16) return FADKV_ERR_INVALID_ARG;

@@ -241,6 +241,9 @@ __device__ __forceinline__ void mbar_arrive_peer(uint32_t remote_bar)
 
 }  // namespace tc
 
+// Host: the driver's tensor-map encoder, or null.
+PFN_cuTensorMapEncodeTiled_v12000 tma_encode_fn();
+
 // Host: TMA descriptor of a [rows][d] binary16 matrix, boxes of 64 elements
 // x box_rows rows, 128-byte swizzle.  False if the driver entry point is
 // missing or rejects the arguments.

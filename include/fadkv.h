@@ -575,8 +575,12 @@ fadkv_status fadkv_paged_attend_workspace_bytes(const fadkv_paged_params* params
    pools hold where no row sees it is never used; a value that is not finite
    and that one row sees may reach other rows of its request.  The
    probabilities enter the product with the values in the type of the pools.
-   Other arguments and errors as for fadkv_paged_attend; the workspace
-   (fadkv_paged_prefill_workspace_bytes) may be null where 0 bytes are asked. */
+   workspace   >= fadkv_paged_prefill_workspace_bytes bytes, 256-byte aligned,
+               ZERO-FILLED before its first use.  Its first 8 bytes are a
+               status word: FADKV_DEV_TIMEOUT is set in it if a kernel gave
+               up waiting on its own pipeline (that call's out is then not
+               complete)
+   Other arguments and errors as for fadkv_paged_attend. */
 fadkv_status fadkv_paged_prefill(const fadkv_paged_params* params, const void* k_pages, const void* v_pages,
                                  const int32_t* block_table, const int32_t* lengths, const int32_t* starts,
                                  const void* q, void* out, float* lse, void* workspace,
