@@ -54,7 +54,7 @@ template <int D> struct PreCfg {
     static constexpr int NST = D == 128 ? 5 : 8;   // stages of the K / V ring
     static constexpr int TILE = kRows * D * 2;     // bytes of a Q, K or V tile
     static constexpr int bar_off = (2 + NST) * TILE;
-    static constexpr int n_bars = 2 * NST + 8 + kFix;
+    static constexpr int n_bars = 2 * NST + 10 + kFix;
     static constexpr int ok_off = bar_off + n_bars * 8;
     static constexpr int alloc = ok_off + kOkRing * 20 + 16 + 1024;
     static_assert(alloc <= 227 * 1024, "shared memory");
@@ -105,6 +105,45 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         : "memory");
 }
 
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 104;"); }
+
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Two 32-bit values in one register pair: one instruction for both.
+__device__ __forceinline__ uint64_t pair(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // Bits 0 .. n-1 set (none for n <= 0, all for n >= 32).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
@@ -124,13 +163,13 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto empty = [&](int s) { return bar0 + 8u * (NST + s); };
     auto sfull = [&](int q) { return bar0 + 8u * (2 * NST + q); };
-    auto pfull = [&](int q) { return bar0 + 8u * (2 * NST + 2 + q); };
-    auto pvdone = [&](int q) { return bar0 + 8u * (2 * NST + 4 + q); };
-    auto qfull = [&](int q) { return bar0 + 8u * (2 * NST + 6 + q); };
-    auto fixed = [&](int j) { return bar0 + 8u * (2 * NST + 8 + (j & (kFix - 1))); };
+    auto pvdone = [&](int q) { return bar0 + 8u * (2 * NST + 2 + q); };
+    auto qfull = [&](int q) { return bar0 + 8u * (2 * NST + 4 + q); };
+    auto pfull = [&](int q, int half) { return bar0 + 8u * (2 * NST + 6 + 2 * q + half); };
+    auto fixed = [&](int j) { return bar0 + 8u * (2 * NST + 10 + (j & (kFix - 1))); };
     unsigned long long* status = reinterpret_cast<unsigned long long*>(a.ws);
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int grp = a.grp, B = a.p.B;
     const int gch = min(grp, kRows), chunks = (grp + gch - 1) / gch, tq = kRows / gch;   // tokens per tile
     const int heads = a.p.Hkv * chunks, per_cta = 2 * tq;
@@ -161,7 +200,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         }
         for (int q = 0; q < 2; ++q) {
             mbar_init(sfull(q), 1);
-            mbar_init(pfull(q), 128);
+            mbar_init(pfull(q, 0), 4);
+            mbar_init(pfull(q, 1), 4);
             mbar_init(pvdone(q), 1);
             mbar_init(qfull(q), 128);
         }
@@ -176,9 +216,9 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tbase = s_taddr;
+    const uint32_t tbase = __shfl_sync(0xffffffffu, s_taddr, 0);
 
-    const int b = s_b, t0 = s_tile * per_cta, start = a.starts[b];
+    const int b = __shfl_sync(0xffffffffu, s_b, 0), t0 = __shfl_sync(0xffffffffu, s_tile, 0) * per_cta, start = a.starts[b];
     const int nt = min(per_cta, rows_of(b) - t0);      // tokens of this CTA
     const int nq = nt > tq ? 2 : 1;                    // tiles that hold any
     const int len = clamp_len(a.lengths[b], a);
@@ -190,13 +230,16 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     const int tiles_to = last >= 0 ? last / kKeys + 1 : 0;
     const int from = W > 0 ? max(0, first - W + 1) / kKeys : 0;
     const int sink_tiles = W > 0 ? min(from, (S + kKeys - 1) / kKeys) : 0;
-    const int tiles = tiles_to > from ? sink_tiles + tiles_to - from : 0;
+    const int tiles = __shfl_sync(0xffffffffu, tiles_to > from ? sink_tiles + tiles_to - from : 0, 0);
     auto key0 = [&](int i) { return (i < sink_tiles ? i : i - sink_tiles + from) * kKeys; };
     // whether some row of the CTA sees a key; whether a tile holds keys that none sees
     auto seen = [&](int key) { return key <= last && (W == 0 || key > first - W || key < S); };
     auto ragged = [&](int k0) { return !(k0 + kKeys - 1 <= last && (W == 0 || k0 > first - W || k0 + kKeys <= S)); };
 
+    // Registers: 168 a thread at launch (384 threads, 64512 in all); the four
+    // service warps keep 104, the eight softmax warps take 200.
     if (warp == 0) {
+        regs_dec();
         // ---------------- K and V pages ----------------
         const int rows = min(1 << a.shift, kKeys), boxes = kKeys / rows * HALVES;   // at most 32
         const int row = lane / HALVES * rows, half = lane % HALVES;
@@ -248,64 +291,98 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         // drain: every issued load lands before the CTA exits
         for (int i = max(0, issued - NST); i < issued; ++i) mbar_wait(full(i % NST), (uint32_t)(i / NST) & 1u, status);
     } else if (warp == 1) {
+        regs_dec();
         // ---------------- products ----------------
-        if (lane == 0 && tiles > 0) {
+        // The whole warp walks the tiles, so that descriptors and addresses stay in
+        // uniform registers; one thread issues.  (With the walk in one thread alone
+        // each product costs about 90 cycles to issue, against 64 to run.)
+        if (tiles > 0) {
             constexpr uint32_t kQK = idesc_of<T>(kRows, kKeys, false), kPV = idesc_of<T>(kRows, D, true);
+            const bool leader = elect_one();
             bool ok = true;
             int pvs[2] = {0, 0}, qks[2] = {0, 0};
-            auto wait_ring = [&](int r) { return mbar_wait(full(r % NST), (uint32_t)(r / NST) & 1u, status); };
-            auto qk = [&](int q, int i) {
-                const uint32_t sk = sR + (2 * i % NST) * TILE, qa = sQ + q * TILE;
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (uint32_t)((k >> 2) * 128 * 128 + (k & 3) * 32);
-                    mma_ss(tbase + C::S(q), sdesc(qa + off), sdesc(sk + off), kQK, k > 0 ? 1u : 0u);
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
+            };
+            // stage and parity of the next ring entry: K and V in turn
+            int st = 0;
+            uint32_t ph = 0;
+            auto next_entry = [&] {
+                if (++st == NST) {
+                    st = 0;
+                    ph ^= 1u;
                 }
-                mma_commit(sfull(q));
+            };
+            const uint64_t dq0 = sdesc(sQ), dr0 = sdesc(sR), dn0 = sdesc_n(sR);
+            // descriptors count in 16 bytes: 32 bytes a step of 16 elements, a half of 64 elements one panel on
+            auto qk = [&](int q, int stage) {
+                const uint64_t dq = dq0 + (uint64_t)(q * (TILE >> 4)), dk = dr0 + (uint64_t)(stage * (TILE >> 4));
+                if (leader) {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint64_t off = (uint64_t)(((k >> 2) * 128 * 128 + (k & 3) * 32) >> 4);
+                        mma_ss(tbase + C::S(q), dq + off, dk + off, kQK, k > 0 ? 1u : 0u);
+                    }
+                    mma_commit(sfull(q));
+                }
                 ++qks[q];
             };
-            auto pv = [&](int q, int i) {
-                const uint32_t sv = sR + ((2 * i + 1) % NST) * TILE;
+            // one half of the keys
+            auto pv = [&](int q, int stage, int half, bool add) {
+                const uint64_t dv = dn0 + (uint64_t)(stage * (TILE >> 4) + half * (kKeys / 2 * 128 >> 4));
+                if (leader)
 #pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                    mma_ts(tbase + C::O(q), tbase + C::P(q) + k * 8, sdesc_n(sv + k * 2048), kPV, i > 0 || k > 0 ? 1u : 0u);
-                mma_commit(pvdone(q));
-                ++pvs[q];
+                    for (int j = 0; j < kKeys / 32; ++j)
+                        mma_ts(tbase + C::O(q), tbase + C::P(q) + (half * (kKeys / 32) + j) * 8, dv + (uint64_t)(j * 2048 >> 4),
+                               kPV, add || j > 0 ? 1u : 0u);
             };
-            for (int q = 0; q < nq && ok; ++q) ok = mbar_wait(qfull(q), 0u, status);
-            ok = ok && wait_ring(0);
+            for (int q = 0; q < nq; ++q) wait(qfull(q), 0u);
+            wait(full(0), 0u);
             if (ok) {
                 fence_after();
                 for (int q = 0; q < nq; ++q) qk(q, 0);
-                mma_commit(empty(0));
+                if (leader) mma_commit(empty(0));
+                next_entry();
             }
             for (int i = 0; i < tiles && ok; ++i) {
-                for (int q = 0; q < nq && ok; ++q) {
-                    ok = mbar_wait(pfull(q), (uint32_t)i & 1u, status);
+                const int sv = st;
+                const uint32_t pv_ph = ph;
+                next_entry();                              // now the next tile's K
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    if (q >= nq || !ok) continue;
                     if (q == 0) {
-                        ok = ok && wait_ring(2 * i + 1);
-                        ok = ok && mbar_wait(fixed(i), (uint32_t)(i / kFix) & 1u, status);
+                        wait(full(sv), pv_ph);
+                        wait(fixed(i), (uint32_t)(i / kFix) & 1u);
                     }
+                    wait(pfull(q, 0), (uint32_t)i & 1u);
                     if (!ok) break;
                     fence_after();
-                    pv(q, i);
-                    if (q == nq - 1) mma_commit(empty((2 * i + 1) % NST));
+                    pv(q, sv, 0, i > 0);
+                    wait(pfull(q, 1), (uint32_t)i & 1u);
+                    if (q == 0 && i + 1 < tiles) wait(full(st), ph);
+                    if (!ok) break;
+                    fence_after();
+                    pv(q, sv, 1, true);
+                    if (leader) mma_commit(pvdone(q));
+                    ++pvs[q];
+                    if (q == nq - 1 && leader) mma_commit(empty(sv));
                     if (i + 1 < tiles) {
-                        if (q == 0) ok = wait_ring(2 * i + 2);
-                        if (!ok) break;
-                        fence_after();
-                        qk(q, i + 1);
-                        if (q == nq - 1) mma_commit(empty((2 * i + 2) % NST));
+                        qk(q, st);
+                        if (q == nq - 1 && leader) mma_commit(empty(st));
                     }
                 }
+                next_entry();
             }
             // drain: the last products of each tile are complete before TMEM is freed
             for (int q = 0; q < 2; ++q) {
                 if (qks[q] > 0) mbar_wait(sfull(q), (uint32_t)(qks[q] - 1) & 1u, status);
                 if (pvs[q] > 0) mbar_wait(pvdone(q), (uint32_t)(pvs[q] - 1) & 1u, status);
             }
+            __syncwarp();
         }
     } else if (warp == 2) {
+        regs_dec();
         // ---------------- value rows that no row sees: zeros ----------------
         // Every value tile passes here on its way to the product, so that this
         // warp stays within one round of the ring.
@@ -328,7 +405,10 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
             }
             if (lane == 0) mbar_arrive(fixed(i));
         }
-    } else if (warp >= 4) {
+    } else if (warp == 3) {
+        regs_dec();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         // ---------------- softmax ----------------
         const int q = (warp - 4) >> 2, r = tid & 127;
         if (q < nq) {
@@ -391,11 +471,12 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     float x[4];
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        x[c] = __uint_as_float(s[c][0]);
+                        x[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
 #pragma unroll
-                        for (int j = 1; j < 32; ++j) x[c] = fmaxf(x[c], __uint_as_float(s[c][j]));
+                        for (int j = 2; j < 32; j += 2)
+                            x[c] = max3(x[c], __uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1]));
                     }
-                    mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * scale;
+                    mx = fmaxf(max3(x[0], x[1], x[2]), x[3]) * scale;
                 }
                 const bool grow = mx > m + kGrow;
                 if (__any_sync(0xffffffffu, grow)) {
@@ -423,23 +504,31 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                     }
                 }
                 const float mm = m == -INFINITY ? 0.f : m;     // nothing seen yet: every p is 0
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t sc2 = pair(scale, scale), mm2 = pair(-mm, -mm);
+                uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t p[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const float p0 = exp2_fast(fmaf(__uint_as_float(s[c][2 * j]), scale, -mm));
-                        const float p1 = exp2_fast(fmaf(__uint_as_float(s[c][2 * j + 1]), scale, -mm));
-                        sum[j & 3] += p0 + p1;
+                        float p0, p1;
+                        unpair(fma2(pair(__uint_as_float(s[c][2 * j]), __uint_as_float(s[c][2 * j + 1])), sc2, mm2), p0, p1);
+                        p0 = exp2_fast(p0);
+                        p1 = exp2_fast(p1);
+                        sum[j & 1] = add2(sum[j & 1], pair(p0, p1));
                         p[j] = Num<T>::pack(p0, p1);
                     }
                     tmem_st16(lanes + C::P(q) + c * 16, p);
+                    if (c & 1) {                               // half of the keys: the product may begin
+                        tmem_st_wait();
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(pfull(q, c >> 1));
+                    }
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tmem_st_wait();
-                fence_before();
-                mbar_arrive(pfull(q));
+                float x0, x1;
+                unpair(add2(sum[0], sum[1]), x0, x1);
+                l += x0 + x1;
             }
             if (tiles > 0 && ok) {
                 ok = mbar_wait(pvdone(q), (uint32_t)(tiles - 1) & 1u, status);
