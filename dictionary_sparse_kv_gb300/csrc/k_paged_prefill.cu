@@ -30,8 +30,14 @@
 // page holds past the tokens that the tile sees may be anything, so its value
 // rows are zeroed in shared memory before the product (0 x NaN would be NaN).
 //
-// Warps: 0 TMA, 1 MMA, 2 TMEM and the zeroing, 4..7 and 8..11 softmax of the
-// two tiles.  Every wait is bounded; one that runs out sets
+// CTAs are persistent, one a multiprocessor, and take items (two tiles of one
+// request and KV head) from a counter, a request's last tiles, which see the
+// most keys, first.  The next item's queries and first pages are on their way
+// while the last tiles of the current one are worked on; only the reading of
+// O by the softmax warps stands between two items' products.
+//
+// Warps: 0 TMA, 1 MMA, 2 TMEM and the zeroing, 3 the items, 4..7 and 8..11
+// softmax of the two tiles.  Every wait is bounded; one that runs out sets
 // FADKV_DEV_TIMEOUT in the workspace's first word, and the CTA drains and
 // returns.
 #include "paged.cuh"
@@ -50,19 +56,32 @@ constexpr int kFix = 4;                            // barriers of the zeroing, i
 constexpr int kOkRing = 16;                        // key tiles whose page masks are kept
 constexpr float kGrow = 8.f;                       // growth of the maximum (log2) that rescales
 
+constexpr int kPreCtas = 152;                      // one per multiprocessor
+constexpr int kItemReaders = 11;                   // warps that read an item
+
 template <int D> struct PreCfg {
     static constexpr int NST = D == 128 ? 5 : 8;   // stages of the K / V ring
     static constexpr int TILE = kRows * D * 2;     // bytes of a Q, K or V tile
     static constexpr int bar_off = (2 + NST) * TILE;
-    static constexpr int n_bars = 2 * NST + 10 + kFix;
+    static constexpr int n_bars = 2 * NST + 16 + kFix + 2;
     static constexpr int ok_off = bar_off + n_bars * 8;
     static constexpr int alloc = ok_off + kOkRing * 20 + 16 + 1024;
-    static_assert(alloc <= 227 * 1024, "shared memory");
+    static_assert(alloc <= 227 * 1024 - 256, "shared memory");
     // TMEM columns.  d = 128: P over the first half of its S (the products of
-    // one thread with one shape run in order); d = 64: room for its own.
+    // one thread with one shape run in order); d = 64: room for its own, so
+    // the next scores need not wait for the product that reads P.
+    static constexpr bool kOwnP = D == 64;
     static constexpr int S(int q) { return q * 128; }
     static constexpr int O(int q) { return 256 + q * D; }
-    static constexpr int P(int q) { return D == 128 ? q * 128 : 384 + q * 64; }
+    static constexpr int P(int q) { return kOwnP ? 384 + q * 64 : q * 128; }
+};
+
+// An item as the scheduling warp hands it to the others.
+struct Item {
+    int live;                  // 0: no more items
+    int row0, nt;              // first row of q, tokens
+    int first, len;            // position of the first row; tokens of the request
+    int b, head0, hk, hn;      // request, first query head, KV head, query heads
 };
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar)
@@ -70,6 +89,14 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
     asm volatile(
         "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
         ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
 
@@ -91,6 +118,8 @@ template <typename T> __host__ __device__ constexpr uint32_t idesc_of(int M, int
     const uint32_t t = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
     return idesc_f16(M, N) | (t << 7) | (t << 10) | (b_n_major ? 1u << 16 : 0u);
 }
+
+constexpr uint32_t kNegateA = 1u << 13;            // of the instruction descriptor
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32])
 {
@@ -147,52 +176,76 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 // Bits 0 .. n-1 set (none for n <= 0, all for n >= 32).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
+// The key tiles of an item: those of the first tokens, then those of the
+// window (or all).
+struct Tiles {
+    int first, last, W, S, from, sinks, count;
+    __device__ __forceinline__ Tiles(const Item& it, const PagedArgs& a)
+    {
+        first = it.first;
+        last = it.first + it.nt - 1;
+        W = min(a.p.window, 1 << 30);
+        S = min(a.p.sinks, it.len);
+        const int to = last >= 0 ? last / kKeys + 1 : 0;
+        from = W > 0 ? max(0, first - W + 1) / kKeys : 0;
+        sinks = W > 0 ? min(from, (S + kKeys - 1) / kKeys) : 0;
+        count = to > from ? sinks + to - from : 0;
+    }
+    __device__ __forceinline__ int key0(int i) const { return (i < sinks ? i : i - sinks + from) * kKeys; }
+    // whether some row of the item sees a key; whether a tile holds keys that none sees
+    __device__ __forceinline__ bool seen(int key) const { return key <= last && (W == 0 || key > first - W || key < S); }
+    __device__ __forceinline__ bool ragged(int k0) const
+    {
+        return !(k0 + kKeys - 1 <= last && (W == 0 || k0 > first - W || k0 + kKeys <= S));
+    }
+};
+
+// Stage and parity of the ring's next entry.
+template <int NST> struct Ring {
+    int st = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++st == NST) {
+            st = 0;
+            ph ^= 1u;
+        }
+    }
+};
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kPreThreads, 1)
-paged_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
-                     const __grid_constant__ PagedArgs a)
+paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                     const __grid_constant__ CUtensorMap map_v, const __grid_constant__ PagedArgs a)
 {
     using C = PreCfg<D>;
     constexpr int NST = C::NST, HALVES = D / 64, TILE = C::TILE;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ int s_b, s_tile;
     __shared__ uint32_t s_taddr;
+    __shared__ Item s_item;
     unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sQ = smem_u32(smem), sR = sQ + 2 * TILE, bar0 = sQ + C::bar_off;
     uint32_t* ok_ring = reinterpret_cast<uint32_t*>(smem + C::ok_off);   // [kOkRing][5]: all ok, four words of key bits
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto empty = [&](int s) { return bar0 + 8u * (NST + s); };
-    auto sfull = [&](int q) { return bar0 + 8u * (2 * NST + q); };
-    auto pvdone = [&](int q) { return bar0 + 8u * (2 * NST + 2 + q); };
-    auto qfull = [&](int q) { return bar0 + 8u * (2 * NST + 4 + q); };
-    auto pfull = [&](int q, int half) { return bar0 + 8u * (2 * NST + 6 + 2 * q + half); };
-    auto fixed = [&](int j) { return bar0 + 8u * (2 * NST + 10 + (j & (kFix - 1))); };
+    auto bar = [&](int k) { return bar0 + 8u * (2 * NST + k); };
+    auto sfull = [&](int q) { return bar(q); };                 // scores are in TMEM
+    auto sfree = [&](int q) { return bar(2 + q); };             // scores are in registers (d = 64)
+    auto pvdone = [&](int q) { return bar(4 + q); };            // products with V are done
+    auto ofree = [&](int q) { return bar(6 + q); };             // O has been read
+    auto qfull = [&](int q) { return bar(8 + q); };
+    auto qempty = [&](int q) { return bar(10 + q); };
+    auto pfull = [&](int q, int half) { return bar(12 + 2 * q + half); };
+    auto fixed = [&](int j) { return bar(16 + (j & (kFix - 1))); };
+    const uint32_t ifull = bar(16 + kFix), iempty = bar(17 + kFix);
     unsigned long long* status = reinterpret_cast<unsigned long long*>(a.ws);
+    unsigned int* counter = reinterpret_cast<unsigned int*>(a.ws) + 2;   // items handed out; CTAs that are done
 
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    const int grp = a.grp, B = a.p.B;
-    const int gch = min(grp, kRows), chunks = (grp + gch - 1) / gch, tq = kRows / gch;   // tokens per tile
-    const int heads = a.p.Hkv * chunks, per_cta = 2 * tq;
-    const int hk = (int)(blockIdx.x % heads) / chunks, h0 = (int)(blockIdx.x % chunks) * gch, hn = min(gch, grp - h0);
+    const int grp = a.grp;
+    const int gch = min(grp, kRows), chunks = (grp + gch - 1) / gch, tq = kRows / gch;   // heads and tokens per tile
+    const int per_item = 2 * tq;
 
-    auto rows_of = [&](int b) {
-        const int s = a.starts[b];
-        return s < 0 ? 0 : max(0, min(a.starts[b + 1], a.p.T) - s);
-    };
-    {
-        const int each = (B + kPreThreads - 1) / kPreThreads, b0 = min(B, tid * each), b1 = min(B, b0 + each);
-        long long mine = 0, all;
-        for (int b = b0; b < b1; ++b) mine += (rows_of(b) + per_cta - 1) / per_cta;
-        long long at = block_scan<kPreThreads>(mine, &all);
-        const long long u = all - 1 - blockIdx.x / heads;   // a request's last tiles see the most keys: first
-        if (u < 0) return;
-        if (u >= at && u < at + mine) {
-            int b = b0;
-            for (long long n; u >= at + (n = (rows_of(b) + per_cta - 1) / per_cta); ++b) at += n;
-            s_b = b;
-            s_tile = (int)(u - at);
-        }
-    }
     if (tid == 0) {
         for (int i = 0; i < NST; ++i) {
             mbar_init(full(i), 1);
@@ -200,12 +253,17 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
         }
         for (int q = 0; q < 2; ++q) {
             mbar_init(sfull(q), 1);
+            mbar_init(sfree(q), 4);
+            mbar_init(pvdone(q), 1);
+            mbar_init(ofree(q), 4);
+            mbar_init(qfull(q), 1);
+            mbar_init(qempty(q), 1);
             mbar_init(pfull(q, 0), 4);
             mbar_init(pfull(q, 1), 4);
-            mbar_init(pvdone(q), 1);
-            mbar_init(qfull(q), 128);
         }
         for (int j = 0; j < kFix; ++j) mbar_init(fixed(j), 1);
+        mbar_init(ifull, 1);
+        mbar_init(iempty, kItemReaders);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 2) {
@@ -218,265 +276,369 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
     fence_after();
     const uint32_t tbase = __shfl_sync(0xffffffffu, s_taddr, 0);
 
-    const int b = __shfl_sync(0xffffffffu, s_b, 0), t0 = __shfl_sync(0xffffffffu, s_tile, 0) * per_cta, start = a.starts[b];
-    const int nt = min(per_cta, rows_of(b) - t0);      // tokens of this CTA
-    const int nq = nt > tq ? 2 : 1;                    // tiles that hold any
-    const int len = clamp_len(a.lengths[b], a);
-    // positions by the rows that the request has, those cut off at T included
-    const int first = len - (a.starts[b + 1] - start) + t0, last = first + nt - 1;
-    const int W = min(a.p.window, 1 << 30), S = min(a.p.sinks, len);
-
-    // key tiles: those of the first tokens, then those of the window (or all)
-    const int tiles_to = last >= 0 ? last / kKeys + 1 : 0;
-    const int from = W > 0 ? max(0, first - W + 1) / kKeys : 0;
-    const int sink_tiles = W > 0 ? min(from, (S + kKeys - 1) / kKeys) : 0;
-    const int tiles = __shfl_sync(0xffffffffu, tiles_to > from ? sink_tiles + tiles_to - from : 0, 0);
-    auto key0 = [&](int i) { return (i < sink_tiles ? i : i - sink_tiles + from) * kKeys; };
-    // whether some row of the CTA sees a key; whether a tile holds keys that none sees
-    auto seen = [&](int key) { return key <= last && (W == 0 || key > first - W || key < S); };
-    auto ragged = [&](int k0) { return !(k0 + kKeys - 1 <= last && (W == 0 || k0 > first - W || k0 + kKeys <= S)); };
+    bool ok = true;                                    // no wait of this warp has run out
+    auto wait = [&](uint32_t b, uint32_t parity) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(b, parity, status));
+        return ok;
+    };
+    // the n-th item of this CTA, read by a whole warp; false when there is none.  The TMA warp hands the slot back
+    // only after its last load for the item: the next one is then taken, late enough for an even share of a short
+    // list and early enough to be hidden behind the tiles in flight.
+    auto next_item = [&](int n, Item& it) {
+        if (!wait(ifull, (uint32_t)n & 1u)) return false;
+        it = s_item;
+        __syncwarp();
+        if (warp != 0 && lane == 0) mbar_arrive(iempty);
+        return it.live != 0;
+    };
 
     // Registers: 168 a thread at launch (384 threads, 64512 in all); the four
     // service warps keep 104, the eight softmax warps take 200.
     if (warp == 0) {
         regs_dec();
-        // ---------------- K and V pages ----------------
+        // ---------------- queries, K and V pages ----------------
         const int rows = min(1 << a.shift, kKeys), boxes = kKeys / rows * HALVES;   // at most 32
         const int row = lane / HALVES * rows, half = lane % HALVES;
-        int issued = 0;
-        bool ok = true;
-        auto page_of = [&](int i) {
-            int page = -1;
-            if (i < tiles && lane < boxes) {
-                const int key = key0(i) + row;
-                // the box is asked for if any of its keys is seen: the first, the last up to `last`, or one of the first tokens
-                if (key <= last && (seen(key) || seen(min(key + rows - 1, last))))
-                    page = __ldg(a.table + (size_t)b * a.p.max_pages + (key >> a.shift));
-                if (page >= a.p.num_pages) page = -1;
-            }
-            return page;
-        };
-        int page = page_of(0);
-        for (int i = 0; i < tiles && ok; ++i) {
-            const int k0 = key0(i), next = page_of(i + 1);
-            const uint32_t good = __ballot_sync(0xffffffffu, page >= 0 || lane >= boxes);
-            for (int kv = 0; kv < 2 && ok; ++kv) {
-                const int s = issued % NST;
-                ok = mbar_wait(empty(s), ((uint32_t)(issued / NST) & 1u) ^ 1u, status);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                if (lane == 0) {
-                    if (kv == 0) {
-                        uint32_t* o = ok_ring + (i & (kOkRing - 1)) * 5;
-                        o[0] = good == 0xffffffffu;
-                        if (good != 0xffffffffu) {
-                            for (int w = 0; w < 4; ++w) {
-                                uint32_t bits = 0;
-                                for (int r = 0; r < 32; r += 8)
-                                    if ((good >> ((w * 32 + r) / rows * HALVES)) & 1u) bits |= 0xffu << r;
-                                o[1 + w] = bits;
+        Ring<NST> ring;
+        int issued = 0, gtile = 0, uses[2] = {0, 0};
+        Item it;
+        for (int n = 0; next_item(n, it); ++n) {
+            const Tiles ts(it, a);
+            const int tiles = ts.count, nq = it.nt > tq ? 2 : 1;
+            auto page_of = [&](int i) {
+                int page = -1;
+                if (i < tiles && lane < boxes) {
+                    const int key = ts.key0(i) + row;
+                    // the box is asked for if any of its keys is seen: its first one (of the first tokens) or its last
+                    if (key <= ts.last && (ts.seen(key) || ts.seen(min(key + rows - 1, ts.last))))
+                        page = __ldg(a.table + (size_t)it.b * a.p.max_pages + (key >> a.shift));
+                    if (page >= a.p.num_pages) page = -1;
+                }
+                return page;
+            };
+            int page = page_of(0);
+            for (int i = 0; i < tiles && ok; ++i, ++gtile) {
+                const int k0 = ts.key0(i), next = page_of(i + 1);
+                const uint32_t good = __ballot_sync(0xffffffffu, page >= 0 || lane >= boxes);
+                for (int kv = 0; kv < 2; ++kv) {
+                    if (!wait(empty(ring.st), ring.ph ^ 1u)) break;
+                    if (lane == 0) {
+                        if (kv == 0) {
+                            uint32_t* o = ok_ring + (gtile & (kOkRing - 1)) * 5;
+                            o[0] = good == 0xffffffffu;
+                            if (good != 0xffffffffu) {
+                                for (int w = 0; w < 4; ++w) {
+                                    uint32_t bits = 0;
+                                    for (int r = 0; r < 32; r += 8)
+                                        if ((good >> ((w * 32 + r) / rows * HALVES)) & 1u) bits |= 0xffu << r;
+                                    o[1 + w] = bits;
+                                }
                             }
                         }
+                        mbar_expect_tx(full(ring.st), TILE);
                     }
-                    mbar_expect_tx(full(s), TILE);
+                    __syncwarp();
+                    if (lane < boxes)
+                        tma_load_4d(sR + ring.st * TILE + half * (kKeys * 128) + row * 128, kv ? &map_v : &map_k, half * 64,
+                                    k0 & ((1 << a.shift) - 1) & ~(rows - 1), it.hk, page >= 0 ? page : a.p.num_pages,
+                                    full(ring.st));
+                    ring.next();
+                    ++issued;
+                    if (i == 0 && kv == 0)
+                        for (int q = 0; q < nq; ++q) {
+                            if (!wait(qempty(q), (uint32_t)(uses[q] & 1) ^ 1u)) break;
+                            ++uses[q];
+                            if (lane == 0) {
+                                mbar_expect_tx(qfull(q), HALVES * gch * tq * 128);
+                                for (int h = 0; h < HALVES; ++h)
+                                    tma_load_3d(sQ + q * TILE + h * (kRows * 128), &map_q, h * 64, it.head0,
+                                                it.row0 + q * tq, qfull(q));
+                            }
+                            __syncwarp();
+                        }
+                    if (!ok) break;
                 }
-                __syncwarp();
-                if (lane < boxes)
-                    tma_load_4d(sR + s * TILE + half * (kKeys * 128) + row * 128, kv ? &map_v : &map_k, half * 64,
-                                k0 & ((1 << a.shift) - 1) & ~(rows - 1), hk, page >= 0 ? page : a.p.num_pages, full(s));
-                ++issued;
+                page = next;
             }
-            page = next;
+            if (lane == 0) mbar_arrive(iempty);
         }
         // drain: every issued load lands before the CTA exits
         for (int i = max(0, issued - NST); i < issued; ++i) mbar_wait(full(i % NST), (uint32_t)(i / NST) & 1u, status);
+        for (int q = 0; q < 2; ++q)
+            if (uses[q] > 0) mbar_wait(qfull(q), (uint32_t)(uses[q] - 1) & 1u, status);
     } else if (warp == 1) {
         regs_dec();
         // ---------------- products ----------------
         // The whole warp walks the tiles, so that descriptors and addresses stay in
         // uniform registers; one thread issues.  (With the walk in one thread alone
         // each product costs about 90 cycles to issue, against 64 to run.)
-        if (tiles > 0) {
-            constexpr uint32_t kQK = idesc_of<T>(kRows, kKeys, false), kPV = idesc_of<T>(kRows, D, true);
-            const bool leader = elect_one();
-            bool ok = true;
-            int pvs[2] = {0, 0}, qks[2] = {0, 0};
-            auto wait = [&](uint32_t bar, uint32_t parity) {
-                ok = ok && __all_sync(0xffffffffu, mbar_wait(bar, parity, status));
-            };
-            // stage and parity of the next ring entry: K and V in turn
-            int st = 0;
-            uint32_t ph = 0;
-            auto next_entry = [&] {
-                if (++st == NST) {
-                    st = 0;
-                    ph ^= 1u;
-                }
-            };
-            const uint64_t dq0 = sdesc(sQ), dr0 = sdesc(sR), dn0 = sdesc_n(sR);
-            // descriptors count in 16 bytes: 32 bytes a step of 16 elements, a half of 64 elements one panel on
-            auto qk = [&](int q, int stage) {
-                const uint64_t dq = dq0 + (uint64_t)(q * (TILE >> 4)), dk = dr0 + (uint64_t)(stage * (TILE >> 4));
-                if (leader) {
+        constexpr uint32_t kPV = idesc_of<T>(kRows, D, true);
+        const uint32_t kQK = idesc_of<T>(kRows, kKeys, false) | (a.p.scale < 0.f ? kNegateA : 0u);
+        const bool leader = elect_one();
+        Ring<NST> ring;
+        int gtile = 0;
+        int uses[2] = {0, 0}, qks[2] = {0, 0}, pvs[2] = {0, 0};   // items, score products, value products of a tile
+        const uint64_t dq0 = sdesc(sQ), dr0 = sdesc(sR), dn0 = sdesc_n(sR);
+        // descriptors count in 16 bytes: 32 bytes a step of 16 elements, a half of 64 elements one panel on
+        auto qk = [&](int q, int stage) {
+            const uint64_t dq = dq0 + (uint64_t)(q * (TILE >> 4)), dk = dr0 + (uint64_t)(stage * (TILE >> 4));
+            if (leader) {
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint64_t off = (uint64_t)(((k >> 2) * 128 * 128 + (k & 3) * 32) >> 4);
-                        mma_ss(tbase + C::S(q), dq + off, dk + off, kQK, k > 0 ? 1u : 0u);
-                    }
-                    mma_commit(sfull(q));
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint64_t off = (uint64_t)(((k >> 2) * 128 * 128 + (k & 3) * 32) >> 4);
+                    mma_ss(tbase + C::S(q), dq + off, dk + off, kQK, k > 0 ? 1u : 0u);
                 }
-                ++qks[q];
-            };
-            // one half of the keys
-            auto pv = [&](int q, int stage, int half, bool add) {
-                const uint64_t dv = dn0 + (uint64_t)(stage * (TILE >> 4) + half * (kKeys / 2 * 128 >> 4));
-                if (leader)
-#pragma unroll
-                    for (int j = 0; j < kKeys / 32; ++j)
-                        mma_ts(tbase + C::O(q), tbase + C::P(q) + (half * (kKeys / 32) + j) * 8, dv + (uint64_t)(j * 2048 >> 4),
-                               kPV, add || j > 0 ? 1u : 0u);
-            };
-            for (int q = 0; q < nq; ++q) wait(qfull(q), 0u);
-            wait(full(0), 0u);
-            if (ok) {
-                fence_after();
-                for (int q = 0; q < nq; ++q) qk(q, 0);
-                if (leader) mma_commit(empty(0));
-                next_entry();
+                mma_commit(sfull(q));
             }
-            for (int i = 0; i < tiles && ok; ++i) {
-                const int sv = st;
-                const uint32_t pv_ph = ph;
-                next_entry();                              // now the next tile's K
+            ++qks[q];
+        };
+        // one half of the keys
+        auto pv = [&](int q, int stage, int half, bool add) {
+            const uint64_t dv = dn0 + (uint64_t)(stage * (TILE >> 4) + half * (kKeys / 2 * 128 >> 4));
+            if (leader)
+#pragma unroll
+                for (int j = 0; j < kKeys / 32; ++j)
+                    mma_ts(tbase + C::O(q), tbase + C::P(q) + (half * (kKeys / 32) + j) * 8, dv + (uint64_t)(j * 2048 >> 4),
+                           kPV, add || j > 0 ? 1u : 0u);
+        };
+        // scores of the previous tile are in registers (with P over S: the wait for P says so)
+        auto wait_s = [&](int q) {
+            if (C::kOwnP && qks[q] > 0) wait(sfree(q), (uint32_t)(qks[q] - 1) & 1u);
+        };
+        Item it;
+        for (int n = 0; next_item(n, it); ++n) {
+            const int tiles = __shfl_sync(0xffffffffu, Tiles(it, a).count, 0);
+            const int nq = __shfl_sync(0xffffffffu, it.nt > tq ? 2 : 1, 0);
+            if (tiles == 0) continue;
+            wait(full(ring.st), ring.ph);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                if (q >= nq || !ok) continue;
+                wait(qfull(q), (uint32_t)uses[q] & 1u);
+                wait_s(q);
+                if (!ok) break;
+                fence_after();
+                qk(q, ring.st);
+                if (tiles == 1 && leader) mma_commit(qempty(q));
+            }
+            if (!ok) break;
+            if (leader) mma_commit(empty(ring.st));
+            ring.next();
+            for (int i = 0; i < tiles && ok; ++i, ++gtile) {
+                const Ring<NST> rv = ring;
+                ring.next();                               // now the next tile's K
+                const bool more = i + 1 < tiles;
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     if (q >= nq || !ok) continue;
-                    if (q == 0) {
-                        wait(full(sv), pv_ph);
-                        wait(fixed(i), (uint32_t)(i / kFix) & 1u);
+                    if (C::kOwnP && more) {
+                        if (q == 0) wait(full(ring.st), ring.ph);
+                        wait_s(q);
+                        if (!ok) break;
+                        fence_after();
+                        qk(q, ring.st);
+                        if (i + 2 == tiles && leader) mma_commit(qempty(q));
+                        if (q == nq - 1 && leader) mma_commit(empty(ring.st));
                     }
-                    wait(pfull(q, 0), (uint32_t)i & 1u);
+                    if (q == 0) {
+                        wait(full(rv.st), rv.ph);
+                        wait(fixed(gtile), (uint32_t)(gtile / kFix) & 1u);
+                    }
+                    if (i == 0 && uses[q] > 0) wait(ofree(q), (uint32_t)(uses[q] - 1) & 1u);
+                    wait(pfull(q, 0), (uint32_t)pvs[q] & 1u);
                     if (!ok) break;
                     fence_after();
-                    pv(q, sv, 0, i > 0);
-                    wait(pfull(q, 1), (uint32_t)i & 1u);
-                    if (q == 0 && i + 1 < tiles) wait(full(st), ph);
+                    pv(q, rv.st, 0, i > 0);
+                    wait(pfull(q, 1), (uint32_t)pvs[q] & 1u);
+                    if (!C::kOwnP && q == 0 && more) wait(full(ring.st), ring.ph);
                     if (!ok) break;
                     fence_after();
-                    pv(q, sv, 1, true);
+                    pv(q, rv.st, 1, true);
                     if (leader) mma_commit(pvdone(q));
                     ++pvs[q];
-                    if (q == nq - 1 && leader) mma_commit(empty(sv));
-                    if (i + 1 < tiles) {
-                        qk(q, st);
-                        if (q == nq - 1 && leader) mma_commit(empty(st));
+                    if (q == nq - 1 && leader) mma_commit(empty(rv.st));
+                    if (!C::kOwnP && more) {
+                        qk(q, ring.st);
+                        if (i + 2 == tiles && leader) mma_commit(qempty(q));
+                        if (q == nq - 1 && leader) mma_commit(empty(ring.st));
                     }
                 }
-                next_entry();
+                if (more) ring.next();
             }
-            // drain: the last products of each tile are complete before TMEM is freed
-            for (int q = 0; q < 2; ++q) {
-                if (qks[q] > 0) mbar_wait(sfull(q), (uint32_t)(qks[q] - 1) & 1u, status);
-                if (pvs[q] > 0) mbar_wait(pvdone(q), (uint32_t)(pvs[q] - 1) & 1u, status);
-            }
-            __syncwarp();
+            for (int q = 0; q < nq; ++q) ++uses[q];
         }
+        // drain: the last products of each tile are complete before TMEM is freed
+        for (int q = 0; q < 2; ++q) {
+            if (qks[q] > 0) mbar_wait(sfull(q), (uint32_t)(qks[q] - 1) & 1u, status);
+            if (pvs[q] > 0) mbar_wait(pvdone(q), (uint32_t)(pvs[q] - 1) & 1u, status);
+        }
+        __syncwarp();
     } else if (warp == 2) {
         regs_dec();
         // ---------------- value rows that no row sees: zeros ----------------
         // Every value tile passes here on its way to the product, so that this
         // warp stays within one round of the ring.
-        bool ok = true;
-        for (int i = 0; i < tiles && ok; ++i) {
-            const int k0 = key0(i), r = 2 * i + 1, s = r % NST;
-            ok = mbar_wait(full(s), (uint32_t)(r / NST) & 1u, status);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            if (ragged(k0)) {
-                for (int row = 0; row < kKeys; ++row) {
-                    if (seen(k0 + row)) continue;
-                    // the whole row, so wherever the swizzle puts its 16-byte pieces
-                    if (lane < D / 8)
-                        *reinterpret_cast<uint4*>(smem + (2 + s) * TILE + (lane / 8) * (kKeys * 128) + row * 128 +
-                                                  (lane % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        Ring<NST> ring;
+        int gtile = 0;
+        Item it;
+        for (int n = 0; next_item(n, it); ++n) {
+            const Tiles ts(it, a);
+            for (int i = 0; i < ts.count && ok; ++i, ++gtile) {
+                const int k0 = ts.key0(i);
+                ring.next();
+                if (!wait(full(ring.st), ring.ph)) break;
+                if (ts.ragged(k0)) {
+                    for (int row = 0; row < kKeys; ++row) {
+                        if (ts.seen(k0 + row)) continue;
+                        // the whole row, so wherever the swizzle puts its 16-byte pieces
+                        if (lane < D / 8)
+                            *reinterpret_cast<uint4*>(smem + (2 + ring.st) * TILE + (lane / 8) * (kKeys * 128) + row * 128 +
+                                                      (lane % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
+                if (lane == 0) mbar_arrive(fixed(gtile));
+                ring.next();
             }
-            if (lane == 0) mbar_arrive(fixed(i));
         }
     } else if (warp == 3) {
         regs_dec();
+        // ---------------- items ----------------
+        // Item x is heads x % heads of tile x / heads, tiles counted from the last
+        // request's last one.  Requests are looked at 32 at a time, a lane each.
+        const int heads = a.p.Hkv * chunks;
+        int hi = a.p.B - 1;                                // lane l looks at request hi - l
+        long long base = 0;                                // tiles of the requests above hi
+        int start = 0, cnt = 0, all = 0, upto = 0;         // this lane's request: first row, rows, rows before T is cut off, tiles up to it
+        auto look = [&] {
+            const int b = hi - lane;
+            cnt = start = all = 0;
+            if (b >= 0) {
+                start = __ldg(a.starts + b);
+                const int stop = __ldg(a.starts + b + 1);
+                if (start >= 0 && stop > start) {
+                    all = stop - start;
+                    cnt = max(0, min(stop, a.p.T) - start);
+                }
+            }
+            upto = (cnt + per_item - 1) / per_item;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += y;
+            }
+        };
+        look();
+        for (int n = 0; ok; ++n) {
+            unsigned int x = 0;
+            if (lane == 0) x = atomicAdd(counter, 1u);
+            x = __shfl_sync(0xffffffffu, x, 0);
+            const long long u = x / (unsigned int)heads;
+            const int head = (int)(x % (unsigned int)heads);
+            while (hi >= 0 && u >= base + __shfl_sync(0xffffffffu, upto, 31)) {
+                base += __shfl_sync(0xffffffffu, upto, 31);
+                hi -= 32;
+                look();
+            }
+            Item it;
+            it.live = hi >= 0;
+            const int at = hi >= 0 ? __ffs(__ballot_sync(0xffffffffu, base + upto > u)) - 1 : 0;   // the lane whose request it is
+            const int t_end = (int)(base + __shfl_sync(0xffffffffu, upto, at) - u);                // tiles from this one to the request's first, this one included
+            const int rows = __shfl_sync(0xffffffffu, cnt, at), rows_all = __shfl_sync(0xffffffffu, all, at);
+            const int s0 = __shfl_sync(0xffffffffu, start, at);
+            if (it.live) {
+                const int t0 = (t_end - 1) * per_item;
+                it.b = hi - at;
+                it.row0 = s0 + t0;
+                it.nt = min(per_item, rows - t0);
+                it.len = clamp_len(__ldg(a.lengths + it.b), a);
+                // positions by the rows that the request has, those cut off at T included
+                it.first = it.len - rows_all + t0;
+                it.hk = head / chunks;
+                const int h0 = (head % chunks) * gch;
+                it.head0 = it.hk * grp + h0;
+                it.hn = min(gch, grp - h0);
+            }
+            if (lane == 0) {
+                s_item = it;
+                mbar_arrive(ifull);
+            }
+            __syncwarp();
+            if (!it.live || !wait(iempty, (uint32_t)n & 1u)) break;
+        }
+        // the last CTA to stop leaves the counters at zero for the next call
+        if (lane == 0) {
+            __threadfence();
+            if (atomicAdd(counter + 1, 1u) == gridDim.x - 1) {
+                counter[0] = 0u;
+                counter[1] = 0u;
+            }
+        }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         // ---------------- softmax ----------------
         const int q = (warp - 4) >> 2, r = tid & 127;
-        if (q < nq) {
-            // queries into shared memory (swizzled 128-byte rows), a negative scale's sign and a zero scale with them
-            {
-                const uint32_t flip = a.p.scale < 0.f ? 0x80008000u : 0u;
-                const bool zero = a.p.scale == 0.f;
-                const T* qp = (const T*)a.q + (size_t)(hk * grp + h0) * D;
-#pragma unroll 8
-                for (int j = r; j < kRows * (D / 8); j += 128) {
-                    const int row = j / (D / 8), c = j % (D / 8), t = q * tq + row / gch, h = row % gch;
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (row / gch < tq && t < nt && h < hn && !zero) {
-                        v = __ldg(reinterpret_cast<const uint4*>(qp + (size_t)(start + t0 + t) * a.p.q_stride + h * D) + c);
-                        v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
-                    }
-                    *reinterpret_cast<uint4*>(smem + q * TILE + (c / 8) * (kRows * 128) + swz<128>(row, c & 7)) = v;
-                }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                mbar_arrive(qfull(q));
-            }
-            const int t = q * tq + r / gch, h = r % gch;
-            const bool live = r / gch < tq && t < nt && h < hn;
-            const int pos = live ? first + t : -1;
-            const int pmin = first + q * tq, pmax = min(last, pmin + tq - 1);
-            const float scale = a.p.scale == 0.f ? 1.f : fabsf(a.scale_log2);
-            const uint32_t lanes = tbase + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t inv_gch = 65536u / (uint32_t)gch + 1u;          // r / gch = r * inv_gch >> 16 for r < 128
+        const int tr = (int)((r * inv_gch) >> 16), h = r - tr * gch;   // token and head of this thread's row
+        const uint32_t lanes = tbase + ((uint32_t)((warp & 3) * 32) << 16);
+        // positive, so that the largest score gives the largest exponent (a negative scale's sign is in the product);
+        // in place of 0 a scale that leaves every exponent 0, as 0 x -inf would not
+        const float scale = fmaxf(fabsf(a.scale_log2), 1e-37f);
+        int gtile = 0, its = 0;                                        // tiles of all items; those of this half's
+        Item it;
+        for (int n = 0; next_item(n, it); ++n) {
+            const Tiles ts(it, a);
+            const int tiles = ts.count, gt0 = gtile;
+            gtile += tiles;
+            if (q == 1 && it.nt <= tq) continue;
+            const int t = q * tq + tr;
+            const bool live = tr < tq && t < it.nt && h < it.hn;
+            const int pos = live ? it.first + t : -1;
+            const int pmin = it.first + q * tq, pmax = min(ts.last, pmin + tq - 1);
             float m = -INFINITY, l = 0.f;
-            bool ok = true;
-            for (int i = 0; i < tiles && ok; ++i) {
-                ok = mbar_wait(sfull(q), (uint32_t)i & 1u, status);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
+            for (int i = 0; i < tiles && ok; ++i, ++its) {
+                const int k0 = ts.key0(i);
+                const uint32_t* okr = ok_ring + ((gt0 + i) & (kOkRing - 1)) * 5;
+                if (!wait(sfull(q), (uint32_t)its & 1u)) break;
                 fence_after();
+                const bool all_ok = okr[0] != 0;
                 uint32_t s[4][32];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32_async(lanes + C::S(q) + c * 32, s[c]);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_wait32(s[c]);
-                const int k0 = key0(i);
-                const uint32_t* okr = ok_ring + (i & (kOkRing - 1)) * 5;
+                if (C::kOwnP) {
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sfree(q));
+                }
                 // masks only where the tile has keys that some row of the 128 does not see
-                if (!(k0 + kKeys - 1 <= pmin && (W == 0 || k0 > pmax - W || k0 + kKeys <= S) && okr[0])) {
-                    const bool all_ok = okr[0] != 0;
+                if (!(k0 + kKeys - 1 <= pmin && (ts.W == 0 || k0 > pmax - ts.W || k0 + kKeys <= ts.S) && all_ok)) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         const int k = k0 + c * 32;
                         uint32_t bits = low_bits(pos - k + 1);
-                        if (W > 0) bits &= ~low_bits(pos - W - k + 1) | low_bits(S - k);
+                        if (ts.W > 0) bits &= ~low_bits(pos - ts.W - k + 1) | low_bits(ts.S - k);
                         if (!all_ok) bits &= okr[1 + c];
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if (!((bits >> j) & 1u)) s[c][j] = 0xff800000u;
                     }
                 }
-                float mx = -INFINITY;
+                float mx;
                 {
-                    float x[4];
+                    float x[8];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        x[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
+                    for (int c = 0; c < 8; ++c)
+                        x[c] = fmaxf(__uint_as_float(s[c >> 1][(c & 1) * 16]), __uint_as_float(s[c >> 1][(c & 1) * 16 + 1]));
 #pragma unroll
-                        for (int j = 2; j < 32; j += 2)
-                            x[c] = max3(x[c], __uint_as_float(s[c][j]), __uint_as_float(s[c][j + 1]));
-                    }
-                    mx = fmaxf(max3(x[0], x[1], x[2]), x[3]) * scale;
+                    for (int j = 2; j < 16; j += 2)
+#pragma unroll
+                        for (int c = 0; c < 8; ++c)
+                            x[c] = max3(x[c], __uint_as_float(s[c >> 1][(c & 1) * 16 + j]),
+                                        __uint_as_float(s[c >> 1][(c & 1) * 16 + j + 1]));
+                    mx = max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), fmaxf(x[6], x[7])) * scale;
                 }
                 const bool grow = mx > m + kGrow;
                 if (__any_sync(0xffffffffu, grow)) {
@@ -487,11 +649,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                         l *= f;
                     }
                     if (i > 0) {
-                        ok = mbar_wait(pvdone(q), (uint32_t)(i - 1) & 1u, status);
-                        if (!__all_sync(0xffffffffu, ok)) {
-                            ok = false;
-                            break;
-                        }
+                        if (!wait(pvdone(q), (uint32_t)(its - 1) & 1u)) break;
                         fence_after();
 #pragma unroll 1
                         for (int c = 0; c < D / 32; ++c) {
@@ -518,6 +676,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                         sum[j & 1] = add2(sum[j & 1], pair(p0, p1));
                         p[j] = Num<T>::pack(p0, p1);
                     }
+                    // P in its own columns: the product that read the last one must be done (it is, mostly)
+                    if (C::kOwnP && c == 0 && i > 0 && !wait(pvdone(q), (uint32_t)(its - 1) & 1u)) break;
                     tmem_st16(lanes + C::P(q) + c * 16, p);
                     if (c & 1) {                               // half of the keys: the product may begin
                         tmem_st_wait();
@@ -526,39 +686,62 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_con
                         if (lane == 0) mbar_arrive(pfull(q, c >> 1));
                     }
                 }
+                if (!ok) break;
                 float x0, x1;
                 unpair(add2(sum[0], sum[1]), x0, x1);
                 l += x0 + x1;
             }
             if (tiles > 0 && ok) {
-                ok = mbar_wait(pvdone(q), (uint32_t)(tiles - 1) & 1u, status);
-                ok = __all_sync(0xffffffffu, ok);
+                wait(pvdone(q), (uint32_t)(its - 1) & 1u);
                 fence_after();
             }
-            if (ok) {
-                const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
-                const size_t row = (size_t)start + t0 + t, head = (size_t)hk * grp + h0 + h;
-                uint4* out = reinterpret_cast<uint4*>((T*)a.out + row * a.p.out_stride + head * D);
+            if (!ok) break;
+            const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+            if (live && a.lse)
+                a.lse[(size_t)(it.row0 + t) * a.p.Hq + it.head0 + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            // rows out: four lanes exchange their 16-byte pieces, so that each stores 64 bytes of a row together
+            T* orow[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int rr = (r & ~3) + k, tk = (int)((rr * inv_gch) >> 16), hh = rr - tk * gch, tt = q * tq + tk;
+                orow[k] = tk < tq && tt < it.nt && hh < it.hn
+                              ? (T*)a.out + (size_t)(it.row0 + tt) * a.p.out_stride + (size_t)(it.head0 + hh) * D + (lane & 3) * 8
+                              : nullptr;
+            }
 #pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t o[32];
-                    if (tiles > 0) {
-                        tmem_ld32(lanes + C::O(q) + c * 32, o);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) o[j] = 0u;
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                if (tiles > 0) {
+                    tmem_ld32(lanes + C::O(q) + c * 32, o);
+                    if (c == D / 32 - 1) {
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(ofree(q));
                     }
-                    if (live)
+                } else {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            auto two = [&](int k) {
-                                return Num<T>::pack(__uint_as_float(o[8 * j + 2 * k]) * inv,
-                                                    __uint_as_float(o[8 * j + 2 * k + 1]) * inv);
-                            };
-                            out[c * 4 + j] = make_uint4(two(0), two(1), two(2), two(3));
-                        }
+                    for (int j = 0; j < 32; ++j) o[j] = 0u;
                 }
-                if (live && a.lse) a.lse[row * a.p.Hq + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+                uint32_t v[4][4];                              // [piece of the row][word]
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    v[j >> 2][j & 3] = Num<T>::pack(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+                // 4 x 4 transpose over the lanes of a quad: piece k of row j <-> piece j of row k
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const bool odd = lane & 1, high = lane & 2;
+                    uint32_t x = __shfl_xor_sync(0xffffffffu, odd ? v[0][w] : v[1][w], 1);
+                    uint32_t y = __shfl_xor_sync(0xffffffffu, odd ? v[2][w] : v[3][w], 1);
+                    if (odd) v[0][w] = x, v[2][w] = y;
+                    else v[1][w] = x, v[3][w] = y;
+                    x = __shfl_xor_sync(0xffffffffu, high ? v[0][w] : v[2][w], 2);
+                    y = __shfl_xor_sync(0xffffffffu, high ? v[1][w] : v[3][w], 2);
+                    if (high) v[0][w] = x, v[1][w] = y;
+                    else v[2][w] = x, v[3][w] = y;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (orow[k]) *reinterpret_cast<uint4*>(orow[k] + c * 32) = make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
             }
         }
     }
@@ -588,17 +771,35 @@ bool pool_map(CUtensorMap* map, const void* base, const PagedArgs& a)
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Queries as (element, head, row), boxes of 64 elements by the heads and
+// tokens of a tile: row by row as the tile has them.
+bool query_map(CUtensorMap* map, const PagedArgs& a, int heads, int tokens)
+{
+    auto fn = tma_encode_fn();
+    if (!fn) return false;
+    const fadkv_paged_params& p = a.p;
+    cuuint64_t dims[3] = {(cuuint64_t)p.d, (cuuint64_t)p.Hq, (cuuint64_t)p.T};
+    cuuint64_t strides[2] = {(cuuint64_t)p.d * 2, (cuuint64_t)p.q_stride * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)tokens};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, p.dtype == FADKV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+              const_cast<void*>(a.q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename T, int D>
 cudaError_t launch_t(const PagedArgs& a, cudaStream_t st)
 {
     auto k = paged_prefill_kernel<T, D>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, PreCfg<D>::alloc);
     if (e != cudaSuccess) return e;
-    CUtensorMap mk, mv;
-    if (!pool_map(&mk, a.k, a) || !pool_map(&mv, a.v, a)) return cudaErrorInvalidValue;
     const int gch = a.grp < kRows ? a.grp : kRows, chunks = (a.grp + gch - 1) / gch, tq = kRows / gch;
-    const long long tiles = a.p.T / (2 * tq) + a.p.B;
-    k<<<(unsigned)(tiles * a.p.Hkv * chunks), kPreThreads, PreCfg<D>::alloc, st>>>(mk, mv, a);
+    CUtensorMap mq, mk, mv;
+    if (!query_map(&mq, a, gch, tq) || !pool_map(&mk, a.k, a) || !pool_map(&mv, a.v, a)) return cudaErrorInvalidValue;
+    // at most one item a request more than the rows fill
+    const long long items = ((long long)a.p.T / (2 * tq) + a.p.B) * a.p.Hkv * chunks;
+    if (items > 0x7fffffffll) return cudaErrorInvalidValue;
+    k<<<(unsigned)(items < kPreCtas ? items : kPreCtas), kPreThreads, PreCfg<D>::alloc, st>>>(mq, mk, mv, a);
     return cudaGetLastError();
 }
 
