@@ -36,8 +36,8 @@
 // while the last tiles of the current one are worked on; only the reading of
 // O by the softmax warps stands between two items' products.
 //
-// Warps: 0 TMA, 1 MMA, 2 TMEM and the zeroing, 3 the items, 4..7 and 8..11
-// softmax of the two tiles.  Every wait is bounded; one that runs out sets
+// Warps: 0 TMA, 1 MMA, 2 TMEM and the items, 4..7 and 8..11 softmax of the two
+// tiles (3 only makes the count whole).  Every wait is bounded; one that runs out sets
 // FADKV_DEV_TIMEOUT in the workspace's first word, and the CTA drains and
 // returns.
 #include "paged.cuh"
@@ -52,18 +52,17 @@ using namespace tc;
 constexpr int kPreThreads = 384;
 constexpr int kRows = 128;                         // (token, head) rows per tile, two tiles per CTA
 constexpr int kKeys = 128;                         // keys per tile
-constexpr int kFix = 4;                            // barriers of the zeroing, in turn: as many as value stages at least
 constexpr int kOkRing = 16;                        // key tiles whose page masks are kept
 constexpr float kGrow = 8.f;                       // growth of the maximum (log2) that rescales
 
 constexpr int kPreCtas = 152;                      // one per multiprocessor
-constexpr int kItemReaders = 11;                   // warps that read an item
+constexpr int kItemReaders = 10;                   // warps that read an item
 
 template <int D> struct PreCfg {
     static constexpr int NST = D == 128 ? 5 : 8;   // stages of the K / V ring
     static constexpr int TILE = kRows * D * 2;     // bytes of a Q, K or V tile
     static constexpr int bar_off = (2 + NST) * TILE;
-    static constexpr int n_bars = 2 * NST + 16 + kFix + 2;
+    static constexpr int n_bars = 2 * NST + 18;
     static constexpr int ok_off = bar_off + n_bars * 8;
     static constexpr int alloc = ok_off + kOkRing * 20 + 16 + 1024;
     static_assert(alloc <= 227 * 1024 - 256, "shared memory");
@@ -236,8 +235,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     auto qfull = [&](int q) { return bar(8 + q); };
     auto qempty = [&](int q) { return bar(10 + q); };
     auto pfull = [&](int q, int half) { return bar(12 + 2 * q + half); };
-    auto fixed = [&](int j) { return bar(16 + (j & (kFix - 1))); };
-    const uint32_t ifull = bar(16 + kFix), iempty = bar(17 + kFix);
+    const uint32_t ifull = bar(16), iempty = bar(17);
     unsigned long long* status = reinterpret_cast<unsigned long long*>(a.ws);
     unsigned int* counter = reinterpret_cast<unsigned int*>(a.ws) + 2;   // items handed out; CTAs that are done
 
@@ -261,7 +259,6 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             mbar_init(pfull(q, 0), 4);
             mbar_init(pfull(q, 1), 4);
         }
-        for (int j = 0; j < kFix; ++j) mbar_init(fixed(j), 1);
         mbar_init(ifull, 1);
         mbar_init(iempty, kItemReaders);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -297,8 +294,9 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     if (warp == 0) {
         regs_dec();
         // ---------------- queries, K and V pages ----------------
-        const int rows = min(1 << a.shift, kKeys), boxes = kKeys / rows * HALVES;   // at most 32
-        const int row = lane / HALVES * rows, half = lane % HALVES;
+        const int rows = min(1 << a.shift, kKeys), pages = kKeys / rows;   // at most 16
+        const int row = lane * rows;                           // lane l holds page l of a tile
+        const bool leader = elect_one();
         Ring<NST> ring;
         int issued = 0, gtile = 0, uses[2] = {0, 0};
         Item it;
@@ -306,20 +304,20 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             const Tiles ts(it, a);
             const int tiles = ts.count, nq = it.nt > tq ? 2 : 1;
             auto page_of = [&](int i) {
-                int page = -1;
-                if (i < tiles && lane < boxes) {
+                int page = a.p.num_pages;                      // outside the map: zeros
+                if (i < tiles && lane < pages) {
                     const int key = ts.key0(i) + row;
-                    // the box is asked for if any of its keys is seen: its first one (of the first tokens) or its last
+                    // a page is asked for if any of its keys is seen: its first one (of the first tokens) or its last
                     if (key <= ts.last && (ts.seen(key) || ts.seen(min(key + rows - 1, ts.last))))
                         page = __ldg(a.table + (size_t)it.b * a.p.max_pages + (key >> a.shift));
-                    if (page >= a.p.num_pages) page = -1;
+                    if (page < 0 || page > a.p.num_pages) page = a.p.num_pages;
                 }
                 return page;
             };
             int page = page_of(0);
             for (int i = 0; i < tiles && ok; ++i, ++gtile) {
                 const int k0 = ts.key0(i), next = page_of(i + 1);
-                const uint32_t good = __ballot_sync(0xffffffffu, page >= 0 || lane >= boxes);
+                const uint32_t good = __ballot_sync(0xffffffffu, page < a.p.num_pages || lane >= pages);
                 for (int kv = 0; kv < 2; ++kv) {
                     if (!wait(empty(ring.st), ring.ph ^ 1u)) break;
                     if (lane == 0) {
@@ -330,7 +328,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                                 for (int w = 0; w < 4; ++w) {
                                     uint32_t bits = 0;
                                     for (int r = 0; r < 32; r += 8)
-                                        if ((good >> ((w * 32 + r) / rows * HALVES)) & 1u) bits |= 0xffu << r;
+                                        if ((good >> ((w * 32 + r) / rows)) & 1u) bits |= 0xffu << r;
                                     o[1 + w] = bits;
                                 }
                             }
@@ -338,10 +336,17 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                         mbar_expect_tx(full(ring.st), TILE);
                     }
                     __syncwarp();
-                    if (lane < boxes)
-                        tma_load_4d(sR + ring.st * TILE + half * (kKeys * 128) + row * 128, kv ? &map_v : &map_k, half * 64,
-                                    k0 & ((1 << a.shift) - 1) & ~(rows - 1), it.hk, page >= 0 ? page : a.p.num_pages,
-                                    full(ring.st));
+                    const CUtensorMap* map = kv ? &map_v : &map_k;
+                    const int y = k0 & ((1 << a.shift) - 1) & ~(rows - 1);
+#pragma unroll 4
+                    for (int j = 0; j < pages; ++j) {
+                        const int w = __shfl_sync(0xffffffffu, page, j);
+                        const uint32_t dst = sR + ring.st * TILE + j * rows * 128;
+                        if (leader)
+#pragma unroll
+                            for (int h = 0; h < HALVES; ++h)
+                                tma_load_4d(dst + h * (kKeys * 128), map, h * 64, y, it.hk, w, full(ring.st));
+                    }
                     ring.next();
                     ++issued;
                     if (i == 0 && kv == 0)
@@ -376,7 +381,6 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         const uint32_t kQK = idesc_of<T>(kRows, kKeys, false) | (a.p.scale < 0.f ? kNegateA : 0u);
         const bool leader = elect_one();
         Ring<NST> ring;
-        int gtile = 0;
         int uses[2] = {0, 0}, qks[2] = {0, 0}, pvs[2] = {0, 0};   // items, score products, value products of a tile
         const uint64_t dq0 = sdesc(sQ), dr0 = sdesc(sR), dn0 = sdesc_n(sR);
         // descriptors count in 16 bytes: 32 bytes a step of 16 elements, a half of 64 elements one panel on
@@ -401,13 +405,28 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                     mma_ts(tbase + C::O(q), tbase + C::P(q) + (half * (kKeys / 32) + j) * 8, dv + (uint64_t)(j * 2048 >> 4),
                            kPV, add || j > 0 ? 1u : 0u);
         };
+        // value rows that no row of the item sees: zeros (while the softmax works on the scores)
+        auto clear = [&](const Tiles& ts, int k0, int stage) {
+            unsigned char* v = smem + (2 + stage) * TILE;
+            auto rows = [&](int r0, int r1) {                  // whole rows, so wherever the swizzle puts their pieces
+                for (int x = r0 * (D / 8) + lane; x < r1 * (D / 8); x += 32) {
+                    const int row = x / (D / 8), c = x % (D / 8);
+                    *reinterpret_cast<uint4*>(v + (c / 8) * (kKeys * 128) + row * 128 + (c % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                }
+            };
+            rows(max(0, ts.last + 1 - k0), kKeys);
+            if (ts.W > 0) rows(max(0, ts.S - k0), min(kKeys, ts.first - ts.W + 1 - k0));
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+        };
         // scores of the previous tile are in registers (with P over S: the wait for P says so)
         auto wait_s = [&](int q) {
             if (C::kOwnP && qks[q] > 0) wait(sfree(q), (uint32_t)(qks[q] - 1) & 1u);
         };
         Item it;
         for (int n = 0; next_item(n, it); ++n) {
-            const int tiles = __shfl_sync(0xffffffffu, Tiles(it, a).count, 0);
+            const Tiles ts(it, a);
+            const int tiles = __shfl_sync(0xffffffffu, ts.count, 0);
             const int nq = __shfl_sync(0xffffffffu, it.nt > tq ? 2 : 1, 0);
             if (tiles == 0) continue;
             wait(full(ring.st), ring.ph);
@@ -424,7 +443,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             if (!ok) break;
             if (leader) mma_commit(empty(ring.st));
             ring.next();
-            for (int i = 0; i < tiles && ok; ++i, ++gtile) {
+            for (int i = 0; i < tiles && ok; ++i) {
                 const Ring<NST> rv = ring;
                 ring.next();                               // now the next tile's K
                 const bool more = i + 1 < tiles;
@@ -441,8 +460,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                         if (q == nq - 1 && leader) mma_commit(empty(ring.st));
                     }
                     if (q == 0) {
-                        wait(full(rv.st), rv.ph);
-                        wait(fixed(gtile), (uint32_t)(gtile / kFix) & 1u);
+                        if (wait(full(rv.st), rv.ph) && ts.ragged(ts.key0(i))) clear(ts, ts.key0(i), rv.st);
                     }
                     if (i == 0 && uses[q] > 0) wait(ofree(q), (uint32_t)(uses[q] - 1) & 1u);
                     wait(pfull(q, 0), (uint32_t)pvs[q] & 1u);
@@ -474,35 +492,6 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         }
         __syncwarp();
     } else if (warp == 2) {
-        regs_dec();
-        // ---------------- value rows that no row sees: zeros ----------------
-        // Every value tile passes here on its way to the product, so that this
-        // warp stays within one round of the ring.
-        Ring<NST> ring;
-        int gtile = 0;
-        Item it;
-        for (int n = 0; next_item(n, it); ++n) {
-            const Tiles ts(it, a);
-            for (int i = 0; i < ts.count && ok; ++i, ++gtile) {
-                const int k0 = ts.key0(i);
-                ring.next();
-                if (!wait(full(ring.st), ring.ph)) break;
-                if (ts.ragged(k0)) {
-                    for (int row = 0; row < kKeys; ++row) {
-                        if (ts.seen(k0 + row)) continue;
-                        // the whole row, so wherever the swizzle puts its 16-byte pieces
-                        if (lane < D / 8)
-                            *reinterpret_cast<uint4*>(smem + (2 + ring.st) * TILE + (lane / 8) * (kKeys * 128) + row * 128 +
-                                                      (lane % 8) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                }
-                if (lane == 0) mbar_arrive(fixed(gtile));
-                ring.next();
-            }
-        }
-    } else if (warp == 3) {
         regs_dec();
         // ---------------- items ----------------
         // Item x is heads x % heads of tile x / heads, tiles counted from the last
@@ -575,6 +564,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 counter[1] = 0u;
             }
         }
+    } else if (warp == 3) {
+        regs_dec();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         // ---------------- softmax ----------------
