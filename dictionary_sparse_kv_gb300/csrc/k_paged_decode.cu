@@ -16,9 +16,11 @@
 //
 // Inside a CTA each of four warps takes every fourth 16-token tile through a
 // pipeline of its own (cp.async, one block-table lookup per token), with its
-// own m, l and o; nothing synchronises the warps until the piece ends.  The
-// products run on the warp's matrix instructions with the tokens as rows and
-// the query heads that share the KV head as the eight columns:
+// own m, l and o; nothing synchronises the warps until the piece ends, and the
+// first tiles of the next piece are asked for before the last one's results
+// are joined.  The products run on the warp's matrix instructions with the
+// tokens as rows and the query heads that share the KV head as the eight
+// columns:
 //   S^T = K Q^T   [16 tokens][8 heads],   O^T += V^T P^T   [d][8 heads],
 // so a group of up to eight heads fills one instruction and nothing is padded
 // to 16 rows of queries.  P enters as two 16-bit terms (hi + lo): the tensor
@@ -43,11 +45,21 @@ template <int D> struct DecCfg {
     static constexpr int STAGES = D == 128 ? 3 : 6;
     static constexpr int TILE_BYTES = kTile * D * 2;
     static constexpr int WARP_BYTES = STAGES * 2 * TILE_BYTES;
-    static constexpr int SMEM = kDecWarps * WARP_BYTES;
+    // warps' results of eight heads: three quarters each, as the owner of a quarter keeps its own
+    static constexpr int JOIN_BYTES = kDecWarps * 3 * (D / 16 / kDecWarps) * 32 * 16;
+    static constexpr int SMEM = kDecWarps * WARP_BYTES + JOIN_BYTES;
 };
 
-struct Piece {                                     // layout of the workspace behind the counters
-    static __host__ __device__ constexpr size_t floats(int d) { return (size_t)kMaxHeads * (d + 2); }
+// A piece in the workspace: kMaxHeads rows of d sums, then their m and l.
+__host__ __device__ constexpr size_t piece_floats(int d) { return (size_t)kMaxHeads * (d + 2); }
+
+// One piece of work: blocks blk0 .. blk1-1 of nb of request b and a set of
+// heads that share a KV head.
+struct Work {
+    int b, hk, head0, hn, nb, blk0, blk1;
+    int end, tile0, tiles;     // list indices end at `end`; this warp's tiles
+    Seen seen;
+    long long first;           // unit number of block 0
 };
 
 template <typename T, int D, int NT>
@@ -56,7 +68,7 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
 {
     using Cfg = DecCfg<D>;
     constexpr int STAGES = Cfg::STAGES, ROW = D * 2, CPR = D / 8;      // bytes and 16-byte chunks per row
-    constexpr int KS = D / 16;
+    constexpr int KS = D / 16, KQ = KS / kDecWarps;                    // 16-element steps; those a warp writes out
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ int s_b, s_last;
     __shared__ long long s_base;
@@ -64,15 +76,16 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
     __shared__ uint32_t s_ok[kDecWarps][STAGES];
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int Hkv = a.p.Hkv, grp = a.grp, B = a.p.B;
+    const int grp = a.grp, B = a.p.B;
     const int chunks = (grp + 8 * NT - 1) / (8 * NT);                 // pieces per KV head
-    const int segs = Hkv * chunks;
-    unsigned char* wsm = smem + warp * Cfg::WARP_BYTES;
-    const uint32_t wbase = saddr(wsm);
+    const int segs = a.p.Hkv * chunks;
+    const uint32_t wbase = saddr(smem + warp * Cfg::WARP_BYTES);
+    float4* joinbuf = reinterpret_cast<float4*>(smem + kDecWarps * Cfg::WARP_BYTES);
 
     // blocks of a request: at least one, so that one which sees nothing is written too
-    auto blocks = [&](int b) { return max(1, (seen_of(clamp_len(a.lengths[b], a), a).count + kBlock - 1) / kBlock); };
-    long long u0, u1, U;
+    auto blocks_of = [&](const Seen& s) { return max(1, (s.count + kBlock - 1) / kBlock); };
+    auto blocks = [&](int b) { return blocks_of(seen_of(clamp_len(__ldg(a.lengths + b), a), a)); };
+    long long u, u1, U;
     int C;
     {
         const int each = (B + kDecThreads - 1) / kDecThreads, b0 = min(B, tid * each), b1 = min(B, b0 + each);
@@ -81,71 +94,105 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
         long long at = block_scan<kDecThreads>(mine, &U);
         C = (int)min((long long)gridDim.x, U);
         if ((int)blockIdx.x >= C) return;
-        u0 = U * blockIdx.x / C;
-        u1 = U * (blockIdx.x + 1) / C;
-        if (u0 >= at && u0 < at + mine) {
+        if (U < (1 << 22)) {                                          // C <= 304: the products fit 32 bits
+            u = (int)U * (int)blockIdx.x / C;
+            u1 = (int)U * (int)(blockIdx.x + 1) / C;
+        } else {
+            u = U * blockIdx.x / C;
+            u1 = U * (blockIdx.x + 1) / C;
+        }
+        if (u >= at && u < at + mine) {
             int b = b0;
-            for (long long n; u0 >= at + (n = (long long)blocks(b) * segs); ++b) at += n;
+            for (long long n; u >= at + (n = (long long)blocks(b) * segs); ++b) at += n;
             s_b = b;
             s_base = at;
         }
         __syncthreads();
     }
-    int b = s_b;
-    long long base = s_base;
+    int cur_b = s_b;
+    long long base = s_base;                                           // first unit of request cur_b
 
-    for (long long u = u0; u < u1;) {
-        const int len = clamp_len(a.lengths[b], a);
-        const Seen seen = seen_of(len, a);
-        const int nb = max(1, (seen.count + kBlock - 1) / kBlock);
-        const int seg = (int)((u - base) / nb), blk0 = (int)((u - base) % nb);
-        const int blk1 = (int)min((long long)nb, blk0 + (u1 - u));
-        const int hk = seg / chunks, h0 = (seg % chunks) * 8 * NT, hn = min(8 * NT, grp - h0);
-        const size_t head0 = (size_t)hk * grp + h0;
-        const T* kp = (const T*)a.k + hk * a.p.head_stride;
-        const T* vp = (const T*)a.v + hk * a.p.head_stride;
-        const int32_t* table = a.table + (size_t)b * a.p.max_pages;
-        const int end = min(blk1 * kBlock, seen.count);               // list indices of this piece: [blk0 kBlock, end)
-        const int tile0 = blk0 * kDecWarps + warp;
-        const int tiles = max(0, ((end + kTile - 1) / kTile - tile0 + kDecWarps - 1) / kDecWarps);
+    // the piece that begins at unit u (u < u1); u, cur_b and base move past it
+    auto next_work = [&] {
+        Work w;
+        w.b = cur_b;
+        w.seen = seen_of(clamp_len(__ldg(a.lengths + cur_b), a), a);
+        w.nb = blocks_of(w.seen);
+        const long long rel = u - base;
+        const int seg = rel < 0x7fffffffll ? (int)rel / w.nb : (int)(rel / w.nb);
+        w.first = base + (long long)seg * w.nb;
+        w.blk0 = (int)(u - w.first);
+        w.blk1 = (int)min((long long)w.nb, w.blk0 + (u1 - u));
+        w.hk = chunks == 1 ? seg : seg / chunks;
+        const int h0 = chunks == 1 ? 0 : (seg % chunks) * 8 * NT;
+        w.hn = min(8 * NT, grp - h0);
+        w.head0 = w.hk * grp + h0;
+        w.end = min(w.blk1 * kBlock, w.seen.count);
+        w.tile0 = w.blk0 * kDecWarps + warp;
+        w.tiles = max(0, ((w.end + kTile - 1) / kTile - w.tile0 + kDecWarps - 1) / kDecWarps);
+        u += w.blk1 - w.blk0;
+        if (w.blk1 == w.nb && seg == segs - 1) {
+            base += (long long)w.nb * segs;
+            ++cur_b;
+        }
+        return w;
+    };
 
-        // queries as the B operand: lane holds head lane/4, elements 2 (lane % 4) + {0, 1} of each half step
-        uint32_t qf[NT][KS][2];
+    // lane (and lane + 16): token lane % 16 of the piece's tile t, its page one step ahead of its load
+    int tok = -1, page = -1;
+    auto look_up = [&](const Work& w, int t) {
+        const int i = (w.tile0 + t * kDecWarps) * kTile + (lane & 15);
+        tok = i < w.end ? (i < w.seen.first ? i : i - w.seen.first + w.seen.from) : -1;
+        page = tok >= 0 ? __ldg(a.table + (size_t)w.b * a.p.max_pages + (tok >> a.shift)) : -1;
+    };
+    auto load = [&](const Work& w, int t) {
+        const int s = t % STAGES;
+        const T* kp = (const T*)a.k + w.hk * a.p.head_stride;
+        const T* vp = (const T*)a.v + w.hk * a.p.head_stride;
+        const bool ok = page >= 0 && page < a.p.num_pages;
+        const long long off = ok ? page * a.p.page_stride + (tok & ((1 << a.shift) - 1)) * a.p.token_stride : 0;
+        const uint32_t oks = __ballot_sync(0xffffffffu, ok);
+        if (lane == 0) s_ok[warp][s] = oks;
+        const uint32_t dst = wbase + s * 2 * Cfg::TILE_BYTES;
+#pragma unroll
+        for (int j = 0; j < kTile * CPR / 32; ++j) {
+            const int r = (j * 32 + lane) / CPR, c = (j * 32 + lane) % CPR;
+            const long long o = __shfl_sync(0xffffffffu, off, r) + c * 8;
+            const bool v = (oks >> r) & 1u;
+            cp16(dst + swz<ROW>(r, c), kp + o, v);
+            cp16(dst + Cfg::TILE_BYTES + swz<ROW>(r, c), vp + o, v);
+        }
+    };
+    auto begin = [&](const Work& w) {                                   // the first tiles, STAGES - 1 copy groups
+        if (w.tiles > 0) look_up(w, 0);
+        for (int t = 0; t < STAGES - 1; ++t) {
+            if (t < w.tiles) {
+                load(w, t);
+                look_up(w, t + 1);
+            }
+            cp_commit();
+        }
+    };
+    // queries as the B operand: lane holds head lane/4, elements 2 (lane % 4) + {0, 1} of each half step
+    uint32_t qf[NT][KS][2];
+    auto load_q = [&](const Work& w) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int h = n * 8 + (lane >> 2);
-            const uint32_t* q = reinterpret_cast<const uint32_t*>((const T*)a.q + (size_t)b * a.p.q_stride +
-                                                                  (head0 + (h < hn ? h : 0)) * D) + (lane & 3);
+            const uint32_t* q = reinterpret_cast<const uint32_t*>((const T*)a.q + (size_t)w.b * a.p.q_stride +
+                                                                  (size_t)(w.head0 + (h < w.hn ? h : 0)) * D) + (lane & 3);
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
-                qf[n][k][0] = h < hn ? __ldg(q + k * 8) : 0u;
-                qf[n][k][1] = h < hn ? __ldg(q + k * 8 + 4) : 0u;
+                qf[n][k][0] = h < w.hn ? __ldg(q + k * 8) : 0u;
+                qf[n][k][1] = h < w.hn ? __ldg(q + k * 8 + 4) : 0u;
             }
         }
+    };
 
-        // lane (and lane + 16): token lane % 16 of a tile
-        auto token_of = [&](int tile) {
-            const int i = (tile0 + tile * kDecWarps) * kTile + (lane & 15);
-            return i < end ? (i < seen.first ? i : i - seen.first + seen.from) : -1;
-        };
-        auto page_of = [&](int tok) { return tok >= 0 ? __ldg(table + (tok >> a.shift)) : -1; };
-        auto load = [&](int tile, int tok, int page) {
-            const int s = tile % STAGES;
-            const bool ok = page >= 0 && page < a.p.num_pages;
-            const long long off = ok ? page * a.p.page_stride + (tok & ((1 << a.shift) - 1)) * a.p.token_stride : 0;
-            const uint32_t oks = __ballot_sync(0xffffffffu, ok);
-            if (lane == 0) s_ok[warp][s] = oks;
-            const uint32_t dst = wbase + s * 2 * Cfg::TILE_BYTES;
-#pragma unroll
-            for (int j = 0; j < kTile * CPR / 32; ++j) {
-                const int r = (j * 32 + lane) / CPR, c = (j * 32 + lane) % CPR;
-                const long long o = __shfl_sync(0xffffffffu, off, r) + c * 8;
-                const bool v = (oks >> r) & 1u;
-                cp16(dst + swz<ROW>(r, c), kp + o, v);
-                cp16(dst + Cfg::TILE_BYTES + swz<ROW>(r, c), vp + o, v);
-            }
-        };
-
+    Work w = next_work();
+    begin(w);
+    load_q(w);
+    for (;;) {
         float o[NT][KS][4], m[NT][2], l[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -154,23 +201,12 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
 #pragma unroll
             for (int k = 0; k < KS; ++k) o[n][k][0] = o[n][k][1] = o[n][k][2] = o[n][k][3] = 0.f;
         }
-
-        int tok = tiles > 0 ? token_of(0) : -1, page = page_of(tok);
-        for (int t = 0; t < STAGES - 1; ++t) {
-            if (t < tiles) {
-                load(t, tok, page);
-                tok = token_of(t + 1);
-                page = page_of(tok);
-            }
-            cp_commit();
-        }
-        for (int t = 0; t < tiles; ++t) {
+        for (int t = 0; t < w.tiles; ++t) {
             cp_wait<STAGES - 2>();
             __syncwarp();
-            if (t + STAGES - 1 < tiles) {
-                load(t + STAGES - 1, tok, page);
-                tok = token_of(t + STAGES);
-                page = page_of(tok);
+            if (t + STAGES - 1 < w.tiles) {
+                load(w, t + STAGES - 1);
+                look_up(w, t + STAGES);
             }
             cp_commit();
             const int s = t % STAGES;
@@ -258,11 +294,17 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
                 }
             }
         }
-        cp_wait<0>();
         __syncwarp();
+        const Work done = w;
+        const bool more = u < u1;
+        if (more) {                                                     // every buffer of this warp is free
+            w = next_work();
+            begin(w);
+            load_q(w);
+        }
 
-        // the warps' results, through the (now idle) pipeline buffers: [head][D] per warp
-        float* wo = reinterpret_cast<float*>(wsm);
+        // this piece's results: the warps' m and l, then quarter by quarter of d, each by one warp.  o[n][k] holds heads
+        // n 8 + 2 (lane % 4) + {0, 1} of elements k 16 + lane / 4 + {0, 8}, the same in every warp.
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -271,89 +313,129 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
                 v += __shfl_xor_sync(0xffffffffu, v, 4);
                 v += __shfl_xor_sync(0xffffffffu, v, 8);
                 v += __shfl_xor_sync(0xffffffffu, v, 16);
-                const int h = n * 8 + 2 * (lane & 3) + i;
                 if (lane < 4) {
-                    s_m[warp][h] = m[n][i];
-                    s_l[warp][h] = v;
-                }
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    wo[h * D + k * 16 + (lane >> 2)] = o[n][k][i];
-                    wo[h * D + k * 16 + (lane >> 2) + 8] = o[n][k][i + 2];
+                    s_m[warp][n * 8 + 2 * lane + i] = m[n][i];
+                    s_l[warp][n * 8 + 2 * lane + i] = v;
                 }
             }
-        __syncthreads();
-        const bool whole = blk0 == 0 && blk1 == nb;
-        float* piece = reinterpret_cast<float*>((unsigned char*)a.ws + kCounterBytes);
-        const size_t psize = Piece::floats(D);
-        float* mine = piece + (2 * (size_t)blockIdx.x + (blk0 == 0 ? 1 : 0)) * psize;
-        auto finish = [&](int h, int c, float mh, float lh, float oh) {
-            const size_t row = (size_t)b * a.p.Hq + head0 + h;
-            T* out = (T*)a.out + (size_t)b * a.p.out_stride + (head0 + h) * D;
-            const float y = lh > 0.f ? oh / lh : (lh == lh ? 0.f : lh);
-            out[c] = (T)y;
-            if (c == 0 && a.lse) a.lse[row] = lh == 0.f ? -INFINITY : (mh + log2f(lh)) * kLn2;
-        };
-        for (int i = tid; i < hn * D; i += kDecThreads) {
-            const int h = i / D, c = i % D;
-            float mh = -INFINITY, lh = 0.f, oh = 0.f;
+        const bool whole = done.blk0 == 0 && done.blk1 == done.nb;
+        float* pieces = reinterpret_cast<float*>((unsigned char*)a.ws + kCounterBytes);
+        constexpr size_t PF = piece_floats(D);
+        float* mine = pieces + (2 * (size_t)blockIdx.x + (done.blk0 == 0 ? 1 : 0)) * PF;
+        auto lse_of = [&](float mh, float lh) { return lh == 0.f ? -INFINITY : (mh + log2f(lh)) * kLn2; };
 #pragma unroll
-            for (int w = 0; w < kDecWarps; ++w) mh = fmaxf(mh, s_m[w][h]);
+        for (int n = 0; n < NT; ++n) {
+            // slot of warp x's quarter y (y != x): [x][y or y - 1][step][lane]
 #pragma unroll
-            for (int w = 0; w < kDecWarps; ++w) {
-                const float f = s_m[w][h] == -INFINITY ? 0.f : exp2_fast(s_m[w][h] - mh);
-                lh = fmaf(f, s_l[w][h], lh);
-                oh = fmaf(f, reinterpret_cast<const float*>(smem + w * Cfg::WARP_BYTES)[h * D + c], oh);
+            for (int k = 0; k < KS; ++k) {
+                const int y = k / KQ;
+                if (y != warp)
+                    joinbuf[((warp * 3 + (y < warp ? y : y - 1)) * KQ + k % KQ) * 32 + lane] =
+                        make_float4(o[n][k][0], o[n][k][1], o[n][k][2], o[n][k][3]);
             }
-            if (whole) {
-                finish(h, c, mh, lh, oh);
-            } else {
-                mine[h * D + c] = oh;
-                if (c == 0) {
-                    mine[kMaxHeads * D + h] = mh;
-                    mine[kMaxHeads * D + kMaxHeads + h] = lh;
+            __syncthreads();
+            float f[kDecWarps][2], mh[2], lh[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int h = n * 8 + 2 * (lane & 3) + i;
+                mh[i] = -INFINITY;
+                lh[i] = 0.f;
+#pragma unroll
+                for (int x = 0; x < kDecWarps; ++x) mh[i] = fmaxf(mh[i], s_m[x][h]);
+#pragma unroll
+                for (int x = 0; x < kDecWarps; ++x) {
+                    f[x][i] = s_m[x][h] == -INFINITY ? 0.f : exp2_fast(s_m[x][h] - mh[i]);
+                    lh[i] = fmaf(f[x][i], s_l[x][h], lh[i]);
                 }
             }
+#pragma unroll
+            for (int k = 0; k < KQ; ++k) {
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int x = 0; x < kDecWarps; ++x) {
+                    float4 v;
+                    if (x == warp) {
+                        // o[n][warp KQ + k], with constant indexes
+                        v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int y = 0; y < kDecWarps; ++y)
+                            if (y == warp) v = make_float4(o[n][y * KQ + k][0], o[n][y * KQ + k][1], o[n][y * KQ + k][2], o[n][y * KQ + k][3]);
+                    } else {
+                        v = joinbuf[((x * 3 + (warp < x ? warp : warp - 1)) * KQ + k) * 32 + lane];
+                    }
+                    acc.x = fmaf(f[x][0], v.x, acc.x);
+                    acc.y = fmaf(f[x][1], v.y, acc.y);
+                    acc.z = fmaf(f[x][0], v.z, acc.z);
+                    acc.w = fmaf(f[x][1], v.w, acc.w);
+                }
+                const int c = (warp * KQ + k) * 16 + (lane >> 2);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int h = n * 8 + 2 * (lane & 3) + i;
+                    const float y0 = i ? acc.y : acc.x, y1 = i ? acc.w : acc.z;
+                    if (h >= done.hn) continue;
+                    if (whole) {
+                        T* out = (T*)a.out + (size_t)done.b * a.p.out_stride + (size_t)(done.head0 + h) * D + c;
+                        const float inv = lh[i] > 0.f ? 1.f / lh[i] : (lh[i] == lh[i] ? 0.f : lh[i]);
+                        out[0] = (T)(y0 * inv);
+                        out[8] = (T)(y1 * inv);
+                        if (k == 0 && warp == 0 && lane < 4 && a.lse)
+                            a.lse[(size_t)done.b * a.p.Hq + done.head0 + h] = lse_of(mh[i], lh[i]);
+                    } else {
+                        mine[h * D + c] = y0;
+                        mine[h * D + c + 8] = y1;
+                        if (k == 0 && warp == 0 && lane < 4) {
+                            mine[kMaxHeads * D + h] = mh[i];
+                            mine[kMaxHeads * (D + 1) + h] = lh[i];
+                        }
+                    }
+                }
+            }
+            __syncthreads();                            // the buffer, and s_m and s_l, are written again
         }
         if (!whole) {
             // CTAs whose shares hold a part of this (request, heads): unit x is in share ((x + 1) C - 1) / U
-            const long long s0 = base + (long long)seg * nb;
-            const int c0 = (int)(((s0 + 1) * C - 1) / U), c1 = (int)(((s0 + nb) * C - 1) / U);
-            int* counter = reinterpret_cast<int*>(a.ws) + c0;
-            __threadfence();
-            __syncthreads();
+            const int c0 = (int)(((done.first + 1) * C - 1) / U), c1 = (int)(((done.first + done.nb) * C - 1) / U);
             if (tid == 0) {
+                int* counter = reinterpret_cast<int*>(a.ws) + c0;
+                __threadfence();
                 s_last = atomicAdd(counter, 1) == c1 - c0;
                 if (s_last) *counter = 0;
+                __threadfence();
             }
             __syncthreads();
             if (s_last) {
-                __threadfence();
-                for (int i = tid; i < hn * D; i += kDecThreads) {
-                    const int h = i / D, c = i % D;
-                    float mh = -INFINITY, lh = 0.f, oh = 0.f;
+                // pieces in their order, so that it does not matter who joins them: 4 columns a thread, all rows at once
+                auto piece = [&](int x) { return pieces + (2 * (size_t)x + (x == c0 ? 1 : 0)) * PF; };
+                constexpr int TPR = D / 4;              // threads per row
+                for (int h = tid / TPR; h < done.hn; h += kDecThreads / TPR) {
+                    const int c = tid % TPR * 4;
+                    float mh = -INFINITY;
+#pragma unroll 8
+                    for (int x = c0; x <= c1; ++x) mh = fmaxf(mh, __ldcg(piece(x) + kMaxHeads * D + h));
+                    float lh = 0.f;
+                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
                     for (int x = c0; x <= c1; ++x) {
-                        const float* p = piece + (2 * (size_t)x + (x == c0 ? 1 : 0)) * psize;
-                        mh = fmaxf(mh, __ldcg(p + kMaxHeads * D + h));
-                    }
-#pragma unroll 4
-                    for (int x = c0; x <= c1; ++x) {
-                        const float* p = piece + (2 * (size_t)x + (x == c0 ? 1 : 0)) * psize;
-                        const float pm = __ldcg(p + kMaxHeads * D + h);
+                        const float* q = piece(x);
+                        const float pm = __ldcg(q + kMaxHeads * D + h), ll = __ldcg(q + kMaxHeads * (D + 1) + h);
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(q + h * D + c));
                         const float f = pm == -INFINITY ? 0.f : exp2_fast(pm - mh);
-                        lh = fmaf(f, __ldcg(p + kMaxHeads * D + kMaxHeads + h), lh);
-                        oh = fmaf(f, __ldcg(p + h * D + c), oh);
+                        lh = fmaf(f, ll, lh);
+                        y.x = fmaf(f, v.x, y.x);
+                        y.y = fmaf(f, v.y, y.y);
+                        y.z = fmaf(f, v.z, y.z);
+                        y.w = fmaf(f, v.w, y.w);
                     }
-                    finish(h, c, mh, lh, oh);
+                    const float inv = lh > 0.f ? 1.f / lh : (lh == lh ? 0.f : lh);
+                    T* out = (T*)a.out + (size_t)done.b * a.p.out_stride + (size_t)(done.head0 + h) * D + c;
+                    *reinterpret_cast<uint2*>(out) = make_uint2(Num<T>::pack(y.x * inv, y.y * inv), Num<T>::pack(y.z * inv, y.w * inv));
+                    if (c == 0 && a.lse) a.lse[(size_t)done.b * a.p.Hq + done.head0 + h] = lse_of(mh, lh);
                 }
             }
+            __syncthreads();                            // s_last is written again
         }
-        __syncthreads();                                // the buffers and s_m, s_l are written again
-        u += blk1 - blk0;
-        if (blk1 == nb && seg == segs - 1) {
-            base += (long long)nb * segs;
-            ++b;
-        }
+        if (!more) break;
     }
 }
 
@@ -383,7 +465,7 @@ cudaError_t launch_t(const PagedArgs& a, cudaStream_t st)
 
 size_t paged_attend_workspace(const fadkv_paged_params& p)
 {
-    return kCounterBytes + (size_t)2 * kDecCtas * Piece::floats(p.d) * sizeof(float);
+    return kCounterBytes + (size_t)2 * kDecCtas * piece_floats(p.d) * sizeof(float);
 }
 
 cudaError_t launch_paged_attend(const PagedArgs& a, cudaStream_t st)

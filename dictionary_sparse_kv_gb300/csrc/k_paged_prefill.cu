@@ -53,6 +53,7 @@ constexpr int kPreThreads = 384;
 constexpr int kRows = 128;                         // (token, head) rows per tile, two tiles per CTA
 constexpr int kKeys = 128;                         // keys per tile
 constexpr int kOkRing = 16;                        // key tiles whose page masks are kept
+constexpr int kPart = 64;                          // keys whose P is handed over first; the rest follows
 constexpr float kGrow = 8.f;                       // growth of the maximum (log2) that rescales
 
 constexpr int kPreCtas = 152;                      // one per multiprocessor
@@ -234,7 +235,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     auto ofree = [&](int q) { return bar(6 + q); };             // O has been read
     auto qfull = [&](int q) { return bar(8 + q); };
     auto qempty = [&](int q) { return bar(10 + q); };
-    auto pfull = [&](int q, int half) { return bar(12 + 2 * q + half); };
+    auto pfull = [&](int q, int part) { return bar(12 + 2 * q + part); };
     const uint32_t ifull = bar(16), iempty = bar(17);
     unsigned long long* status = reinterpret_cast<unsigned long long*>(a.ws);
     unsigned int* counter = reinterpret_cast<unsigned int*>(a.ws) + 2;   // items handed out; CTAs that are done
@@ -396,14 +397,14 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             }
             ++qks[q];
         };
-        // one half of the keys
-        auto pv = [&](int q, int stage, int half, bool add) {
-            const uint64_t dv = dn0 + (uint64_t)(stage * (TILE >> 4) + half * (kKeys / 2 * 128 >> 4));
+        // 16-key steps j0 .. j1-1
+        auto pv = [&](int q, int stage, int j0, int j1, bool add) {
+            const uint64_t dv = dn0 + (uint64_t)(stage * (TILE >> 4));
             if (leader)
 #pragma unroll
-                for (int j = 0; j < kKeys / 32; ++j)
-                    mma_ts(tbase + C::O(q), tbase + C::P(q) + (half * (kKeys / 32) + j) * 8, dv + (uint64_t)(j * 2048 >> 4),
-                           kPV, add || j > 0 ? 1u : 0u);
+                for (int j = j0; j < j1; ++j)
+                    mma_ts(tbase + C::O(q), tbase + C::P(q) + j * 8, dv + (uint64_t)(j * 2048 >> 4), kPV,
+                           add || j > 0 ? 1u : 0u);
         };
         // value rows that no row of the item sees: zeros (while the softmax works on the scores)
         auto clear = [&](const Tiles& ts, int k0, int stage) {
@@ -466,12 +467,12 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                     wait(pfull(q, 0), (uint32_t)pvs[q] & 1u);
                     if (!ok) break;
                     fence_after();
-                    pv(q, rv.st, 0, i > 0);
-                    wait(pfull(q, 1), (uint32_t)pvs[q] & 1u);
+                    pv(q, rv.st, 0, kPart / 16, i > 0);
                     if (!C::kOwnP && q == 0 && more) wait(full(ring.st), ring.ph);
+                    wait(pfull(q, 1), (uint32_t)pvs[q] & 1u);
                     if (!ok) break;
                     fence_after();
-                    pv(q, rv.st, 1, true);
+                    pv(q, rv.st, kPart / 16, kKeys / 16, true);
                     if (leader) mma_commit(pvdone(q));
                     ++pvs[q];
                     if (q == nq - 1 && leader) mma_commit(empty(rv.st));
@@ -670,11 +671,11 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                     // P in its own columns: the product that read the last one must be done (it is, mostly)
                     if (C::kOwnP && c == 0 && i > 0 && !wait(pvdone(q), (uint32_t)(its - 1) & 1u)) break;
                     tmem_st16(lanes + C::P(q) + c * 16, p);
-                    if (c & 1) {                               // half of the keys: the product may begin
+                    if (c == kPart / 32 - 1 || c == 3) {       // the product may begin on these keys
                         tmem_st_wait();
                         fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(pfull(q, c >> 1));
+                        if (lane == 0) mbar_arrive(pfull(q, c == 3));
                     }
                 }
                 if (!ok) break;
