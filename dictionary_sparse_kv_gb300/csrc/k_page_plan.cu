@@ -17,10 +17,12 @@
 namespace fadkv {
 namespace {
 
-constexpr int kPlanThreads = 1024;
 constexpr int kRowThreads = 256;
 // Rows that the scanning block writes itself, in place of a second launch.
 constexpr int kRowsInPlan = 4096;
+// A block of 128 threads where requests and rows are few: its barriers and
+// scans take less than those of 1024.
+constexpr int kFew = 512;
 
 __device__ __forceinline__ int pages_of(int tokens, int shift) { return (int)(((long long)tokens + (1 << shift) - 1) >> shift); }
 
@@ -38,18 +40,14 @@ __device__ __forceinline__ int owner(const int* pre, int n, int v)
 
 __device__ __forceinline__ int saturate(long long v) { return v > 0x7fffffffll ? 0x7fffffff : (int)v; }
 
-__device__ __forceinline__ void write_row(const PlanArgs& a, int t, int b, int pos)
+__device__ __forceinline__ void write_row(const PlanArgs& a, int t, int pos, int page)
 {
-    int slot = -1;
-    if (pos >= 0) {
-        const int page = a.table[(size_t)b * a.max_pages + (pos >> a.shift)];
-        if (page >= 0 && page < a.num_pages) slot = (page << a.shift) + (pos & ((1 << a.shift) - 1));
-    }
     a.positions[t] = pos;
-    a.slots[t] = slot;
+    a.slots[t] = pos >= 0 && page >= 0 && page < a.num_pages ? (page << a.shift) + (pos & ((1 << a.shift) - 1)) : -1;
 }
 
-__global__ void __launch_bounds__(kPlanThreads)
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS)
 page_plan_kernel(PlanArgs a, int rows_here)
 {
     extern __shared__ int sm[];
@@ -57,65 +55,84 @@ page_plan_kernel(PlanArgs a, int rows_here)
     int* nd = st + a.B + 1;            // [B + 1] prefix of needed pages
     int* bk = nd + a.B + 1;            // [B + 1] prefix of returned pages; then the served requests' lengths, -1 otherwise
     __shared__ int s_taken, s_refused;
-    const int tid = threadIdx.x, B = a.B;
+    __shared__ long long s_part[3][THREADS / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.B;
     const int most = a.max_pages << a.shift;
-    const int each = (B + kPlanThreads - 1) / kPlanThreads, b0 = min(B, tid * each), b1 = min(B, b0 + each);
+    const int each = (B + THREADS - 1) / THREADS, b0 = min(B, tid * each), b1 = min(B, b0 + each);
     if (tid == 0) s_taken = s_refused = 0;
 
     auto length = [&](int b) { return min(max(a.lengths[b], 0), most); };
-    auto item = [&](int b, long long& n, long long& need, long long& back) {
+    // rows, needed and returned pages of a request
+    auto item = [&](int b, long long (&v)[3]) {
         const int len = length(b), add = a.add[b];
-        n = max(add, 0);
-        need = (n > 0 && len + n <= most) ? pages_of((int)(len + n), a.shift) - pages_of(len, a.shift) : 0;
-        back = add < 0 ? pages_of(len, a.shift) : 0;
+        v[0] = max(add, 0);
+        v[1] = add > 0 && (long long)len + add <= most ? pages_of(len + add, a.shift) - pages_of(len, a.shift) : 0;
+        v[2] = add < 0 ? pages_of(len, a.shift) : 0;
     };
-    long long n, need, back, sn = 0, sneed = 0, sback = 0, tn, tneed, tback;
+    const int count = min(max(*a.free_count, 0), a.num_pages);
+    long long v[3], mine[3] = {0, 0, 0}, at[3], total[3];
     for (int b = b0; b < b1; ++b) {
-        item(b, n, need, back);
-        sn += n;
-        sneed += need;
-        sback += back;
+        item(b, v);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) mine[k] += v[k];
     }
-    sn = paged::block_scan<kPlanThreads>(sn, &tn);
-    sneed = paged::block_scan<kPlanThreads>(sneed, &tneed);
-    sback = paged::block_scan<kPlanThreads>(sback, &tback);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        at[k] = mine[k];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, at[k], o);
+            if (lane >= o) at[k] += y;
+        }
+        if (lane == 31) s_part[k][warp] = at[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        at[k] -= mine[k];
+        total[k] = 0;
+        for (int w = 0; w < THREADS / 32; ++w) {
+            if (w < warp) at[k] += s_part[k][w];
+            total[k] += s_part[k][w];
+        }
+    }
     for (int b = b0; b < b1; ++b) {
-        item(b, n, need, back);
-        st[b] = saturate(sn);
-        nd[b] = saturate(sneed);
-        bk[b] = saturate(sback);
+        st[b] = saturate(at[0]);
+        nd[b] = saturate(at[1]);
+        bk[b] = saturate(at[2]);
         a.starts[b] = st[b];
-        sn += n;
-        sneed += need;
-        sback += back;
+        if (each > 1) item(b, v);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) at[k] += each > 1 ? v[k] : mine[k];
     }
     if (tid == 0) {
-        st[B] = saturate(tn);
-        nd[B] = saturate(tneed);
-        bk[B] = saturate(tback);
+        st[B] = saturate(total[0]);
+        nd[B] = saturate(total[1]);
+        bk[B] = saturate(total[2]);
         a.starts[B] = st[B];
     }
-    const int count = min(max(*a.free_count, 0), a.num_pages);
     __syncthreads();
     const int returned = min(bk[B], a.num_pages - count), F = count + returned;
-    for (int i = tid; i < returned; i += kPlanThreads) {
-        const int b = owner(bk, B, i);
-        a.free_pages[count + i] = a.table[(size_t)b * a.max_pages + i - bk[b]];
+    if (returned > 0) {
+        for (int i = tid; i < returned; i += THREADS) {
+            const int b = owner(bk, B, i);
+            a.free_pages[count + i] = a.table[(size_t)b * a.max_pages + i - bk[b]];
+        }
     }
-    __syncthreads();
+    if (bk[B] > 0) __syncthreads();                    // the free list is read, and bk written, below
     for (int b = b0; b < b1; ++b) {
         const int len = length(b), add = a.add[b];
         const bool served = add > 0 && (long long)len + add <= most && st[b + 1] <= a.max_tokens &&
                             (nd[b + 1] == nd[b] || nd[b + 1] <= F);
-        bk[b] = served ? len : -1;
         a.lengths_out[b] = add < 0 ? 0 : (served ? len + add : len);
         if (served && nd[b + 1] > nd[b]) atomicMax(&s_taken, nd[b + 1]);
         if (add > 0 && !served) atomicAdd(&s_refused, 1);
         if (!rows_here && add > 0 && st[b] < a.max_tokens) a.positions[st[b]] = served ? len : -1;
+        bk[b] = served ? len : -1;
     }
     __syncthreads();
     const int taken = s_taken;
-    for (int m = tid; m < taken; m += kPlanThreads) {
+    for (int m = tid; m < taken; m += THREADS) {
         const int b = owner(nd, B, m);
         a.table[(size_t)b * a.max_pages + pages_of(bk[b], a.shift) + m - nd[b]] = a.free_pages[F - 1 - m];
     }
@@ -124,15 +141,19 @@ page_plan_kernel(PlanArgs a, int rows_here)
         *a.refused = s_refused;
     }
     if (!rows_here) return;
-    __syncthreads();
+    // a row's page: one that the request had, or one taken above (from the free list: the table entry may be on its way)
     const int T = st[B];
-    for (int t = tid; t < a.max_tokens; t += kPlanThreads) {
-        int b = 0, pos = -1;
+    for (int t = tid; t < a.max_tokens; t += THREADS) {
+        int pos = -1, page = -1;
         if (t < T) {
-            b = owner(st, B, t);
-            if (bk[b] >= 0) pos = bk[b] + t - st[b];
+            const int b = owner(st, B, t);
+            if (bk[b] >= 0) {
+                pos = bk[b] + t - st[b];
+                const int fresh = (pos >> a.shift) - pages_of(bk[b], a.shift);
+                page = fresh >= 0 ? a.free_pages[F - 1 - nd[b] - fresh] : a.table[(size_t)b * a.max_pages + (pos >> a.shift)];
+            }
         }
-        write_row(a, t, b, pos);
+        write_row(a, t, pos, page);
     }
 }
 
@@ -145,13 +166,15 @@ page_rows_kernel(PlanArgs a)
     pdl_begin();
     const int t = blockIdx.x * kRowThreads + threadIdx.x;
     if (t >= a.max_tokens) return;
-    int b = 0, pos = -1;
+    int pos = -1, page = -1;
     if (t < a.starts[a.B]) {
-        b = owner(a.starts, a.B, t);
-        const int s = a.starts[b], first = a.positions[s];
-        if (first >= 0) pos = first + t - s;
+        const int b = owner(a.starts, a.B, t), s = a.starts[b], first = a.positions[s];
+        if (first >= 0) {
+            pos = first + t - s;
+            page = a.table[(size_t)b * a.max_pages + (pos >> a.shift)];
+        }
     }
-    write_row(a, t, b, pos);
+    write_row(a, t, pos, page);
 }
 
 }  // namespace
@@ -161,10 +184,14 @@ cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t st)
     const size_t smem = (size_t)3 * (a.B + 1) * sizeof(int);
     const int rows_here = a.max_tokens <= kRowsInPlan;
     cudaError_t e = cudaSuccess;
-    if (smem > 48 * 1024)
-        e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    page_plan_kernel<<<1, kPlanThreads, smem, st>>>(a, rows_here);
+    if (a.B <= kFew && a.max_tokens <= kFew) {
+        page_plan_kernel<128><<<1, 128, smem, st>>>(a, rows_here);
+    } else {
+        if (smem > 48 * 1024)
+            e = cudaFuncSetAttribute(page_plan_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        page_plan_kernel<1024><<<1, 1024, smem, st>>>(a, rows_here);
+    }
     e = cudaGetLastError();
     if (e != cudaSuccess || rows_here) return e;
     return launch_pdl(page_rows_kernel, dim3((unsigned)((a.max_tokens + kRowThreads - 1) / kRowThreads)),

@@ -62,6 +62,13 @@ struct Work {
     long long first;           // unit number of block 0
 };
 
+__device__ __forceinline__ int add_acq_rel(int* p, int v)
+{
+    int old;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
+}
+
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kDecThreads)
 paged_decode_kernel(const __grid_constant__ PagedArgs a)
@@ -85,15 +92,10 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
     // blocks of a request: at least one, so that one which sees nothing is written too
     auto blocks_of = [&](const Seen& s) { return max(1, (s.count + kBlock - 1) / kBlock); };
     auto blocks = [&](int b) { return blocks_of(seen_of(clamp_len(__ldg(a.lengths + b), a), a)); };
-    long long u, u1, U;
-    int C;
-    {
-        const int each = (B + kDecThreads - 1) / kDecThreads, b0 = min(B, tid * each), b1 = min(B, b0 + each);
-        long long mine = 0;
-        for (int b = b0; b < b1; ++b) mine += (long long)blocks(b) * segs;
-        long long at = block_scan<kDecThreads>(mine, &U);
+    long long u, u1, U, base;                                          // this CTA's units; all; the first of request cur_b
+    int C, cur_b;
+    auto share = [&] {
         C = (int)min((long long)gridDim.x, U);
-        if ((int)blockIdx.x >= C) return;
         if (U < (1 << 22)) {                                          // C <= 304: the products fit 32 bits
             u = (int)U * (int)blockIdx.x / C;
             u1 = (int)U * (int)(blockIdx.x + 1) / C;
@@ -101,6 +103,27 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
             u = U * blockIdx.x / C;
             u1 = U * (blockIdx.x + 1) / C;
         }
+    };
+    if (B <= 32) {                                                    // a lane a request, each warp for itself
+        const long long mine = lane < B ? (long long)blocks(lane) * segs : 0;
+        long long upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+        }
+        U = __shfl_sync(0xffffffffu, upto, 31);
+        share();
+        if ((int)blockIdx.x >= C) return;
+        cur_b = __ffs(__ballot_sync(0xffffffffu, upto > u)) - 1;
+        base = __shfl_sync(0xffffffffu, upto - mine, cur_b);
+    } else {
+        const int each = (B + kDecThreads - 1) / kDecThreads, b0 = min(B, tid * each), b1 = min(B, b0 + each);
+        long long mine = 0;
+        for (int b = b0; b < b1; ++b) mine += (long long)blocks(b) * segs;
+        long long at = block_scan<kDecThreads>(mine, &U);
+        share();
+        if ((int)blockIdx.x >= C) return;
         if (u >= at && u < at + mine) {
             int b = b0;
             for (long long n; u >= at + (n = (long long)blocks(b) * segs); ++b) at += n;
@@ -108,9 +131,9 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
             s_base = at;
         }
         __syncthreads();
+        cur_b = s_b;
+        base = s_base;
     }
-    int cur_b = s_b;
-    long long base = s_base;                                           // first unit of request cur_b
 
     // the piece that begins at unit u (u < u1); u, cur_b and base move past it
     auto next_work = [&] {
@@ -398,10 +421,8 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
             const int c0 = (int)(((done.first + 1) * C - 1) / U), c1 = (int)(((done.first + done.nb) * C - 1) / U);
             if (tid == 0) {
                 int* counter = reinterpret_cast<int*>(a.ws) + c0;
-                __threadfence();
-                s_last = atomicAdd(counter, 1) == c1 - c0;
+                s_last = add_acq_rel(counter, 1) == c1 - c0;     // the block's stores before it, the other blocks' after it
                 if (s_last) *counter = 0;
-                __threadfence();
             }
             __syncthreads();
             if (s_last) {
@@ -410,22 +431,35 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
                 constexpr int TPR = D / 4;              // threads per row
                 for (int h = tid / TPR; h < done.hn; h += kDecThreads / TPR) {
                     const int c = tid % TPR * 4;
-                    float mh = -INFINITY;
-#pragma unroll 8
-                    for (int x = c0; x <= c1; ++x) mh = fmaxf(mh, __ldcg(piece(x) + kMaxHeads * D + h));
-                    float lh = 0.f;
+                    float mh = -INFINITY, lh = 0.f;
                     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                    for (int x = c0; x <= c1; ++x) {
-                        const float* q = piece(x);
-                        const float pm = __ldcg(q + kMaxHeads * D + h), ll = __ldcg(q + kMaxHeads * (D + 1) + h);
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(q + h * D + c));
-                        const float f = pm == -INFINITY ? 0.f : exp2_fast(pm - mh);
-                        lh = fmaf(f, ll, lh);
-                        y.x = fmaf(f, v.x, y.x);
-                        y.y = fmaf(f, v.y, y.y);
-                        y.z = fmaf(f, v.z, y.z);
-                        y.w = fmaf(f, v.w, y.w);
+                    // eight pieces at a time, all their loads in flight; past the last one the last one again, with weight 0
+                    for (int x0 = c0; x0 <= c1; x0 += 8) {
+                        float pm[8], ll[8];
+                        float4 v[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float* q = piece(min(x0 + j, c1));
+                            pm[j] = __ldcg(q + kMaxHeads * D + h);
+                            ll[j] = __ldcg(q + kMaxHeads * (D + 1) + h);
+                            v[j] = __ldcg(reinterpret_cast<const float4*>(q + h * D + c));
+                        }
+                        float top = mh;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) top = fmaxf(top, pm[j]);
+                        const float g = mh == -INFINITY ? 0.f : exp2_fast(mh - top);
+                        mh = top;
+                        lh *= g;
+                        y.x *= g, y.y *= g, y.z *= g, y.w *= g;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float f = pm[j] == -INFINITY || x0 + j > c1 ? 0.f : exp2_fast(pm[j] - mh);
+                            lh = fmaf(f, ll[j], lh);
+                            y.x = fmaf(f, v[j].x, y.x);
+                            y.y = fmaf(f, v[j].y, y.y);
+                            y.z = fmaf(f, v[j].z, y.z);
+                            y.w = fmaf(f, v[j].w, y.w);
+                        }
                     }
                     const float inv = lh > 0.f ? 1.f / lh : (lh == lh ? 0.f : lh);
                     T* out = (T*)a.out + (size_t)done.b * a.p.out_stride + (size_t)(done.head0 + h) * D + c;

@@ -10,9 +10,12 @@
 //
 // The work is T (Hq + 2 Hkv) rows of d elements, read once and written once
 // (keys twice with k_out): HBM for long prompts, latency for single tokens.
-// Eight elements a lane (one or two 16-byte loads), so a row is d / 8 lanes
-// and a warp takes 32 / (d / 8) rows of one token at a time; the angles of a
-// token are worked out once a warp and used for all the rows it takes.
+// A row is d / 8 lanes and a warp takes 32 / (d / 8) rows of one token at a
+// time.  A lane holds eight elements as two groups of four: with pairs
+// (i, i + rotary_dim / 2) the two groups are partners, with neighbouring pairs
+// they are side by side, so a pair is always in one lane, nothing is
+// exchanged, and four angles a lane, worked out once a warp for all the rows
+// of its token, do for both layouts.
 #include "paged.cuh"
 
 namespace fadkv {
@@ -21,49 +24,32 @@ namespace {
 constexpr int kQkThreads = 256;
 constexpr int kUnroll = 4;       // rows in flight a lane
 
-template <typename T> struct Raw8;
-template <> struct Raw8<float> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const float* p)
+// Four consecutive elements as loaded.
+template <typename T> struct Raw4 {
+    uint2 a;
+    __device__ __forceinline__ void load(const T* p) { a = __ldg(reinterpret_cast<const uint2*>(p)); }
+    __device__ __forceinline__ void get(float* x) const
     {
-        a = __ldg(reinterpret_cast<const float4*>(p));
-        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    }
-    __device__ __forceinline__ void get(float (&x)[8]) const
-    {
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+        const float2 f = paged::Num<T>::unpack(a.x), g = paged::Num<T>::unpack(a.y);
+        x[0] = f.x, x[1] = f.y, x[2] = g.x, x[3] = g.y;
     }
 };
-template <typename T> struct Raw8 {
-    uint4 a;
-    __device__ __forceinline__ void load(const T* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
-    __device__ __forceinline__ void get(float (&x)[8]) const
-    {
-        const uint32_t u[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = paged::Num<T>::unpack(u[i]);
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
-        }
-    }
+template <> struct Raw4<float> {
+    float4 a;
+    __device__ __forceinline__ void load(const float* p) { a = __ldg(reinterpret_cast<const float4*>(p)); }
+    __device__ __forceinline__ void get(float* x) const { x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w; }
 };
 
-__device__ __forceinline__ void store8(void* base, int dtype, long long at, const float (&y)[8])
+__device__ __forceinline__ void store4(void* base, int dtype, long long at, const float* y)
 {
     if (dtype == FADKV_F32) {
-        float4* p = reinterpret_cast<float4*>((float*)base + at);
-        p[0] = make_float4(y[0], y[1], y[2], y[3]);
-        p[1] = make_float4(y[4], y[5], y[6], y[7]);
+        *reinterpret_cast<float4*>((float*)base + at) = make_float4(y[0], y[1], y[2], y[3]);
     } else if (dtype == FADKV_F16) {
         using N = paged::Num<__half>;
-        *reinterpret_cast<uint4*>((__half*)base + at) =
-            make_uint4(N::pack(y[0], y[1]), N::pack(y[2], y[3]), N::pack(y[4], y[5]), N::pack(y[6], y[7]));
+        *reinterpret_cast<uint2*>((__half*)base + at) = make_uint2(N::pack(y[0], y[1]), N::pack(y[2], y[3]));
     } else {
         using N = paged::Num<__nv_bfloat16>;
-        *reinterpret_cast<uint4*>((__nv_bfloat16*)base + at) =
-            make_uint4(N::pack(y[0], y[1]), N::pack(y[2], y[3]), N::pack(y[4], y[5]), N::pack(y[6], y[7]));
+        *reinterpret_cast<uint2*>((__nv_bfloat16*)base + at) = make_uint2(N::pack(y[0], y[1]), N::pack(y[2], y[3]));
     }
 }
 
@@ -78,103 +64,109 @@ qk_norm_rope_kernel(const __grid_constant__ QkArgs a, int each, int parts)
     if (threadIdx.x < half) turns[threadIdx.x] = a.rope.turns[threadIdx.x];
     __syncthreads();
 
-    const long long w = (long long)blockIdx.x * (kQkThreads / 32) + (threadIdx.x >> 5);
-    const int t = (int)(w / parts), part = (int)(w % parts);
+    const unsigned int w = blockIdx.x * (kQkThreads / 32) + (threadIdx.x >> 5);
+    const int t = (int)(w / (unsigned int)parts), part = (int)(w % (unsigned int)parts);
     if (t >= a.p.T) return;
-    const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR, e0 = l * 8;
-    const int Hq = a.p.Hq, Hkv = a.p.Hkv, rows = Hq + 2 * Hkv;
+    const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
+    const int Hq = a.p.Hq, Hk = Hq + a.p.Hkv, rows = Hk + a.p.Hkv;   // rows: queries, keys, values
     const int pos = a.positions[t];
     const int slot = a.slots ? a.slots[t] : -1;
     const bool append = pos >= 0 && slot >= 0 && (slot >> a.shift) < a.p.num_pages;
     const long long at = (long long)(slot >> a.shift) * a.p.page_stride +
                          (long long)(slot & ((1 << a.shift) - 1)) * a.p.token_stride;
 
-    // cosines and sines of this lane's elements (pairs: one a pair of them)
-    const bool turned = e0 < rd;
-    float cs[8], sn[8];
-    int partner = lane;
+    // this lane's two groups: the first rd / 8 lanes of a row take the rotated part
+    const bool turned = l < rd / 8;
+    const int e0 = PAIRS || !turned ? l * 8 : l * 4, e1 = PAIRS || !turned ? e0 + 4 : e0 + half;
+    float cs[4], sn[4];
     if (turned) {
-        const int i0 = PAIRS ? e0 / 2 : (e0 < half ? e0 : e0 - half);
 #pragma unroll
-        for (int k = 0; k < (PAIRS ? 4 : 8); ++k) {
-            const unsigned long long phase = (unsigned long long)(long long)pos * turns[i0 + k];
+        for (int k = 0; k < 4; ++k) {
+            const unsigned long long phase = (unsigned long long)(long long)pos * turns[l * 4 + k];
             sincospif((float)(int)(phase >> 32) * 0x1p-31f, &sn[k], &cs[k]);
             cs[k] *= a.rope.amplitude;
             sn[k] *= a.rope.amplitude;
-            if (!PAIRS && e0 < half) sn[k] = -sn[k];
         }
-        if (!PAIRS) partner = sub * LPR + (e0 < half ? l + half / 8 : l - half / 8);
     }
+    const bool norm = a.wq || a.wk;
     float wq[8], wk[8];
     if (a.wq) {
-        Raw8<T> r;
-        r.load((const T*)a.wq + e0);
-        r.get(wq);
+        Raw4<T> r[2];
+        r[0].load((const T*)a.wq + e0), r[1].load((const T*)a.wq + e1);
+        r[0].get(wq), r[1].get(wq + 4);
     }
     if (a.wk) {
-        Raw8<T> r;
-        r.load((const T*)a.wk + e0);
-        r.get(wk);
+        Raw4<T> r[2];
+        r[0].load((const T*)a.wk + e0), r[1].load((const T*)a.wk + e1);
+        r[0].get(wk), r[1].get(wk + 4);
     }
 
-    const T* q = (const T*)a.q + t * a.p.q_stride + e0;
-    const T* k = (const T*)a.k + t * a.p.k_stride + e0;
-    const T* v = (const T*)a.v + t * a.p.v_stride + e0;
+    const T* q = (const T*)a.q + t * a.p.q_stride;
+    const T* k = (const T*)a.k + t * a.p.k_stride;
+    const T* v = (const T*)a.v + t * a.p.v_stride;
     const int last = min(rows, (part + 1) * each * RPW);
     for (int r0 = part * each * RPW; r0 < last; r0 += RPW * kUnroll) {
-        Raw8<T> raw[kUnroll];
+        Raw4<T> raw[kUnroll][2];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             const int r = min(r0 + u * RPW + sub, rows - 1);
-            raw[u].load(r < Hq ? q + r * D : r < Hq + Hkv ? k + (r - Hq) * D : v + (r - Hq - Hkv) * D);
+            const T* p = r < Hq ? q + r * D : r < Hk ? k + (r - Hq) * D : v + (r - Hk) * D;
+            raw[u][0].load(p + e0);
+            raw[u][1].load(p + e1);
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
+            if (r0 + u * RPW >= last) break;
             const int r = r0 + u * RPW + sub;
             float x[8];
-            raw[u].get(x);
-            const bool is_q = r < Hq, is_v = r >= Hq + Hkv;
-            if (a.wq || a.wk) {
-                float ss = 0.f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-                for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                const float inv = rsqrtf(ss * (1.f / D) + a.p.eps);
-                if (is_q ? a.wq != nullptr : (!is_v && a.wk != nullptr)) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = x[i] * inv * (is_q ? wq[i] : wk[i]);
-                }
-            }
-            if (rd > 0) {
-                float y[8];
-                if (PAIRS) {
+            raw[u][0].get(x);
+            raw[u][1].get(x + 4);
+            const bool is_q = r < Hq;
+            if (r0 + u * RPW < Hk) {                       // not values alone
+                const bool is_v = r >= Hk;
+                if (norm) {
+                    float s0 = 0.f, s1 = 0.f;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        y[2 * i] = x[2 * i] * cs[i] - x[2 * i + 1] * sn[i];
-                        y[2 * i + 1] = x[2 * i] * sn[i] + x[2 * i + 1] * cs[i];
+                        s0 = fmaf(x[i], x[i], s0);
+                        s1 = fmaf(x[i + 4], x[i + 4], s1);
                     }
-                } else {
+                    float ss = s0 + s1;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        y[i] = x[i] * cs[i] + __shfl_sync(0xffffffffu, x[i], partner) * sn[i];
+                    for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                    const float inv = rsqrtf(ss * (1.f / D) + a.p.eps);
+                    if (is_q ? a.wq != nullptr : (!is_v && a.wk != nullptr)) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] *= inv * (is_q ? wq[i] : wk[i]);
+                    }
                 }
-                if (turned && !is_v)
+                if (turned && !is_v) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = y[i];
+                    for (int i = 0; i < 4; ++i) {
+                        float& p0 = PAIRS ? x[2 * i] : x[i];
+                        float& p1 = PAIRS ? x[2 * i + 1] : x[i + 4];
+                        const float c = p0 * cs[i] - p1 * sn[i];
+                        p1 = p0 * sn[i] + p1 * cs[i];
+                        p0 = c;
+                    }
+                }
+                if (!is_v && pos < 0)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = 0.f;
             }
             if (r >= last) continue;
-            if (!is_v && pos < 0)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = 0.f;
+            auto put = [&](void* base, int dtype, long long row) {
+                store4(base, dtype, row + e0, x);
+                store4(base, dtype, row + e1, x + 4);
+            };
             if (is_q) {
-                store8(a.q_out, a.p.q_dtype, ((long long)t * Hq + r) * D + e0, x);
-            } else if (!is_v) {
+                put(a.q_out, a.p.q_dtype, ((long long)t * Hq + r) * D);
+            } else if (r < Hk) {
                 const int h = r - Hq;
-                if (a.k_out) store8(a.k_out, a.p.kv_dtype, ((long long)t * Hkv + h) * D + e0, x);
-                if (append) store8(a.k_pages, a.p.kv_dtype, at + h * a.p.head_stride + e0, x);
+                if (a.k_out) put(a.k_out, a.p.kv_dtype, ((long long)t * a.p.Hkv + h) * D);
+                if (append) put(a.k_pages, a.p.kv_dtype, at + h * a.p.head_stride);
             } else if (append) {
-                store8(a.v_pages, a.p.kv_dtype, at + (r - Hq - Hkv) * a.p.head_stride + e0, x);
+                put(a.v_pages, a.p.kv_dtype, at + (r - Hk) * a.p.head_stride);
             }
         }
     }
@@ -193,6 +185,7 @@ cudaError_t launch_t(const QkArgs& a, cudaStream_t st)
     if (each > kUnroll) each = (each + kUnroll - 1) / kUnroll * kUnroll;
     const int parts = (int)((steps + each - 1) / each);
     const long long warps = (long long)a.p.T * parts;
+    if (warps > 0x7fffffffll) return cudaErrorInvalidValue;
     const unsigned grid = (unsigned)((warps + kQkThreads / 32 - 1) / (kQkThreads / 32));
     if (a.rope.interleaved)
         qk_norm_rope_kernel<T, D, true><<<grid, kQkThreads, 0, st>>>(a, (int)each, parts);

@@ -158,6 +158,8 @@ KERNEL_NAMES = ("screen", "topn", "greedy", "adapt", "reconstruct", "gram", "k6"
 def lib():
     """The loaded CUDA library (raises FadkvLibraryMissing if not built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -173,19 +175,27 @@ def lib():
 
 
 def _addr(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    return t if t is None or type(t) is int else t.data_ptr()
+
+
+_raw_stream = None       # torch's current stream of a device as an integer
 
 
 def _stream(stream, *tensors):
+    global _raw_stream
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
+    if _raw_stream is None:
+        import torch
+        _raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None) or
+                       (lambda d: torch.cuda.current_stream(d).cuda_stream))
+    for t in tensors:
+        if t is not None and type(t) is not int:
+            dev = t.get_device()
+            if dev >= 0:
+                return _raw_stream(dev)
     import torch
-    dev = next((t.device for t in tensors if hasattr(t, "device") and t.device.type == "cuda"), None)
-    return torch.cuda.current_stream(dev).cuda_stream
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _check(func, rc):
