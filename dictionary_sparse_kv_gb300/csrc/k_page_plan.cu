@@ -8,21 +8,29 @@
 // of the step belongs to the request whose prefix of needs holds m, row t to
 // the request whose prefix of rows holds t, and both find it by bisection, so
 // a prompt of thousands of tokens is spread over the threads like thousands
-// of single tokens.  One block scans the requests; it has to read 8 bytes a
-// request and to write 8 bytes a row, so the small calls are latency (one
-// block, one launch) and for many rows a second kernel over the whole grid
-// writes positions and slots.
+// of single tokens.  A page taken from the part of the free list that ended
+// requests return in this very step is read from its old place in the block
+// table, so nothing waits for the list.
+//
+// A call has to read 8 bytes a request and to write 8 bytes a row: always
+// latency.  Few rows: one block does all of it.  Many rows: every block of a
+// grid repeats the scan (cheaper than to wait for one that does it) and takes
+// an even part of the pages and rows; the lengths and the count, which may be
+// updated in place and which every block reads, are written by a last block
+// launched behind the grid.
 #include "paged.cuh"
 
 namespace fadkv {
 namespace {
 
-constexpr int kRowThreads = 256;
-// Rows that the scanning block writes itself, in place of a second launch.
-constexpr int kRowsInPlan = 4096;
-// A block of 128 threads where requests and rows are few: its barriers and
-// scans take less than those of 1024.
+// Rows and requests that one block takes: 128 threads where there are few
+// (barriers and scans take less than those of 1024), else 1024 threads.
 constexpr int kFew = 512;
+constexpr int kOneBlock = 4096;
+constexpr int kGridThreads = 1024;
+constexpr int kGridBlocks = 152;
+
+enum Part { kAll, kGrid, kLast };      // a whole plan; the parts of a plan over a grid
 
 __device__ __forceinline__ int pages_of(int tokens, int shift) { return (int)(((long long)tokens + (1 << shift) - 1) >> shift); }
 
@@ -46,19 +54,23 @@ __device__ __forceinline__ void write_row(const PlanArgs& a, int t, int pos, int
     a.slots[t] = pos >= 0 && page >= 0 && page < a.num_pages ? (page << a.shift) + (pos & ((1 << a.shift) - 1)) : -1;
 }
 
-template <int THREADS>
+template <int THREADS, int PART>
 __global__ void __launch_bounds__(THREADS)
-page_plan_kernel(PlanArgs a, int rows_here)
+page_plan_kernel(PlanArgs a)
 {
     extern __shared__ int sm[];
     int* st = sm;                      // [B + 1] prefix of rows
     int* nd = st + a.B + 1;            // [B + 1] prefix of needed pages
-    int* bk = nd + a.B + 1;            // [B + 1] prefix of returned pages; then the served requests' lengths, -1 otherwise
+    int* bk = nd + a.B + 1;            // [B + 1] prefix of returned pages
+    int* ln = bk + a.B + 1;            // [B] the served requests' lengths, -1 otherwise
     __shared__ int s_taken, s_refused;
     __shared__ long long s_part[3][THREADS / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.B;
+    const int first = PART == kGrid ? blockIdx.x * THREADS + tid : tid;       // pages and rows first, first + step, ...
+    const int step = PART == kGrid ? gridDim.x * THREADS : THREADS;
     const int most = a.max_pages << a.shift;
     const int each = (B + THREADS - 1) / THREADS, b0 = min(B, tid * each), b1 = min(B, b0 + each);
+    if (PART == kGrid) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid == 0) s_taken = s_refused = 0;
 
     auto length = [&](int b) { return min(max(a.lengths[b], 0), most); };
@@ -96,106 +108,106 @@ page_plan_kernel(PlanArgs a, int rows_here)
             total[k] += s_part[k][w];
         }
     }
+    const int returned = (int)min(total[2], (long long)(a.num_pages - count)), F = count + returned;
+    int taken = 0, refused = 0;
     for (int b = b0; b < b1; ++b) {
+        const int len = length(b), add = a.add[b];
+        item(b, v);
+        const bool fits = (long long)len + max(add, 0) <= most && at[0] + v[0] <= a.max_tokens;
+        const bool served = add > 0 && fits && (v[1] == 0 || at[1] + v[1] <= F);
         st[b] = saturate(at[0]);
         nd[b] = saturate(at[1]);
         bk[b] = saturate(at[2]);
-        a.starts[b] = st[b];
-        if (each > 1) item(b, v);
+        ln[b] = served ? len : -1;
+        if (served && v[1] > 0) taken = (int)(at[1] + v[1]);
+        refused += add > 0 && !served;
+        if (PART == kAll || (PART == kGrid && blockIdx.x == 0)) a.starts[b] = st[b];
 #pragma unroll
-        for (int k = 0; k < 3; ++k) at[k] += each > 1 ? v[k] : mine[k];
+        for (int k = 0; k < 3; ++k) at[k] += v[k];
     }
+    if (taken) atomicMax(&s_taken, taken);
+    if (refused) atomicAdd(&s_refused, refused);
     if (tid == 0) {
         st[B] = saturate(total[0]);
         nd[B] = saturate(total[1]);
         bk[B] = saturate(total[2]);
-        a.starts[B] = st[B];
+        if (PART == kAll || (PART == kGrid && blockIdx.x == 0)) a.starts[B] = st[B];
     }
     __syncthreads();
-    const int returned = min(bk[B], a.num_pages - count), F = count + returned;
-    if (returned > 0) {
-        for (int i = tid; i < returned; i += THREADS) {
-            const int b = owner(bk, B, i);
-            a.free_pages[count + i] = a.table[(size_t)b * a.max_pages + i - bk[b]];
+    taken = s_taken;
+
+    if (PART != kLast) {
+        // entry i of the free list after the returns
+        auto entry = [&](int i) {
+            if (i < count) return a.free_pages[i];
+            const int b = owner(bk, B, i - count);
+            return a.table[(size_t)b * a.max_pages + i - count - bk[b]];
+        };
+        for (int i = first; i < returned; i += step) a.free_pages[count + i] = entry(count + i);
+        for (int m = first; m < taken; m += step) {
+            const int b = owner(nd, B, m);
+            a.table[(size_t)b * a.max_pages + pages_of(ln[b], a.shift) + m - nd[b]] = entry(F - 1 - m);
+        }
+        const int T = st[B];
+        for (int t = first; t < a.max_tokens; t += step) {
+            int pos = -1, slot = -1;
+            if (t < T) {
+                const int b = owner(st, B, t);
+                if (ln[b] >= 0) {
+                    pos = ln[b] + t - st[b];
+                    // a page that the request had, or one taken in this step
+                    const int fresh = (pos >> a.shift) - pages_of(ln[b], a.shift);
+                    const int page = fresh >= 0 ? entry(F - 1 - nd[b] - fresh) : a.table[(size_t)b * a.max_pages + (pos >> a.shift)];
+                    if (page >= 0 && page < a.num_pages) slot = (page << a.shift) + (pos & ((1 << a.shift) - 1));
+                }
+            }
+            a.positions[t] = pos;
+            a.slots[t] = slot;
         }
     }
-    if (bk[B] > 0) __syncthreads();                    // the free list is read, and bk written, below
+    if (PART == kGrid) return;
+    // nothing of the grid reads the lengths and the count any more
+    if (PART == kLast) asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int b = b0; b < b1; ++b) {
         const int len = length(b), add = a.add[b];
-        const bool served = add > 0 && (long long)len + add <= most && st[b + 1] <= a.max_tokens &&
-                            (nd[b + 1] == nd[b] || nd[b + 1] <= F);
-        a.lengths_out[b] = add < 0 ? 0 : (served ? len + add : len);
-        if (served && nd[b + 1] > nd[b]) atomicMax(&s_taken, nd[b + 1]);
-        if (add > 0 && !served) atomicAdd(&s_refused, 1);
-        if (!rows_here && add > 0 && st[b] < a.max_tokens) a.positions[st[b]] = served ? len : -1;
-        bk[b] = served ? len : -1;
-    }
-    __syncthreads();
-    const int taken = s_taken;
-    for (int m = tid; m < taken; m += THREADS) {
-        const int b = owner(nd, B, m);
-        a.table[(size_t)b * a.max_pages + pages_of(bk[b], a.shift) + m - nd[b]] = a.free_pages[F - 1 - m];
+        a.lengths_out[b] = add < 0 ? 0 : (ln[b] >= 0 ? len + add : len);
     }
     if (tid == 0) {
         *a.free_count_out = F - taken;
         *a.refused = s_refused;
     }
-    if (!rows_here) return;
-    // a row's page: one that the request had, or one taken above (from the free list: the table entry may be on its way)
-    const int T = st[B];
-    for (int t = tid; t < a.max_tokens; t += THREADS) {
-        int pos = -1, page = -1;
-        if (t < T) {
-            const int b = owner(st, B, t);
-            if (bk[b] >= 0) {
-                pos = bk[b] + t - st[b];
-                const int fresh = (pos >> a.shift) - pages_of(bk[b], a.shift);
-                page = fresh >= 0 ? a.free_pages[F - 1 - nd[b] - fresh] : a.table[(size_t)b * a.max_pages + (pos >> a.shift)];
-            }
-        }
-        write_row(a, t, pos, page);
-    }
 }
 
-// Rows over the whole grid.  The first row of each request holds its first
-// position already (-1 if refused); the thread of that row writes the same
-// value again.
-__global__ void __launch_bounds__(kRowThreads)
-page_rows_kernel(PlanArgs a)
+template <int THREADS, int PART>
+cudaError_t allow_smem(size_t smem)
 {
-    pdl_begin();
-    const int t = blockIdx.x * kRowThreads + threadIdx.x;
-    if (t >= a.max_tokens) return;
-    int pos = -1, page = -1;
-    if (t < a.starts[a.B]) {
-        const int b = owner(a.starts, a.B, t), s = a.starts[b], first = a.positions[s];
-        if (first >= 0) {
-            pos = first + t - s;
-            page = a.table[(size_t)b * a.max_pages + (pos >> a.shift)];
-        }
-    }
-    write_row(a, t, pos, page);
+    if (smem <= 48 * 1024) return cudaSuccess;
+    return cudaFuncSetAttribute(page_plan_kernel<THREADS, PART>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
 }
 
 }  // namespace
 
 cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t st)
 {
-    const size_t smem = (size_t)3 * (a.B + 1) * sizeof(int);
-    const int rows_here = a.max_tokens <= kRowsInPlan;
-    cudaError_t e = cudaSuccess;
+    const size_t smem = (size_t)(4 * a.B + 3) * sizeof(int);
     if (a.B <= kFew && a.max_tokens <= kFew) {
-        page_plan_kernel<128><<<1, 128, smem, st>>>(a, rows_here);
-    } else {
-        if (smem > 48 * 1024)
-            e = cudaFuncSetAttribute(page_plan_kernel<1024>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-        page_plan_kernel<1024><<<1, 1024, smem, st>>>(a, rows_here);
+        page_plan_kernel<128, kAll><<<1, 128, smem, st>>>(a);
+        return cudaGetLastError();
     }
+    if (a.max_tokens <= kOneBlock) {
+        const cudaError_t e = allow_smem<1024, kAll>(smem);
+        if (e != cudaSuccess) return e;
+        page_plan_kernel<1024, kAll><<<1, 1024, smem, st>>>(a);
+        return cudaGetLastError();
+    }
+    cudaError_t e = allow_smem<kGridThreads, kGrid>(smem);
+    if (e == cudaSuccess) e = allow_smem<1024, kLast>(smem);
+    if (e != cudaSuccess) return e;
+    const int blocks = (a.max_tokens + kGridThreads - 1) / kGridThreads;
+    page_plan_kernel<kGridThreads, kGrid><<<blocks < kGridBlocks ? blocks : kGridBlocks, kGridThreads, smem, st>>>(a);
     e = cudaGetLastError();
-    if (e != cudaSuccess || rows_here) return e;
-    return launch_pdl(page_rows_kernel, dim3((unsigned)((a.max_tokens + kRowThreads - 1) / kRowThreads)),
-                      dim3(kRowThreads), 0, st, a);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(page_plan_kernel<1024, kLast>, dim3(1), dim3(1024), smem, st, a);
 }
 
 }  // namespace fadkv

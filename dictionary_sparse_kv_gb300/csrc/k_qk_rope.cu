@@ -15,13 +15,14 @@
 // (i, i + rotary_dim / 2) the two groups are partners, with neighbouring pairs
 // they are side by side, so a pair is always in one lane, nothing is
 // exchanged, and four angles a lane, worked out once a warp for all the rows
-// of its token, do for both layouts.
+// of its token, do for both layouts.  1 / sqrt goes into the cosines and
+// sines, and products run two values an instruction.
 #include "paged.cuh"
 
 namespace fadkv {
 namespace {
 
-constexpr int kQkThreads = 256;
+constexpr int kQkThreads = 128;
 constexpr int kUnroll = 4;       // rows in flight a lane
 
 // Four consecutive elements as loaded.
@@ -57,6 +58,11 @@ template <typename T, int D, bool PAIRS>
 __global__ void __launch_bounds__(kQkThreads)
 qk_norm_rope_kernel(const __grid_constant__ QkArgs a, int each, int parts)
 {
+    using paged::add2;
+    using paged::fma2;
+    using paged::mul2;
+    using paged::pair;
+    using paged::unpair;
     constexpr int LPR = D / 8;            // lanes per row
     constexpr int RPW = 32 / LPR;         // rows per warp step
     __shared__ unsigned long long turns[FADKV_ROPE_MAX_PAIRS];
@@ -68,7 +74,6 @@ qk_norm_rope_kernel(const __grid_constant__ QkArgs a, int each, int parts)
     const int t = (int)(w / (unsigned int)parts), part = (int)(w % (unsigned int)parts);
     if (t >= a.p.T) return;
     const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
-    const int Hq = a.p.Hq, Hk = Hq + a.p.Hkv, rows = Hk + a.p.Hkv;   // rows: queries, keys, values
     const int pos = a.positions[t];
     const int slot = a.slots ? a.slots[t] : -1;
     const bool append = pos >= 0 && slot >= 0 && (slot >> a.shift) < a.p.num_pages;
@@ -78,96 +83,131 @@ qk_norm_rope_kernel(const __grid_constant__ QkArgs a, int each, int parts)
     // this lane's two groups: the first rd / 8 lanes of a row take the rotated part
     const bool turned = l < rd / 8;
     const int e0 = PAIRS || !turned ? l * 8 : l * 4, e1 = PAIRS || !turned ? e0 + 4 : e0 + half;
-    float cs[4], sn[4];
-    if (turned) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const unsigned long long phase = (unsigned long long)(long long)pos * turns[l * 4 + k];
-            sincospif((float)(int)(phase >> 32) * 0x1p-31f, &sn[k], &cs[k]);
-            cs[k] *= a.rope.amplitude;
-            sn[k] *= a.rope.amplitude;
+    // Eight values as four pairs of registers: the first members of the pairs that turn, x[0] and x[1], and the second,
+    // x[2] and x[3].
+    auto pack8 = [](const Raw4<T> (&r)[2], uint64_t (&x)[4]) {
+        float f[8];
+        r[0].get(f);
+        r[1].get(f + 4);
+        if (PAIRS) {
+            x[0] = pair(f[0], f[2]), x[1] = pair(f[4], f[6]);
+            x[2] = pair(f[1], f[3]), x[3] = pair(f[5], f[7]);
+        } else {
+            x[0] = pair(f[0], f[1]), x[1] = pair(f[2], f[3]);
+            x[2] = pair(f[4], f[5]), x[3] = pair(f[6], f[7]);
         }
-    }
-    const bool norm = a.wq || a.wk;
-    float wq[8], wk[8];
-    if (a.wq) {
-        Raw4<T> r[2];
-        r[0].load((const T*)a.wq + e0), r[1].load((const T*)a.wq + e1);
-        r[0].get(wq), r[1].get(wq + 4);
-    }
-    if (a.wk) {
-        Raw4<T> r[2];
-        r[0].load((const T*)a.wk + e0), r[1].load((const T*)a.wk + e1);
-        r[0].get(wk), r[1].get(wk + 4);
+    };
+    auto put = [&](void* base, int dtype, long long row, const uint64_t (&x)[4]) {
+        float f[8];
+        if (PAIRS) {
+            unpair(x[0], f[0], f[2]), unpair(x[1], f[4], f[6]);
+            unpair(x[2], f[1], f[3]), unpair(x[3], f[5], f[7]);
+        } else {
+            unpair(x[0], f[0], f[1]), unpair(x[1], f[2], f[3]);
+            unpair(x[2], f[4], f[5]), unpair(x[3], f[6], f[7]);
+        }
+        store4(base, dtype, row + e0, f);
+        store4(base, dtype, row + e1, f + 4);
+    };
+    // cosines and sines of the four pairs; 1 and 0 where nothing turns (there amplitude does not enter either)
+    uint64_t cs[2], sn[2], ns[2];
+    {
+        float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
+        if (turned) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const unsigned long long phase = (unsigned long long)(long long)pos * turns[l * 4 + k];
+                sincospif((float)(int)(phase >> 32) * 0x1p-31f, &s[k], &c[k]);
+                c[k] *= a.rope.amplitude;
+                s[k] *= a.rope.amplitude;
+            }
+        }
+        cs[0] = pair(c[0], c[1]), cs[1] = pair(c[2], c[3]);
+        sn[0] = pair(s[0], s[1]), sn[1] = pair(s[2], s[3]);
+        ns[0] = pair(-s[0], -s[1]), ns[1] = pair(-s[2], -s[3]);
     }
 
-    const T* q = (const T*)a.q + t * a.p.q_stride;
-    const T* k = (const T*)a.k + t * a.p.k_stride;
-    const T* v = (const T*)a.v + t * a.p.v_stride;
-    const int last = min(rows, (part + 1) * each * RPW);
-    for (int r0 = part * each * RPW; r0 < last; r0 += RPW * kUnroll) {
+    // steps of RPW rows: queries, then keys, then values; this warp's from `begin` on, `count` of them
+    const int q_steps = (a.p.Hq + RPW - 1) / RPW, kv_steps = (a.p.Hkv + RPW - 1) / RPW;
+    const int begin = part * each, end = min(q_steps + 2 * kv_steps, begin + each);
+
+    auto rotated = [&](const T* src, const T* weight, int rows, int s0, int s1, auto&& store) {
+        uint64_t wt[4];
+        if (weight) {
+            Raw4<T> r[2];
+            r[0].load(weight + e0), r[1].load(weight + e1);
+            pack8(r, wt);
+        }
+        for (int s = s0; s < s1; s += kUnroll) {
+            Raw4<T> raw[kUnroll][2];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                const T* p = src + (size_t)min((s + u) * RPW + sub, rows - 1) * D;
+                raw[u][0].load(p + e0);
+                raw[u][1].load(p + e1);
+            }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                if (s + u >= s1) break;
+                const int h = (s + u) * RPW + sub;
+                uint64_t x[4], c[2] = {cs[0], cs[1]}, sp[2] = {sn[0], sn[1]}, sm[2] = {ns[0], ns[1]};
+                pack8(raw[u], x);
+                if (weight) {
+                    float s0f, s1f;
+                    unpair(add2(fma2(x[0], x[0], mul2(x[1], x[1])), fma2(x[2], x[2], mul2(x[3], x[3]))), s0f, s1f);
+                    float ss = s0f + s1f;
+#pragma unroll
+                    for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                    const float inv = rsqrtf(ss * (1.f / D) + a.p.eps);
+                    const uint64_t inv2 = pair(inv, inv);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = mul2(x[i], wt[i]);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) c[i] = mul2(c[i], inv2), sp[i] = mul2(sp[i], inv2), sm[i] = mul2(sm[i], inv2);
+                }
+                uint64_t y[4];
+                if (turned) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        y[i] = fma2(x[i], c[i], mul2(x[i + 2], sm[i]));
+                        y[i + 2] = fma2(x[i], sp[i], mul2(x[i + 2], c[i]));
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[i] = mul2(x[i], c[i & 1]);
+                }
+                if (pos < 0) y[0] = y[1] = y[2] = y[3] = 0ull;
+                if (h < rows) store(h, y);
+            }
+        }
+    };
+    if (begin < q_steps)
+        rotated((const T*)a.q + t * a.p.q_stride, (const T*)a.wq, a.p.Hq, begin, min(end, q_steps),
+                [&](int h, const uint64_t (&y)[4]) { put(a.q_out, a.p.q_dtype, ((long long)t * a.p.Hq + h) * D, y); });
+    const int k0 = max(begin - q_steps, 0), k1 = min(end - q_steps, kv_steps);
+    if (k0 < k1)
+        rotated((const T*)a.k + t * a.p.k_stride, (const T*)a.wk, a.p.Hkv, k0, k1, [&](int h, const uint64_t (&y)[4]) {
+            if (a.k_out) put(a.k_out, a.p.kv_dtype, ((long long)t * a.p.Hkv + h) * D, y);
+            if (append) put(a.k_pages, a.p.kv_dtype, at + h * a.p.head_stride, y);
+        });
+    if (!append) return;
+    const int v0 = max(begin - q_steps - kv_steps, 0), v1 = end - q_steps - kv_steps;
+    for (int s = v0; s < v1; s += kUnroll) {
         Raw4<T> raw[kUnroll][2];
+        const T* v = (const T*)a.v + t * a.p.v_stride;
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int r = min(r0 + u * RPW + sub, rows - 1);
-            const T* p = r < Hq ? q + r * D : r < Hk ? k + (r - Hq) * D : v + (r - Hk) * D;
+            const T* p = v + (size_t)min((s + u) * RPW + sub, a.p.Hkv - 1) * D;
             raw[u][0].load(p + e0);
             raw[u][1].load(p + e1);
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            if (r0 + u * RPW >= last) break;
-            const int r = r0 + u * RPW + sub;
-            float x[8];
-            raw[u][0].get(x);
-            raw[u][1].get(x + 4);
-            const bool is_q = r < Hq;
-            if (r0 + u * RPW < Hk) {                       // not values alone
-                const bool is_v = r >= Hk;
-                if (norm) {
-                    float s0 = 0.f, s1 = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        s0 = fmaf(x[i], x[i], s0);
-                        s1 = fmaf(x[i + 4], x[i + 4], s1);
-                    }
-                    float ss = s0 + s1;
-#pragma unroll
-                    for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                    const float inv = rsqrtf(ss * (1.f / D) + a.p.eps);
-                    if (is_q ? a.wq != nullptr : (!is_v && a.wk != nullptr)) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] *= inv * (is_q ? wq[i] : wk[i]);
-                    }
-                }
-                if (turned && !is_v) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float& p0 = PAIRS ? x[2 * i] : x[i];
-                        float& p1 = PAIRS ? x[2 * i + 1] : x[i + 4];
-                        const float c = p0 * cs[i] - p1 * sn[i];
-                        p1 = p0 * sn[i] + p1 * cs[i];
-                        p0 = c;
-                    }
-                }
-                if (!is_v && pos < 0)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = 0.f;
-            }
-            if (r >= last) continue;
-            auto put = [&](void* base, int dtype, long long row) {
-                store4(base, dtype, row + e0, x);
-                store4(base, dtype, row + e1, x + 4);
-            };
-            if (is_q) {
-                put(a.q_out, a.p.q_dtype, ((long long)t * Hq + r) * D);
-            } else if (r < Hk) {
-                const int h = r - Hq;
-                if (a.k_out) put(a.k_out, a.p.kv_dtype, ((long long)t * a.p.Hkv + h) * D);
-                if (append) put(a.k_pages, a.p.kv_dtype, at + h * a.p.head_stride);
-            } else if (append) {
-                put(a.v_pages, a.p.kv_dtype, at + (r - Hk) * a.p.head_stride);
-            }
+            const int h = (s + u) * RPW + sub;
+            if (s + u >= v1 || h >= a.p.Hkv) break;
+            uint64_t x[4];
+            pack8(raw[u], x);
+            put(a.v_pages, a.p.kv_dtype, at + h * a.p.head_stride, x);
         }
     }
 }
@@ -176,13 +216,12 @@ template <typename T, int D>
 cudaError_t launch_t(const QkArgs& a, cudaStream_t st)
 {
     constexpr int RPW = 32 / (D / 8);
-    const long long steps = (a.p.Hq + 2 * a.p.Hkv + RPW - 1) / RPW;
+    const long long steps = (a.p.Hq + RPW - 1) / RPW + 2 * ((a.p.Hkv + RPW - 1) / RPW);
     // warp steps a warp takes: one while the warps do not fill the GPU (152
     // multiprocessors of 64 warps), then up to a whole token, so that the
     // angles are worked out as few times as that allows
     long long each = (long long)a.p.T * steps / (152 * 64);
     each = each < 1 ? 1 : each > steps ? steps : each;
-    if (each > kUnroll) each = (each + kUnroll - 1) / kUnroll * kUnroll;
     const int parts = (int)((steps + each - 1) / each);
     const long long warps = (long long)a.p.T * parts;
     if (warps > 0x7fffffffll) return cudaErrorInvalidValue;

@@ -400,7 +400,7 @@ fadkv_status fadkv_attend_workspace_bytes(const fadkv_attn_params* params, size_
    of the block table [B][max_pages] int32 lists the pages of request b in
    token order.  The slot of a token is page * page_size + token in page.
    --------------------------------------------------------------------------- */
-#define FADKV_MAX_REQUESTS 16384   /* largest B of the paged-cache calls */
+#define FADKV_MAX_REQUESTS 12288   /* largest B of the paged-cache calls */
 
 typedef struct {
     int32_t B;            /* requests, 0 .. FADKV_MAX_REQUESTS */

@@ -46,7 +46,7 @@ def test_page_plan_refusals(L, monkeypatch):
         F.page_plan(F.page_params(**{**ok, **kw}), *(ptrs or [FAKE] * 11), stream=0)
     for kw, status in ((dict(B=-1), 1), (dict(num_pages=-1), 1), (dict(max_pages=0), 1), (dict(max_tokens=-1), 1),
                        (dict(page_size=12), 2), (dict(page_size=4), 2), (dict(page_size=2048), 2),
-                       (dict(B=16385), 2), (dict(num_pages=2 ** 28), 2), (dict(max_pages=2 ** 28), 2)):
+                       (dict(B=12289), 2), (dict(num_pages=2 ** 28), 2), (dict(max_pages=2 ** 28), 2)):
         assert _status(call, **kw) == status, kw
     for i in range(11):
         assert _status(call, ptrs=[FAKE] * i + [None] + [FAKE] * (10 - i)) == 1
@@ -122,7 +122,7 @@ BAD_PAGED = [(dict(B=-1), 1), (dict(T=-1), 1), (dict(Hq=25), 1), (dict(Hkv=0), 1
              (dict(dtype=5), 1), (dict(page_size=20), 2), (dict(num_pages=-2), 1), (dict(max_pages=0), 1),
              (dict(max_pages=2 ** 28), 2), (dict(window=-1), 1), (dict(sinks=-1), 1), (dict(scale=math.nan), 1),
              (dict(q_stride=100), 1), (dict(out_stride=24 * 128 + 4), 1), (dict(head_stride=0), 1),
-             (dict(B=16385, T=16385), 2)]
+             (dict(B=12289, T=12289), 2)]
 
 
 @pytest.mark.parametrize("prefill", [False, True])
