@@ -36,6 +36,11 @@
 // while the last tiles of the current one are worked on; only the reading of
 // O by the softmax warps stands between two items' products.
 //
+// Where the items are fewer than the multiprocessors (a short chunk on a long
+// cache) each is cut along its keys into as many pieces as fill them twice; the
+// pieces' sums go to the workspace, and a second kernel joins them as
+//   m = max m_i,  l = sum 2^(m_i - m) l_i,  o = sum 2^(m_i - m) o_i.
+//
 // Warps: 0 TMA, 1 MMA, 2 TMEM and the items, 4..7 and 8..11 softmax of the two
 // tiles (3 only makes the count whole).  Every wait is bounded; one that runs out sets
 // FADKV_DEV_TIMEOUT in the workspace's first word, and the CTA drains and
@@ -58,6 +63,23 @@ constexpr float kGrow = 8.f;                       // growth of the maximum (log
 
 constexpr int kPreCtas = 152;                      // one per multiprocessor
 constexpr int kItemReaders = 10;                   // warps that read an item
+
+// Pieces of an item: at most so many, and none shorter than so many key tiles
+// (a piece costs about two tiles' time to begin, write out and join).
+constexpr int kMaxParts = 64;
+constexpr int kLeastTiles = 4;
+constexpr int kSplitSlots = 2 * kPreCtas;          // pieces of all items where items are cut
+
+// Head of the workspace.
+struct PreHead {
+    unsigned long long status;
+    unsigned int taken, left;                      // pieces handed out, CTAs that are done: zero between calls
+    int parts, items;                              // of this call, for the join
+    struct { int row0, nt, head0, hn; } item[kPreCtas];
+};
+constexpr size_t kHeadBytes = 4096;
+static_assert(sizeof(PreHead) <= kHeadBytes, "workspace head");
+__host__ __device__ constexpr size_t slot_floats(int d) { return (size_t)kRows * (d + 2); }   // a tile's rows: o by column, m, l
 
 template <int D> struct PreCfg {
     static constexpr int NST = D == 128 ? 5 : 8;   // stages of the K / V ring
@@ -82,6 +104,7 @@ struct Item {
     int row0, nt;              // first row of q, tokens
     int first, len;            // position of the first row; tokens of the request
     int b, head0, hk, hn;      // request, first query head, KV head, query heads
+    int index, piece, parts;   // number of the item; which part of its key tiles
 };
 
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w, uint32_t bar)
@@ -155,7 +178,7 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 
 // The key tiles of an item: those of the first tokens, then those of the
 // window (or all).
 struct Tiles {
-    int first, last, W, S, from, sinks, count;
+    int first, last, W, S, from, sinks, lo, count;     // count tiles from number lo on
     __device__ __forceinline__ Tiles(const Item& it, const PagedArgs& a)
     {
         first = it.first;
@@ -166,8 +189,17 @@ struct Tiles {
         from = W > 0 ? max(0, first - W + 1) / kKeys : 0;
         sinks = W > 0 ? min(from, (S + kKeys - 1) / kKeys) : 0;
         count = to > from ? sinks + to - from : 0;
+        lo = 0;
+        if (it.parts > 1) {
+            lo = count * it.piece / it.parts;
+            count = count * (it.piece + 1) / it.parts - lo;
+        }
     }
-    __device__ __forceinline__ int key0(int i) const { return (i < sinks ? i : i - sinks + from) * kKeys; }
+    __device__ __forceinline__ int key0(int i) const
+    {
+        i += lo;
+        return (i < sinks ? i : i - sinks + from) * kKeys;
+    }
     // whether some row of the item sees a key; whether a tile holds keys that none sees
     __device__ __forceinline__ bool seen(int key) const { return key <= last && (W == 0 || key > first - W || key < S); }
     __device__ __forceinline__ bool ragged(int k0) const
@@ -213,8 +245,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     auto qempty = [&](int q) { return bar(10 + q); };
     auto pfull = [&](int q, int part) { return bar(12 + 2 * q + part); };
     const uint32_t ifull = bar(16), iempty = bar(17);
-    unsigned long long* status = reinterpret_cast<unsigned long long*>(a.ws);
-    unsigned int* counter = reinterpret_cast<unsigned int*>(a.ws) + 2;   // items handed out; CTAs that are done
+    PreHead* head = reinterpret_cast<PreHead*>(a.ws);
+    unsigned long long* status = &head->status;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int grp = a.grp;
@@ -495,19 +527,57 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 if (lane >= o) upto += y;
             }
         };
+        Item it;
+        // the item of the request's rows t0 .. t0 + nt - 1
+        auto rows_of = [&](int b, int s0, int rows_all, int t0, int nt) {
+            it.b = b;
+            it.row0 = s0 + t0;
+            it.nt = nt;
+            it.len = clamp_len(__ldg(a.lengths + b), a);
+            // positions by the rows that the request has, those cut off at T included
+            it.first = it.len - rows_all + t0;
+        };
+        unsigned int parts = 1;
+        if (a.split) {
+            // every CTA comes to the same number of parts
+            long long items = 0;
+            int longest = 0;
+            for (;; hi -= 32) {
+                look();
+                items += __shfl_sync(0xffffffffu, upto, 31);
+                if (cnt > 0) {
+                    const int t0 = (cnt - 1) / per_item * per_item;
+                    it.parts = 1;
+                    rows_of(hi - lane, start, all, t0, cnt - t0);
+                    longest = max(longest, Tiles(it, a).count);
+                }
+                if (hi < 32) break;
+            }
+            hi = a.p.B - 1;
+            items *= heads;
+            for (int o = 16; o > 0; o >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
+            if (items > 0 && items <= kPreCtas)
+                parts = (unsigned int)max(1, min(min(kMaxParts, longest / kLeastTiles), kSplitSlots / (int)items));
+            if (blockIdx.x == 0 && lane == 0) {
+                head->parts = (int)parts;
+                head->items = (int)min(items, (long long)kPreCtas);
+            }
+        }
         look();
         for (int n = 0; ok; ++n) {
             unsigned int x = 0;
-            if (lane == 0) x = atomicAdd(counter, 1u);
+            if (lane == 0) x = atomicAdd(&head->taken, 1u);
             x = __shfl_sync(0xffffffffu, x, 0);
-            const long long u = x / (unsigned int)heads;
-            const int head = (int)(x % (unsigned int)heads);
+            it.parts = (int)parts;
+            it.piece = (int)(x % parts);
+            it.index = (int)(x / parts);
+            const long long u = it.index / heads;
+            const int kvh = it.index % heads;
             while (hi >= 0 && u >= base + __shfl_sync(0xffffffffu, upto, 31)) {
                 base += __shfl_sync(0xffffffffu, upto, 31);
                 hi -= 32;
                 look();
             }
-            Item it;
             it.live = hi >= 0;
             const int at = hi >= 0 ? __ffs(__ballot_sync(0xffffffffu, base + upto > u)) - 1 : 0;   // the lane whose request it is
             const int t_end = (int)(base + __shfl_sync(0xffffffffu, upto, at) - u);                // tiles from this one to the request's first, this one included
@@ -515,18 +585,19 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             const int s0 = __shfl_sync(0xffffffffu, start, at);
             if (it.live) {
                 const int t0 = (t_end - 1) * per_item;
-                it.b = hi - at;
-                it.row0 = s0 + t0;
-                it.nt = min(per_item, rows - t0);
-                it.len = clamp_len(__ldg(a.lengths + it.b), a);
-                // positions by the rows that the request has, those cut off at T included
-                it.first = it.len - rows_all + t0;
-                it.hk = head / chunks;
-                const int h0 = (head % chunks) * gch;
+                rows_of(hi - at, s0, rows_all, t0, min(per_item, rows - t0));
+                it.hk = kvh / chunks;
+                const int h0 = (kvh % chunks) * gch;
                 it.head0 = it.hk * grp + h0;
                 it.hn = min(gch, grp - h0);
             }
             if (lane == 0) {
+                if (it.live && it.parts > 1 && it.piece == 0) {
+                    head->item[it.index].row0 = it.row0;
+                    head->item[it.index].nt = it.nt;
+                    head->item[it.index].head0 = it.head0;
+                    head->item[it.index].hn = it.hn;
+                }
                 s_item = it;
                 mbar_arrive(ifull);
             }
@@ -536,9 +607,9 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         // the last CTA to stop leaves the counters at zero for the next call
         if (lane == 0) {
             __threadfence();
-            if (atomicAdd(counter + 1, 1u) == gridDim.x - 1) {
-                counter[0] = 0u;
-                counter[1] = 0u;
+            if (atomicAdd(&head->left, 1u) == gridDim.x - 1) {
+                head->taken = 0u;
+                head->left = 0u;
             }
         }
     } else if (warp == 3) {
@@ -664,6 +735,28 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 fence_after();
             }
             if (!ok) break;
+            if (it.parts > 1) {
+                // a piece: its sums, column by column, a lane a row
+                float* part = reinterpret_cast<float*>((unsigned char*)a.ws + kHeadBytes) +
+                              ((size_t)(it.index * it.parts + it.piece) * a.split + q) * slot_floats(D) + r;
+                part[(size_t)D * kRows] = tiles > 0 ? m : -INFINITY;
+                part[(size_t)(D + 1) * kRows] = l;
+                if (tiles > 0) {
+                    const bool any = __any_sync(0xffffffffu, live);
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(lanes + C::O(q) + c * 32, o);
+                        if (any)
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) part[(size_t)(c * 32 + j) * kRows] = __uint_as_float(o[j]);
+                    }
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(ofree(q));
+                }
+                continue;
+            }
             const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
             if (live && a.lse)
                 a.lse[(size_t)(it.row0 + t) * a.p.Hq + it.head0 + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
@@ -722,6 +815,48 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     }
 }
 
+// Joins the pieces of cut items: a block takes 8 columns of a tile's 128 rows.
+template <typename T, int D>
+__global__ void __launch_bounds__(kRows)
+paged_prefill_join_kernel(const __grid_constant__ PagedArgs a)
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const PreHead* head = reinterpret_cast<const PreHead*>(a.ws);
+    const int parts = head->parts, item = blockIdx.x / a.split, q = blockIdx.x % a.split;
+    if (parts <= 1 || item >= head->items) return;
+    const int gch = min(a.grp, kRows), tq = kRows / gch, r = threadIdx.x, t = q * tq + r / gch, h = r % gch;
+    const int row0 = head->item[item].row0, head0 = head->item[item].head0;
+    if (r / gch >= tq || t >= head->item[item].nt || h >= head->item[item].hn) return;
+    if (row0 < 0 || row0 + t >= a.p.T || head0 < 0 || head0 + h >= a.p.Hq) return;   // (after a wait that ran out)
+    const size_t step = slot_floats(D) * a.split;
+    const float* part = reinterpret_cast<const float*>((const unsigned char*)a.ws + kHeadBytes) +
+                        ((size_t)item * parts * a.split + q) * slot_floats(D) + r;
+    const int c0 = blockIdx.y * 8;
+    float m = -INFINITY, l = 0.f, o[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = 0.f;
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) m = fmaxf(m, part[p * step + (size_t)D * kRows]);
+#pragma unroll 4
+    for (int p = 0; p < parts; ++p) {
+        const float pm = part[p * step + (size_t)D * kRows], pl = part[p * step + (size_t)(D + 1) * kRows];
+        const float f = pm == -INFINITY ? 0.f : exp2_fast(pm - m);
+        // a piece that saw nothing may have left its columns unwritten
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float v = part[p * step + (size_t)(c0 + j) * kRows];
+            o[j] = f > 0.f ? fmaf(f, v, o[j]) : o[j];
+        }
+        l = f > 0.f ? fmaf(f, pl, l) : (pl == pl ? l : pl);
+    }
+    const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
+    const size_t row = (size_t)row0 + t, hd = (size_t)head0 + h;
+    *reinterpret_cast<uint4*>((T*)a.out + row * a.p.out_stride + hd * D + c0) =
+        make_uint4(Num<T>::pack(o[0] * inv, o[1] * inv), Num<T>::pack(o[2] * inv, o[3] * inv),
+                   Num<T>::pack(o[4] * inv, o[5] * inv), Num<T>::pack(o[6] * inv, o[7] * inv));
+    if (c0 == 0 && a.lse) a.lse[row * a.p.Hq + hd] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
 // A pool as (element, token in page, head, page), boxes of 64 elements by up
 // to 128 tokens of one page and head.
 bool pool_map(CUtensorMap* map, const void* base, const PagedArgs& a)
@@ -755,25 +890,56 @@ bool query_map(CUtensorMap* map, const PagedArgs& a, int heads, int tokens)
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+struct PreShape {
+    int gch, chunks, tq;       // heads of a tile, tiles a KV head's group takes, tokens of a tile
+    long long items;           // at most
+    int split;                 // 0: items are not cut; else the tiles of an item that can hold rows
+};
+
+PreShape pre_shape(const fadkv_paged_params& p)
+{
+    PreShape s;
+    const int grp = p.Hq / p.Hkv;
+    s.gch = grp < kRows ? grp : kRows;
+    s.chunks = (grp + s.gch - 1) / s.gch;
+    s.tq = kRows / s.gch;
+    const long long heads = (long long)p.Hkv * s.chunks, tiles = p.T / (2 * s.tq);
+    s.items = (tiles + (p.B < p.T ? p.B : p.T)) * heads;           // one more a request than its rows fill
+    // Cutting can pay only if the rows fill fewer items than there are multiprocessors, however they are spread over
+    // requests, and if there can be keys for two pieces.  How many pieces there are is decided on the device.
+    long long most = (long long)p.max_pages * p.page_size;
+    if (p.window > 0) most = most < (long long)p.window + p.sinks + 2 * kKeys ? most : (long long)p.window + p.sinks + 2 * kKeys;
+    const bool cut = p.B <= 256 && (tiles + 1) * heads <= kPreCtas && most >= 2 * kLeastTiles * kKeys;
+    s.split = !cut ? 0 : (p.T <= s.tq ? 1 : 2);
+    return s;
+}
+
 template <typename T, int D>
-cudaError_t launch_t(const PagedArgs& a, cudaStream_t st)
+cudaError_t launch_t(const PagedArgs& args, cudaStream_t st)
 {
     auto k = paged_prefill_kernel<T, D>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, PreCfg<D>::alloc);
     if (e != cudaSuccess) return e;
-    const int gch = a.grp < kRows ? a.grp : kRows, chunks = (a.grp + gch - 1) / gch, tq = kRows / gch;
+    PagedArgs a = args;
+    const PreShape s = pre_shape(a.p);
+    a.split = s.split;
     CUtensorMap mq, mk, mv;
-    if (!query_map(&mq, a, gch, tq) || !pool_map(&mk, a.k, a) || !pool_map(&mv, a.v, a)) return cudaErrorInvalidValue;
-    // at most one item a request more than the rows fill
-    const long long items = ((long long)a.p.T / (2 * tq) + a.p.B) * a.p.Hkv * chunks;
-    if (items > 0x7fffffffll) return cudaErrorInvalidValue;
-    k<<<(unsigned)(items < kPreCtas ? items : kPreCtas), kPreThreads, PreCfg<D>::alloc, st>>>(mq, mk, mv, a);
-    return cudaGetLastError();
+    if (!query_map(&mq, a, s.gch, s.tq) || !pool_map(&mk, a.k, a) || !pool_map(&mv, a.v, a)) return cudaErrorInvalidValue;
+    if (s.items > 0x7fffffffll) return cudaErrorInvalidValue;
+    const int ctas = s.split || s.items > kPreCtas ? kPreCtas : (int)s.items;
+    k<<<ctas, kPreThreads, PreCfg<D>::alloc, st>>>(mq, mk, mv, a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !s.split) return e;
+    const int items = (int)(s.items < kPreCtas ? s.items : kPreCtas);
+    return launch_pdl(paged_prefill_join_kernel<T, D>, dim3(items * s.split, D / 8), dim3(kRows), 0, st, a);
 }
 
 }  // namespace
 
-size_t paged_prefill_workspace(const fadkv_paged_params&) { return 256; }
+size_t paged_prefill_workspace(const fadkv_paged_params& p)
+{
+    return kHeadBytes + (size_t)kSplitSlots * pre_shape(p).split * slot_floats(p.d) * sizeof(float);
+}
 
 cudaError_t launch_paged_prefill(const PagedArgs& a, cudaStream_t st)
 {

@@ -45,6 +45,7 @@ cudaError_t launch_qk_norm_rope(const QkArgs& a, cudaStream_t st);
 struct PagedArgs {
     fadkv_paged_params p;
     int shift, grp;           // page_size = 1 << shift; query heads per KV head
+    int split;                // prefill: whether items may be cut along their keys (the launcher sets it)
     float scale_log2;         // scale * log2(e): scores in units of powers of two
     const void* k;
     const void* v;

@@ -76,6 +76,7 @@ PagedArgs paged_args(const fadkv_paged_params& p, const void* k, const void* v, 
     a.p = p;
     a.shift = log2_exact(p.page_size);
     a.grp = p.Hq / p.Hkv;
+    a.split = 0;
     a.scale_log2 = p.scale * 1.44269504088896f;
     a.k = k;
     a.v = v;

@@ -364,6 +364,15 @@ PREFILLS = [
          bad_pages=[(0, 0, -1), (0, 3, 10 ** 6), (2, 0, -5)]),
     dict(lens=[30 + i for i in range(140)], new=[1 + i % 5 for i in range(140)], Hq=2, Hkv=1, d=64, dt="f16", ps=16),
     dict(lens=[1500], new=[600], Hq=2, Hkv=1, d=128, dt="bf16", ps=256),
+    # few rows on many keys: cut along the keys
+    dict(lens=[3000], new=[5], Hq=6, Hkv=2, d=128, dt="f16", ps=16),
+    dict(lens=[3000, 100, 0, 2100], new=[40, 7, 0, 90], Hq=4, Hkv=2, d=64, dt="bf16", ps=32, layout="token"),
+    dict(lens=[5000], new=[1], Hq=2, Hkv=2, d=128, dt="bf16", ps=64),
+    dict(lens=[4000, 1100], new=[70, 33], Hq=3, Hkv=1, d=128, dt="f16", ps=16, window=2000, sinks=130),
+    dict(lens=[2500], new=[17], Hq=140, Hkv=1, d=64, dt="f16", ps=128),
+    dict(lens=[1200], new=[1300], Hq=1, Hkv=1, d=64, dt="f16", ps=16),
+    dict(lens=[2048], new=[3], Hq=4, Hkv=2, d=128, dt="f16", ps=128, scale=-0.3, bad_pages=[(0, j, -1) for j in range(3, 12)]),
+    dict(lens=[2048], new=[3], Hq=4, Hkv=2, d=128, dt="f16", ps=128, bad_pages=[(0, j, 10 ** 9) for j in range(16)]),
 ]
 
 
