@@ -272,7 +272,32 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         mbar_init(iempty, kItemReaders);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    // the items' warp reads its first requests meanwhile
+    int start = 0, cnt = 0, all = 0, upto = 0;         // its lane's request: first row, rows, rows before T is cut off, items up to it
+    auto look = [&](int hi) {
+        const int b = hi - lane;
+        cnt = start = all = 0;
+        if (b >= 0) {
+            start = __ldg(a.starts + b);
+            const int stop = __ldg(a.starts + b + 1);
+            if (start >= 0 && stop > start) {
+                all = stop - start;
+                cnt = max(0, min(stop, a.p.T) - start);
+            }
+        }
+        upto = (cnt + per_item - 1) / per_item;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+        }
+    };
+    int my_len = 0;                                    // its request's tokens
     if (warp == 2) {
+        look(a.p.B - 1);
+        my_len = a.p.B - 1 - lane >= 0 ? clamp_len(__ldg(a.lengths + a.p.B - 1 - lane), a) : 0;
+    }
+    if (warp == 3) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_taddr)),
                      "r"(512));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -508,52 +533,34 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         const int heads = a.p.Hkv * chunks;
         int hi = a.p.B - 1;                                // lane l looks at request hi - l
         long long base = 0;                                // tiles of the requests above hi
-        int start = 0, cnt = 0, all = 0, upto = 0;         // this lane's request: first row, rows, rows before T is cut off, tiles up to it
-        auto look = [&] {
-            const int b = hi - lane;
-            cnt = start = all = 0;
-            if (b >= 0) {
-                start = __ldg(a.starts + b);
-                const int stop = __ldg(a.starts + b + 1);
-                if (start >= 0 && stop > start) {
-                    all = stop - start;
-                    cnt = max(0, min(stop, a.p.T) - start);
-                }
-            }
-            upto = (cnt + per_item - 1) / per_item;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += y;
-            }
+        auto look_at = [&] {
+            look(hi);
+            my_len = hi - lane >= 0 ? clamp_len(__ldg(a.lengths + hi - lane), a) : 0;
         };
         Item it;
-        // the item of the request's rows t0 .. t0 + nt - 1
-        auto rows_of = [&](int b, int s0, int rows_all, int t0, int nt) {
-            it.b = b;
-            it.row0 = s0 + t0;
-            it.nt = nt;
-            it.len = clamp_len(__ldg(a.lengths + b), a);
-            // positions by the rows that the request has, those cut off at T included
-            it.first = it.len - rows_all + t0;
-        };
         unsigned int parts = 1;
         if (a.split) {
             // every CTA comes to the same number of parts
             long long items = 0;
             int longest = 0;
-            for (;; hi -= 32) {
-                look();
+            for (;;) {
                 items += __shfl_sync(0xffffffffu, upto, 31);
-                if (cnt > 0) {
+                if (cnt > 0) {                                 // the request's last item sees the most keys
                     const int t0 = (cnt - 1) / per_item * per_item;
                     it.parts = 1;
-                    rows_of(hi - lane, start, all, t0, cnt - t0);
+                    it.len = my_len;
+                    it.first = my_len - all + t0;
+                    it.nt = cnt - t0;
                     longest = max(longest, Tiles(it, a).count);
                 }
                 if (hi < 32) break;
+                hi -= 32;
+                look_at();
             }
-            hi = a.p.B - 1;
+            if (hi != a.p.B - 1) {
+                hi = a.p.B - 1;
+                look_at();
+            }
             items *= heads;
             for (int o = 16; o > 0; o >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
             if (items > 0 && items <= kPreCtas)
@@ -563,11 +570,13 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 head->items = (int)min(items, (long long)kPreCtas);
             }
         }
-        look();
         for (int n = 0; ok; ++n) {
-            unsigned int x = 0;
-            if (lane == 0) x = atomicAdd(&head->taken, 1u);
-            x = __shfl_sync(0xffffffffu, x, 0);
+            // the first one by the CTA's number, the others from the counter
+            unsigned int x = blockIdx.x;
+            if (n > 0) {
+                if (lane == 0) x = gridDim.x + atomicAdd(&head->taken, 1u);
+                x = __shfl_sync(0xffffffffu, x, 0);
+            }
             it.parts = (int)parts;
             it.piece = (int)(x % parts);
             it.index = (int)(x / parts);
@@ -576,16 +585,21 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             while (hi >= 0 && u >= base + __shfl_sync(0xffffffffu, upto, 31)) {
                 base += __shfl_sync(0xffffffffu, upto, 31);
                 hi -= 32;
-                look();
+                look_at();
             }
             it.live = hi >= 0;
             const int at = hi >= 0 ? __ffs(__ballot_sync(0xffffffffu, base + upto > u)) - 1 : 0;   // the lane whose request it is
             const int t_end = (int)(base + __shfl_sync(0xffffffffu, upto, at) - u);                // tiles from this one to the request's first, this one included
             const int rows = __shfl_sync(0xffffffffu, cnt, at), rows_all = __shfl_sync(0xffffffffu, all, at);
             const int s0 = __shfl_sync(0xffffffffu, start, at);
+            it.len = __shfl_sync(0xffffffffu, my_len, at);
             if (it.live) {
                 const int t0 = (t_end - 1) * per_item;
-                rows_of(hi - at, s0, rows_all, t0, min(per_item, rows - t0));
+                it.b = hi - at;
+                it.row0 = s0 + t0;
+                it.nt = min(per_item, rows - t0);
+                // positions by the rows that the request has, those cut off at T included
+                it.first = it.len - rows_all + t0;
                 it.hk = kvh / chunks;
                 const int h0 = (kvh % chunks) * gch;
                 it.head0 = it.hk * grp + h0;
@@ -809,7 +823,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
 
     fence_before();
     __syncthreads();
-    if (warp == 2) {
+    if (warp == 3) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tbase), "r"(512));
     }
@@ -835,19 +849,37 @@ paged_prefill_join_kernel(const __grid_constant__ PagedArgs a)
     float m = -INFINITY, l = 0.f, o[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) o[j] = 0.f;
-#pragma unroll 4
-    for (int p = 0; p < parts; ++p) m = fmaxf(m, part[p * step + (size_t)D * kRows]);
-#pragma unroll 4
-    for (int p = 0; p < parts; ++p) {
-        const float pm = part[p * step + (size_t)D * kRows], pl = part[p * step + (size_t)(D + 1) * kRows];
-        const float f = pm == -INFINITY ? 0.f : exp2_fast(pm - m);
-        // a piece that saw nothing may have left its columns unwritten
+    // eight pieces at a time, all their loads in flight; past the last one the last one again, with weight 0
+    for (int p0 = 0; p0 < parts; p0 += 8) {
+        float pm[8], pl[8], v[8][8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float v = part[p * step + (size_t)(c0 + j) * kRows];
-            o[j] = f > 0.f ? fmaf(f, v, o[j]) : o[j];
+        for (int p = 0; p < 8; ++p) {
+            const float* at = part + min(p0 + p, parts - 1) * step;
+            pm[p] = at[(size_t)D * kRows];
+            pl[p] = at[(size_t)(D + 1) * kRows];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[p][j] = at[(size_t)(c0 + j) * kRows];
         }
-        l = f > 0.f ? fmaf(f, pl, l) : (pl == pl ? l : pl);
+        float top = m;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) top = fmaxf(top, pm[p]);
+        const float g = m == -INFINITY ? 0.f : exp2_fast(m - top);
+        m = top;
+        l *= g;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] *= g;
+#pragma unroll
+        for (int p = 0; p < 8; ++p) {
+            // a piece that saw nothing of this row may have left its columns unwritten
+            const float f = pm[p] == -INFINITY || p0 + p >= parts ? 0.f : exp2_fast(pm[p] - m);
+            if (f > 0.f) {
+                l = fmaf(f, pl[p], l);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] = fmaf(f, v[p][j], o[j]);
+            } else if (pl[p] != pl[p]) {
+                l = pl[p];
+            }
+        }
     }
     const float inv = l > 0.f ? 1.f / l : (l == l ? 0.f : l);
     const size_t row = (size_t)row0 + t, hd = (size_t)head0 + h;
