@@ -70,7 +70,8 @@ page_plan_kernel(PlanArgs a)
     const int step = PART == kGrid ? gridDim.x * THREADS : THREADS;
     const int most = a.max_pages << a.shift;
     const int each = (B + THREADS - 1) / THREADS, b0 = min(B, tid * each), b1 = min(B, b0 + each);
-    if (PART == kGrid) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // the last block starts behind every grid block's wait: what the plan reads is complete for it too
+    if (PART != kLast) pdl_begin();
     if (tid == 0) s_taken = s_refused = 0;
 
     auto length = [&](int b) { return min(max(a.lengths[b], 0), most); };
@@ -191,21 +192,19 @@ cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t st)
 {
     const size_t smem = (size_t)(4 * a.B + 3) * sizeof(int);
     if (a.B <= kFew && a.max_tokens <= kFew) {
-        page_plan_kernel<128, kAll><<<1, 128, smem, st>>>(a);
-        return cudaGetLastError();
+        return launch_pdl(page_plan_kernel<128, kAll>, dim3(1), dim3(128), smem, st, a);
     }
     if (a.max_tokens <= kOneBlock) {
         const cudaError_t e = allow_smem<1024, kAll>(smem);
         if (e != cudaSuccess) return e;
-        page_plan_kernel<1024, kAll><<<1, 1024, smem, st>>>(a);
-        return cudaGetLastError();
+        return launch_pdl(page_plan_kernel<1024, kAll>, dim3(1), dim3(1024), smem, st, a);
     }
     cudaError_t e = allow_smem<kGridThreads, kGrid>(smem);
     if (e == cudaSuccess) e = allow_smem<1024, kLast>(smem);
     if (e != cudaSuccess) return e;
     const int blocks = (a.max_tokens + kGridThreads - 1) / kGridThreads;
-    page_plan_kernel<kGridThreads, kGrid><<<blocks < kGridBlocks ? blocks : kGridBlocks, kGridThreads, smem, st>>>(a);
-    e = cudaGetLastError();
+    e = launch_pdl(page_plan_kernel<kGridThreads, kGrid>, dim3(blocks < kGridBlocks ? blocks : kGridBlocks),
+                   dim3(kGridThreads), smem, st, a);
     if (e != cudaSuccess) return e;
     return launch_pdl(page_plan_kernel<1024, kLast>, dim3(1), dim3(1024), smem, st, a);
 }

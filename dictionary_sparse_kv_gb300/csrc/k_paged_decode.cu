@@ -12,7 +12,10 @@
 // without a tail, and a share may begin or end inside a (request, KV head).
 // Such pieces go to the workspace, and the CTA that arrives last at a
 // (request, KV head) joins its pieces in their order: one launch, and results
-// that do not depend on which CTA that was.
+// that do not depend on which CTA that was.  Requests of about one length (a
+// full window, say) are cut into equal parts instead, one a CTA, where that
+// fills the grid: a share that begins in one (request, KV head) and ends in the
+// next costs two beginnings and two joins.
 //
 // Inside a CTA each of four warps takes every fourth 16-token tile through a
 // pipeline of its own (cp.async, one block-table lookup per token), with its
@@ -37,12 +40,15 @@ constexpr int kDecThreads = 128;
 constexpr int kDecWarps = kDecThreads / 32;
 constexpr int kTile = 16;                          // tokens per warp step
 constexpr int kBlock = kTile * kDecWarps;          // tokens per unit of work
-constexpr int kDecCtas = 304;                      // two per multiprocessor (152)
+// CTAs: two per multiprocessor (152), three at d = 64, whose buffers are half as large (113 requests, window 1024, d = 64:
+// 14.7 us against 16.0 with two CTAs of six stages; d = 128 with three CTAs of two stages: 16 of 4096 34.8 against 27.7 us)
+__host__ __device__ constexpr int dec_ctas(int d) { return d == 128 ? 304 : 456; }
 constexpr int kMaxHeads = 16;                      // query heads per piece; larger groups are several pieces
 constexpr size_t kCounterBytes = 4096;             // at the workspace's start whatever the parameters
 
 template <int D> struct DecCfg {
-    static constexpr int STAGES = D == 128 ? 3 : 6;
+    static constexpr int STAGES = 3;
+    static constexpr int CTAS = dec_ctas(D);
     static constexpr int TILE_BYTES = kTile * D * 2;
     static constexpr int WARP_BYTES = STAGES * 2 * TILE_BYTES;
     // warps' results of eight heads: three quarters each, as the owner of a quarter keeps its own
@@ -58,8 +64,8 @@ __host__ __device__ constexpr size_t piece_floats(int d) { return (size_t)kMaxHe
 struct Work {
     int b, hk, head0, hn, nb, blk0, blk1;
     int end, tile0, tiles;     // list indices end at `end`; this warp's tiles
+    long long first;           // unit number of block 0 (shares)
     Seen seen;
-    long long first;           // unit number of block 0
 };
 
 __device__ __forceinline__ int add_acq_rel(int* p, int v)
@@ -77,7 +83,7 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
     constexpr int STAGES = Cfg::STAGES, ROW = D * 2, CPR = D / 8;      // bytes and 16-byte chunks per row
     constexpr int KS = D / 16, KQ = KS / kDecWarps;                    // 16-element steps; those a warp writes out
     extern __shared__ __align__(1024) unsigned char smem[];
-    __shared__ int s_b, s_last;
+    __shared__ int s_b, s_last, s_longest;
     __shared__ long long s_base;
     __shared__ float s_m[kDecWarps][8 * NT], s_l[kDecWarps][8 * NT];
     __shared__ uint32_t s_ok[kDecWarps][STAGES];
@@ -88,15 +94,24 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
     const int segs = a.p.Hkv * chunks;
     const uint32_t wbase = saddr(smem + warp * Cfg::WARP_BYTES);
     float4* joinbuf = reinterpret_cast<float4*>(smem + kDecWarps * Cfg::WARP_BYTES);
+    pdl_begin();
 
     // blocks of a request: at least one, so that one which sees nothing is written too
     auto blocks_of = [&](const Seen& s) { return max(1, (s.count + kBlock - 1) / kBlock); };
     auto blocks = [&](int b) { return blocks_of(seen_of(clamp_len(__ldg(a.lengths + b), a), a)); };
     long long u, u1, U, base;                                          // this CTA's units; all; the first of request cur_b
-    int C, cur_b;
+    int C, cur_b, longest, parts = 0;                                  // parts > 0: (request, heads) in so many equal parts
+    // Equal parts: the lengths are within an eighth of the longest one on average, and the parts are at least three
+    // fifths of the grid.  (113 requests, window 1024, two KV heads of 64: 14.0 us in equal parts, 16.6 in shares.)
     auto share = [&] {
-        C = (int)min((long long)gridDim.x, U);
-        if (U < (1 << 22)) {                                          // C <= 304: the products fit 32 bits
+        const int pieces = B * segs, grid = (int)gridDim.x;
+        C = (int)min((long long)grid, U);
+        if (pieces <= grid && 8 * U >= 7ll * pieces * longest) {
+            parts = min(longest, grid / pieces);
+            if (5 * pieces * parts >= 3 * C) C = pieces * parts;
+            else parts = 0;
+        }
+        if (U < (1 << 22)) {                                          // C <= 456: the products fit 32 bits
             u = (int)U * (int)blockIdx.x / C;
             u1 = (int)U * (int)(blockIdx.x + 1) / C;
         } else {
@@ -105,8 +120,10 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
         }
     };
     if (B <= 32) {                                                    // a lane a request, each warp for itself
-        const long long mine = lane < B ? (long long)blocks(lane) * segs : 0;
+        const int nb = lane < B ? blocks(lane) : 0;
+        const long long mine = (long long)nb * segs;
         long long upto = mine;
+        longest = __reduce_max_sync(0xffffffffu, nb);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long long y = __shfl_up_sync(0xffffffffu, upto, o);
@@ -115,16 +132,28 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
         U = __shfl_sync(0xffffffffu, upto, 31);
         share();
         if ((int)blockIdx.x >= C) return;
-        cur_b = __ffs(__ballot_sync(0xffffffffu, upto > u)) - 1;
-        base = __shfl_sync(0xffffffffu, upto - mine, cur_b);
+        if (parts == 0) {
+            cur_b = __ffs(__ballot_sync(0xffffffffu, upto > u)) - 1;
+            base = __shfl_sync(0xffffffffu, upto - mine, cur_b);
+        }
     } else {
         const int each = (B + kDecThreads - 1) / kDecThreads, b0 = min(B, tid * each), b1 = min(B, b0 + each);
         long long mine = 0;
-        for (int b = b0; b < b1; ++b) mine += (long long)blocks(b) * segs;
+        int most = 0;
+        if (tid == 0) s_longest = 0;
+        for (int b = b0; b < b1; ++b) {
+            const int nb = blocks(b);
+            mine += (long long)nb * segs;
+            most = max(most, nb);
+        }
         long long at = block_scan<kDecThreads>(mine, &U);
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) atomicMax(&s_longest, most);
+        __syncthreads();
+        longest = s_longest;
         share();
         if ((int)blockIdx.x >= C) return;
-        if (u >= at && u < at + mine) {
+        if (parts == 0 && u >= at && u < at + mine) {
             int b = b0;
             for (long long n; u >= at + (n = (long long)blocks(b) * segs); ++b) at += n;
             s_b = b;
@@ -141,11 +170,26 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
         w.b = cur_b;
         w.seen = seen_of(clamp_len(__ldg(a.lengths + cur_b), a), a);
         w.nb = blocks_of(w.seen);
-        const long long rel = u - base;
-        const int seg = rel < 0x7fffffffll ? (int)rel / w.nb : (int)(rel / w.nb);
-        w.first = base + (long long)seg * w.nb;
-        w.blk0 = (int)(u - w.first);
-        w.blk1 = (int)min((long long)w.nb, w.blk0 + (u1 - u));
+        int seg;
+        if (parts > 0) {
+            seg = (int)blockIdx.x / parts % segs;
+            const int n = min(parts, w.nb), part = (int)blockIdx.x % parts;   // a short request has fewer parts
+            const int each = w.nb / n, rest = w.nb % n;                      // the first `rest` parts take one block more
+            w.blk0 = part * each + min(part, rest);
+            w.blk1 = part < n ? w.blk0 + each + (part < rest) : w.blk0;
+            u = u1;
+        } else {
+            const long long rel = u - base;
+            seg = rel < 0x7fffffffll ? (int)rel / w.nb : (int)(rel / w.nb);
+            w.first = base + (long long)seg * w.nb;
+            w.blk0 = (int)(u - w.first);
+            w.blk1 = (int)min((long long)w.nb, w.blk0 + (u1 - u));
+            u += w.blk1 - w.blk0;
+            if (w.blk1 == w.nb && seg == segs - 1) {
+                base += (long long)w.nb * segs;
+                ++cur_b;
+            }
+        }
         w.hk = chunks == 1 ? seg : seg / chunks;
         const int h0 = chunks == 1 ? 0 : (seg % chunks) * 8 * NT;
         w.hn = min(8 * NT, grp - h0);
@@ -153,11 +197,6 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
         w.end = min(w.blk1 * kBlock, w.seen.count);
         w.tile0 = w.blk0 * kDecWarps + warp;
         w.tiles = max(0, ((w.end + kTile - 1) / kTile - w.tile0 + kDecWarps - 1) / kDecWarps);
-        u += w.blk1 - w.blk0;
-        if (w.blk1 == w.nb && seg == segs - 1) {
-            base += (long long)w.nb * segs;
-            ++cur_b;
-        }
         return w;
     };
 
@@ -212,7 +251,9 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
         }
     };
 
+    if (parts > 0) cur_b = (int)blockIdx.x / parts / segs;
     Work w = next_work();
+    if (w.blk0 == w.blk1) return;                                       // a part that a short request does not have
     begin(w);
     load_q(w);
     for (;;) {
@@ -417,8 +458,18 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
             __syncthreads();                            // the buffer, and s_m and s_l, are written again
         }
         if (!whole) {
-            // CTAs whose shares hold a part of this (request, heads): unit x is in share ((x + 1) C - 1) / U
-            const int c0 = (int)(((done.first + 1) * C - 1) / U), c1 = (int)(((done.first + done.nb) * C - 1) / U);
+            // the CTAs that have its parts; of shares, unit x is in share ((x + 1) C - 1) / U
+            int c0, c1;
+            if (parts > 0) {
+                c0 = (int)blockIdx.x / parts * parts;
+                c1 = c0 + min(parts, done.nb) - 1;
+            } else if (U < (1 << 22)) {
+                c0 = (int)(((unsigned int)done.first + 1) * (unsigned int)C - 1) / (int)U;
+                c1 = (int)(((unsigned int)done.first + done.nb) * (unsigned int)C - 1) / (int)U;
+            } else {
+                c0 = (int)(((done.first + 1) * C - 1) / U);
+                c1 = (int)(((done.first + done.nb) * C - 1) / U);
+            }
             if (tid == 0) {
                 int* counter = reinterpret_cast<int*>(a.ws) + c0;
                 s_last = add_acq_rel(counter, 1) == c1 - c0;     // the block's stores before it, the other blocks' after it
@@ -477,7 +528,7 @@ template <typename T, int D, int NT>
 cudaError_t launch_nt(const PagedArgs& a, cudaStream_t st)
 {
     auto k = paged_decode_kernel<T, D, NT>;
-    const int smem = DecCfg<D>::SMEM;
+    const int smem = DecCfg<D>::SMEM, ctas = DecCfg<D>::CTAS;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     // an upper bound of the units: lengths are known on the device only
@@ -485,8 +536,7 @@ cudaError_t launch_nt(const PagedArgs& a, cudaStream_t st)
     if (a.p.window > 0) most = most < (long long)a.p.window + a.p.sinks ? most : (long long)a.p.window + a.p.sinks;
     const long long chunks = (a.grp + 8 * NT - 1) / (8 * NT);
     const long long units = ((most + kBlock - 1) / kBlock + 1) * a.p.B * a.p.Hkv * chunks;
-    k<<<(unsigned)(units < kDecCtas ? units : kDecCtas), kDecThreads, smem, st>>>(a);
-    return cudaGetLastError();
+    return launch_pdl(k, dim3((unsigned)(units < ctas ? units : ctas)), dim3(kDecThreads), smem, st, a);
 }
 
 template <typename T, int D>
@@ -499,7 +549,7 @@ cudaError_t launch_t(const PagedArgs& a, cudaStream_t st)
 
 size_t paged_attend_workspace(const fadkv_paged_params& p)
 {
-    return kCounterBytes + (size_t)2 * kDecCtas * piece_floats(p.d) * sizeof(float);
+    return kCounterBytes + (size_t)2 * dec_ctas(p.d) * piece_floats(p.d) * sizeof(float);
 }
 
 cudaError_t launch_paged_attend(const PagedArgs& a, cudaStream_t st)

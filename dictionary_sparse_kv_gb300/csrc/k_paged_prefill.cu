@@ -272,6 +272,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         mbar_init(iempty, kItemReaders);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    pdl_begin();
     // the items' warp reads its first requests meanwhile
     int start = 0, cnt = 0, all = 0, upto = 0;         // its lane's request: first row, rows, rows before T is cut off, items up to it
     auto look = [&](int hi) {
@@ -834,6 +835,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kRows)
 paged_prefill_join_kernel(const __grid_constant__ PagedArgs a)
 {
+    // (waits only: a dependent let in early would take the registers that the other blocks of this grid need)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const PreHead* head = reinterpret_cast<const PreHead*>(a.ws);
     const int parts = head->parts, item = blockIdx.x / a.split, q = blockIdx.x % a.split;
@@ -959,8 +961,7 @@ cudaError_t launch_t(const PagedArgs& args, cudaStream_t st)
     if (!query_map(&mq, a, s.gch, s.tq) || !pool_map(&mk, a.k, a) || !pool_map(&mv, a.v, a)) return cudaErrorInvalidValue;
     if (s.items > 0x7fffffffll) return cudaErrorInvalidValue;
     const int ctas = s.split || s.items > kPreCtas ? kPreCtas : (int)s.items;
-    k<<<ctas, kPreThreads, PreCfg<D>::alloc, st>>>(mq, mk, mv, a);
-    e = cudaGetLastError();
+    e = launch_pdl(k, dim3(ctas), dim3(kPreThreads), PreCfg<D>::alloc, st, mq, mk, mv, a);
     if (e != cudaSuccess || !s.split) return e;
     const int items = (int)(s.items < kPreCtas ? s.items : kPreCtas);
     return launch_pdl(paged_prefill_join_kernel<T, D>, dim3(items * s.split, D / 8), dim3(kRows), 0, st, a);

@@ -69,6 +69,7 @@ qk_norm_rope_kernel(const __grid_constant__ QkArgs a, int each, int parts)
     const int rd = a.rope.rotary_dim, half = rd / 2;
     if (threadIdx.x < half) turns[threadIdx.x] = a.rope.turns[threadIdx.x];
     __syncthreads();
+    pdl_begin();
 
     const unsigned int w = blockIdx.x * (kQkThreads / 32) + (threadIdx.x >> 5);
     const int t = (int)(w / (unsigned int)parts), part = (int)(w % (unsigned int)parts);
@@ -226,11 +227,8 @@ cudaError_t launch_t(const QkArgs& a, cudaStream_t st)
     const long long warps = (long long)a.p.T * parts;
     if (warps > 0x7fffffffll) return cudaErrorInvalidValue;
     const unsigned grid = (unsigned)((warps + kQkThreads / 32 - 1) / (kQkThreads / 32));
-    if (a.rope.interleaved)
-        qk_norm_rope_kernel<T, D, true><<<grid, kQkThreads, 0, st>>>(a, (int)each, parts);
-    else
-        qk_norm_rope_kernel<T, D, false><<<grid, kQkThreads, 0, st>>>(a, (int)each, parts);
-    return cudaGetLastError();
+    return launch_pdl(a.rope.interleaved ? qk_norm_rope_kernel<T, D, true> : qk_norm_rope_kernel<T, D, false>, dim3(grid),
+                      dim3(kQkThreads), 0, st, a, (int)each, parts);
 }
 
 template <typename T>
