@@ -100,14 +100,25 @@ page_plan_kernel(PlanArgs a)
         if (lane == 31) s_part[k][warp] = at[k];
     }
     __syncthreads();
+    constexpr int W = THREADS / 32;
+    if (warp == 0) {                                   // the warps' sums: their prefix sums, the whole one last
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            long long x = lane < W ? s_part[k][lane] : 0;
+#pragma unroll
+            for (int o = 1; o < W; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o) x += y;
+            }
+            if (lane < W) s_part[k][lane] = x;
+        }
+    }
+    __syncthreads();
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
         at[k] -= mine[k];
-        total[k] = 0;
-        for (int w = 0; w < THREADS / 32; ++w) {
-            if (w < warp) at[k] += s_part[k][w];
-            total[k] += s_part[k][w];
-        }
+        if (warp > 0) at[k] += s_part[k][warp - 1];
+        total[k] = s_part[k][W - 1];
     }
     const int returned = (int)min(total[2], (long long)(a.num_pages - count)), F = count + returned;
     int taken = 0, refused = 0;
