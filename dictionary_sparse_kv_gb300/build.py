@@ -4,7 +4,9 @@ Compiles every ``csrc/*.cu`` into an object file in parallel (one nvcc per
 translation unit, a single -gencode) and links them into
 ``dictionary_sparse_kv_gb300/_build/libfadkv.so`` with the CUDA runtime linked
 statically, so the library loads without a GPU and its only runtime
-dependency is the NVIDIA driver (libcuda).
+dependency is the NVIDIA driver (libcuda).  ``csrc/pycalls.c``, the binding's
+direct calls, becomes ``_build/_fadkv_calls.so`` (the C compiler and Python's
+own headers; nothing of CUDA in it).
 
     python -m dictionary_sparse_kv_gb300.build [--force] [--verbose]
 """
@@ -17,6 +19,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -24,6 +27,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "libfadkv.so")
+CALLS = os.path.join(OUT, "_fadkv_calls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -42,14 +46,28 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    return _sources() + glob.glob(os.path.join(CSRC, "*.c")) + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return all(os.path.getmtime(p) <= t for p in _deps())
+
+
+def build_calls():
+    """The binding's direct calls, with the C compiler."""
+    cc = os.environ.get("CC") or shutil.which("cc") or shutil.which("gcc")
+    if not cc:
+        raise RuntimeError("no C compiler found")
+    tmp = CALLS + f".{os.getpid()}.tmp"
+    cmd = [cc, "-std=gnu11", "-O2", "-Wall", "-shared", "-fPIC", "-I", INCLUDE, "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "pycalls.c"), "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cc} failed on pycalls.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
@@ -77,6 +95,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=None) -> str:
     for f in os.listdir(OUT):
         if f.endswith(".o") and f not in keep:
             os.remove(os.path.join(OUT, f))
+    build_calls()
     with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
         objs = list(ex.map(compile_one, srcs))
     tmp = LIB + f".{os.getpid()}.tmp"

@@ -678,6 +678,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                         uint32_t bits = low_bits(pos - k + 1);
                         if (ts.W > 0) bits &= ~low_bits(pos - ts.W - k + 1) | low_bits(ts.S - k);
                         if (!all_ok) bits &= okr[1 + c];
+                        if (__all_sync(0xffffffffu, bits == 0xffffffffu)) continue;
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             if (!((bits >> j) & 1u)) s[c][j] = 0xff800000u;

@@ -1,8 +1,10 @@
 """Thin Python binding of the FAD-KV C ABI (include/fadkv.h).
 
-Only marshals arguments: every step of encode / adapt / reconstruct runs in
-the CUDA library ``_build/libfadkv.so``.  There is no fallback: if the library
-is missing, importing the functions raises ``FadkvLibraryMissing``.
+Only marshals arguments (the paged-cache calls through the small module
+``_build/_fadkv_calls.so``, the others through ctypes): every step of encode /
+adapt / reconstruct runs in the CUDA library ``_build/libfadkv.so``.  There is
+no fallback: if a library is missing, importing the functions raises
+``FadkvLibraryMissing``.
 
 Functions carry the C names without the ``fadkv_`` prefix.  Device arrays are
 passed as torch CUDA tensors (their ``data_ptr()``) or raw integer addresses;
@@ -17,6 +19,7 @@ from dataclasses import dataclass
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "_build", "libfadkv.so")
+CALLS_PATH = os.path.join(_PKG, "_build", "_fadkv_calls.so")
 
 F16 = 0
 F32 = 1
@@ -172,6 +175,28 @@ def lib():
                 fn.restype = res
             _lib = L
     return _lib
+
+
+_calls = None            # module _fadkv_calls: direct calls of the paged-cache functions
+_direct = {}             # their addresses in the library, by name
+
+
+def _load_calls():
+    global _calls
+    import importlib.machinery
+    import importlib.util
+    L = lib()
+    with _lock:
+        if _calls is None:
+            if not os.path.exists(CALLS_PATH):
+                raise FadkvLibraryMissing(f"{CALLS_PATH} is not built; run `python -m dictionary_sparse_kv_gb300.build`")
+            loader = importlib.machinery.ExtensionFileLoader("_fadkv_calls", CALLS_PATH)
+            m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fadkv_calls", loader))
+            loader.exec_module(m)
+            for name in ("page_plan", "qk_norm_rope", "paged_attend", "paged_prefill"):
+                _direct[name] = C.cast(getattr(L, "fadkv_" + name), C.c_void_p).value
+            _calls = m
+    return _calls
 
 
 def _addr(t):
@@ -338,11 +363,11 @@ def page_params(B: int, page_size: int, num_pages: int, max_pages: int, max_toke
 def page_plan(p: PageParams, add, lengths, block_table, free_pages, free_count, lengths_out, free_count_out, starts,
               positions, slots, refused, stream=None) -> None:
     """Pages, positions and slots of one step's new tokens (see fadkv_page_plan)."""
-    st = _stream(stream, lengths)
-    _check("fadkv_page_plan", lib().fadkv_page_plan(C.byref(p), _addr(add), _addr(lengths), _addr(block_table),
-                                                    _addr(free_pages), _addr(free_count), _addr(lengths_out),
-                                                    _addr(free_count_out), _addr(starts), _addr(positions),
-                                                    _addr(slots), _addr(refused), st))
+    rc = (_calls or _load_calls()).page_plan(_direct["page_plan"], p, add, lengths, block_table, free_pages, free_count,
+                                             lengths_out, free_count_out, starts, positions, slots, refused,
+                                             _stream(stream, lengths))
+    if rc:
+        _check("fadkv_page_plan", rc)
 
 
 def rope_init(d: int, rotary_dim: int, interleaved: bool = False, base: float = 10000.0, scaling: str = "plain",
@@ -380,11 +405,10 @@ def qk_params(q, k, v, q_out, k_pages, layout: str = "head", eps: float = 1e-6, 
 def qk_norm_rope(p: QkParams, rope: Rope, q, k, v, wq, wk, positions, slots, q_out, k_out, k_pages, v_pages,
                  stream=None) -> None:
     """Norm and rotation of queries and keys, keys and values appended to the pools (see fadkv_qk_norm_rope)."""
-    st = _stream(stream, q, q_out)
-    _check("fadkv_qk_norm_rope", lib().fadkv_qk_norm_rope(C.byref(p), C.byref(rope), _addr(q), _addr(k), _addr(v),
-                                                          _addr(wq), _addr(wk), _addr(positions), _addr(slots),
-                                                          _addr(q_out), _addr(k_out), _addr(k_pages),
-                                                          _addr(v_pages), st))
+    rc = (_calls or _load_calls()).qk_norm_rope(_direct["qk_norm_rope"], p, rope, q, k, v, wq, wk, positions, slots, q_out,
+                                                k_out, k_pages, v_pages, _stream(stream, q, q_out))
+    if rc:
+        _check("fadkv_qk_norm_rope", rc)
 
 
 def paged_params(q, out, k_pages, layout: str = "head", block_table=None, window: int = 0, sinks: int = 0,
@@ -419,26 +443,26 @@ def paged_prefill_workspace_bytes(p: PagedParams) -> int:
 
 
 def _nbytes(workspace) -> int:
-    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return 0 if workspace is None else workspace.nbytes
 
 
 def paged_attend(p: PagedParams, k_pages, v_pages, block_table, lengths, q, out, lse, workspace, stream=None) -> None:
     """Attention of one new token per request over the pages (see fadkv_paged_attend).  The workspace is
     zero-filled before its first use."""
-    st = _stream(stream, q, out)
-    _check("fadkv_paged_attend", lib().fadkv_paged_attend(C.byref(p), _addr(k_pages), _addr(v_pages),
-                                                          _addr(block_table), _addr(lengths), _addr(q), _addr(out),
-                                                          _addr(lse), _addr(workspace), _nbytes(workspace), st))
+    rc = (_calls or _load_calls()).paged_attend(_direct["paged_attend"], p, k_pages, v_pages, block_table, lengths, q, out,
+                                                lse, workspace, _nbytes(workspace), _stream(stream, q, out))
+    if rc:
+        _check("fadkv_paged_attend", rc)
 
 
 def paged_prefill(p: PagedParams, k_pages, v_pages, block_table, lengths, starts, q, out, lse=None, workspace=None,
                   stream=None) -> None:
-    """Attention of each request's last tokens over the pages (see fadkv_paged_prefill)."""
-    st = _stream(stream, q, out)
-    _check("fadkv_paged_prefill", lib().fadkv_paged_prefill(C.byref(p), _addr(k_pages), _addr(v_pages),
-                                                            _addr(block_table), _addr(lengths), _addr(starts),
-                                                            _addr(q), _addr(out), _addr(lse), _addr(workspace),
-                                                            _nbytes(workspace), st))
+    """Attention of each request's last tokens over the pages (see fadkv_paged_prefill).  The workspace is
+    zero-filled before its first use."""
+    rc = (_calls or _load_calls()).paged_prefill(_direct["paged_prefill"], p, k_pages, v_pages, block_table, lengths, starts,
+                                                 q, out, lse, workspace, _nbytes(workspace), _stream(stream, q, out))
+    if rc:
+        _check("fadkv_paged_prefill", rc)
 
 
 def reconstruct(h: int, V: int, idx, coef, repl_id, repl_coef, xhat, stream=None) -> None:

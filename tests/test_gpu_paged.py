@@ -560,3 +560,19 @@ def test_a_loop_of_steps_and_its_graph():
         got = np.stack([_np(outs[0][b, t]) for t in range(prompts[b])] + [_np(dec[t][b]) for t in range(steps)])
         assert (np.abs(got - want[0]) <= e_out).all()
     assert int(direct["refused"]) == 0 and int(direct["count"]) == pages - sum(-(-(n + steps) // ps) for n in prompts)
+
+
+def test_the_example_runs():
+    """examples/paged_loop.py: prompts, decode steps and codes of one layer."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "paged_loop.py")
+    spec = importlib.util.spec_from_file_location("paged_loop", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    r = m.main(["--prompt", "20", "--steps", "3", "--requests", "3"])
+    assert r["tokens"] == [23, 23, 23] and r["refused"] == 0 and r["pages left"] == 0
+    # one token's output twice: rounded once each, and once more for the probabilities of the prefill; values are of the
+    # order of one, so half a step is 2^-11 and |out| + sum p |v| at most 5 or so
+    assert r["prefill and decode differ by"] < 2.0 ** -11 * 3 * 5
+    assert all(math.isfinite(r[k + " against full"]) for k in ("window", "codes"))

@@ -171,3 +171,20 @@ def test_tensor_helpers_refuse(L):
     for bad in (dict(k=k.float()), dict(v=k[:, :4]), dict(q=q[..., ::2])):
         with pytest.raises(ValueError):
             F.qk_params(**{**dict(q=q, k=k, v=k, q_out=q, k_pages=pool), **bad})
+
+
+def test_direct_calls_check_their_arguments(L):
+    """The binding's own module: other structs and objects are refused before the library is called."""
+    p, r = _qk(), F.rope_init(128, 128)
+    with pytest.raises(TypeError):
+        F.qk_norm_rope(F.page_params(1, 8, 1, 1, 1), r, *[FAKE] * 11, stream=0)
+    with pytest.raises(TypeError):
+        F.qk_norm_rope(p, p, *[FAKE] * 11, stream=0)
+    with pytest.raises(AttributeError):
+        F.qk_norm_rope(p, r, "q", *[FAKE] * 10, stream=0)
+    with pytest.raises(OverflowError):
+        F.qk_norm_rope(p, r, 1 << 70, *[FAKE] * 10, stream=0)
+    with pytest.raises(TypeError):
+        F._calls.paged_attend(F._direct["paged_attend"], _paged())
+    with pytest.raises(AttributeError):
+        F.paged_prefill(_paged(), *[FAKE] * 8, workspace=object(), stream=0)
