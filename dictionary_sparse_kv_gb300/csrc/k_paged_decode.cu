@@ -44,7 +44,6 @@ constexpr int kBlock = kTile * kDecWarps;          // tokens per unit of work
 // 14.7 us against 16.0 with two CTAs of six stages; d = 128 with three CTAs of two stages: 16 of 4096 34.8 against 27.7 us)
 __host__ __device__ constexpr int dec_ctas(int d) { return d == 128 ? 304 : 456; }
 constexpr int kMaxHeads = 16;                      // query heads per piece; larger groups are several pieces
-constexpr size_t kCounterBytes = 4096;             // at the workspace's start whatever the parameters
 
 template <int D> struct DecCfg {
     static constexpr int STAGES = 3;
@@ -55,6 +54,8 @@ template <int D> struct DecCfg {
     static constexpr int JOIN_BYTES = kDecWarps * 3 * (D / 16 / kDecWarps) * 32 * 16;
     static constexpr int SMEM = kDecWarps * WARP_BYTES + JOIN_BYTES;
 };
+
+static_assert(dec_ctas(64) * sizeof(int) <= kHeadBytes - kDecodeHead && dec_ctas(128) <= dec_ctas(64), "workspace head");
 
 // A piece in the workspace: kMaxHeads rows of d sums, then their m and l.
 __host__ __device__ constexpr size_t piece_floats(int d) { return (size_t)kMaxHeads * (d + 2); }
@@ -383,7 +384,7 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
                 }
             }
         const bool whole = done.blk0 == 0 && done.blk1 == done.nb;
-        float* pieces = reinterpret_cast<float*>((unsigned char*)a.ws + kCounterBytes);
+        float* pieces = reinterpret_cast<float*>((unsigned char*)a.ws + kHeadBytes);
         constexpr size_t PF = piece_floats(D);
         float* mine = pieces + (2 * (size_t)blockIdx.x + (done.blk0 == 0 ? 1 : 0)) * PF;
         auto lse_of = [&](float mh, float lh) { return lh == 0.f ? -INFINITY : (mh + log2f(lh)) * kLn2; };
@@ -471,7 +472,7 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
                 c1 = (int)(((done.first + done.nb) * C - 1) / U);
             }
             if (tid == 0) {
-                int* counter = reinterpret_cast<int*>(a.ws) + c0;
+                int* counter = reinterpret_cast<int*>((unsigned char*)a.ws + kDecodeHead) + c0;
                 s_last = add_acq_rel(counter, 1) == c1 - c0;     // the block's stores before it, the other blocks' after it
                 if (s_last) *counter = 0;
             }
@@ -549,7 +550,7 @@ cudaError_t launch_t(const PagedArgs& a, cudaStream_t st)
 
 size_t paged_attend_workspace(const fadkv_paged_params& p)
 {
-    return kCounterBytes + (size_t)2 * dec_ctas(p.d) * piece_floats(p.d) * sizeof(float);
+    return kHeadBytes + (size_t)2 * dec_ctas(p.d) * piece_floats(p.d) * sizeof(float);
 }
 
 cudaError_t launch_paged_attend(const PagedArgs& a, cudaStream_t st)

@@ -78,8 +78,7 @@ struct PreHead {
     int parts, items;                              // of this call, for the join
     struct { int row0, nt, head0, hn; } item[kPreCtas];
 };
-constexpr size_t kHeadBytes = 4096;
-static_assert(sizeof(PreHead) <= kHeadBytes, "workspace head");
+static_assert(sizeof(PreHead) <= kDecodeHead, "workspace head");
 __host__ __device__ constexpr size_t slot_floats(int d) { return (size_t)kRows * (d + 2); }   // a tile's rows: o by column, m, l
 
 template <int D> struct PreCfg {
@@ -176,10 +175,10 @@ __device__ __forceinline__ float max3(float a, float b, float c)
 // Bits 0 .. n-1 set (none for n <= 0, all for n >= 32).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
 
-// The key tiles of an item: those of the first tokens, then those of the
-// window (or all).
+// The key tiles of an item: those of the window (or all), then those of the
+// first tokens, whose few keys would set a maximum that the next tile exceeds.
 struct Tiles {
-    int first, last, W, S, from, sinks, lo, count;     // count tiles from number lo on
+    int first, last, W, S, from, sinks, all, lo, count;     // count tiles of all from number lo on
     __device__ __forceinline__ Tiles(const Item& it, const PagedArgs& a)
     {
         first = it.first;
@@ -189,7 +188,7 @@ struct Tiles {
         const int to = last >= 0 ? last / kKeys + 1 : 0;
         from = W > 0 ? max(0, first - W + 1) / kKeys : 0;
         sinks = W > 0 ? min(from, (S + kKeys - 1) / kKeys) : 0;
-        count = to > from ? sinks + to - from : 0;
+        count = all = to > from ? sinks + to - from : 0;
         lo = 0;
         if (it.parts > 1) {
             lo = count * it.piece / it.parts;
@@ -199,7 +198,7 @@ struct Tiles {
     __device__ __forceinline__ int key0(int i) const
     {
         i += lo;
-        return (i < sinks ? i : i - sinks + from) * kKeys;
+        return (i < all - sinks ? i + from : i - (all - sinks)) * kKeys;
     }
     // whether some row of the item sees a key; whether a tile holds keys that none sees
     __device__ __forceinline__ bool seen(int key) const { return key <= last && (W == 0 || key > first - W || key < S); }
@@ -652,11 +651,15 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             const int t = q * tq + tr;
             const bool live = tr < tq && t < it.nt && h < it.hn;
             const int pos = live ? it.first + t : -1;
-            const int pmin = it.first + q * tq, pmax = min(ts.last, pmin + tq - 1);
+            // the lowest and highest position among the warp's rows (no rows: nothing to mask)
+            const int pmin = __reduce_min_sync(0xffffffffu, live ? pos : 0x3fffffff);
+            const int pmax = __reduce_max_sync(0xffffffffu, live ? pos : -1);
             float m = -INFINITY, l = 0.f;
             for (int i = 0; i < tiles && ok; ++i, ++its) {
                 const int k0 = ts.key0(i);
                 const uint32_t* okr = ok_ring + ((gt0 + i) & (kOkRing - 1)) * 5;
+                // masks only where some row of the warp does not see some key (worked out while the scores are on their way)
+                const bool masked = !(k0 + kKeys - 1 <= pmin && (ts.W == 0 || k0 > pmax - ts.W || k0 + kKeys <= ts.S));
                 if (!wait(sfull(q), (uint32_t)its & 1u)) break;
                 fence_after();
                 const bool all_ok = okr[0] != 0;
@@ -670,8 +673,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                     __syncwarp();
                     if (lane == 0) mbar_arrive(sfree(q));
                 }
-                // masks only where the tile has keys that some row of the 128 does not see
-                if (!(k0 + kKeys - 1 <= pmin && (ts.W == 0 || k0 > pmax - ts.W || k0 + kKeys <= ts.S) && all_ok)) {
+                if (masked || !all_ok) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
                         const int k = k0 + c * 32;

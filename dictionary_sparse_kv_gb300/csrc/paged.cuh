@@ -64,6 +64,12 @@ cudaError_t launch_paged_prefill(const PagedArgs& a, cudaStream_t st);
 
 namespace paged {
 
+// The workspaces' heads, which have to be zero between calls, lie apart, so
+// that one workspace can serve both calls in turn: the prefill's first, then
+// (from kDecodeHead on) the counters of the single-token call, then what
+// either keeps only while it runs.
+constexpr size_t kDecodeHead = 4096, kHeadBytes = 8192;
+
 constexpr float kLn2 = 0.693147180559945f;
 
 // Type traits of the two 16-bit storage types.

@@ -517,6 +517,7 @@ typedef struct {
                  (v = t * Hkv + h) with kv_dtype the dictionary's type
      k_pages, v_pages  pools (null with null slots)
    16-byte aligned throughout (positions, slots 4).  rope->d must equal d.
+   Outputs and pools do not overlap the inputs.
    Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 fadkv_status fadkv_qk_norm_rope(const fadkv_qk_params* params, const fadkv_rope* rope, const void* q,
                                 const void* k, const void* v, const void* wq, const void* wk,
@@ -551,8 +552,9 @@ typedef struct {
      lse         [T][Hq] float32, or null
      workspace   >= fadkv_paged_attend_workspace_bytes bytes, 256-byte aligned,
                  ZERO-FILLED before its first use (each call leaves it fit for
-                 the next, whatever that call's parameters); not to be shared
-                 by calls that may run concurrently
+                 the next, whatever that call's parameters; one workspace, of
+                 the larger size, may serve fadkv_paged_prefill too); not to be
+                 shared by calls that may run concurrently
    Scores, softmax and sums in 32 bits; the probabilities enter the product
    with the values as two 16-bit terms each.
    Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */

@@ -381,6 +381,19 @@ def test_paged_prefill(i):
     Case(**PREFILLS[i]).run().check()
 
 
+def test_both_calls_share_one_workspace():
+    """Single tokens and chunks, cut along their keys and not, in turn on one workspace: the same bits each time."""
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device=DEV)
+    cases = [Case(**DECODES[0]), Case(**PREFILLS[17]), Case(**DECODES[6]), Case(**PREFILLS[2]), Case(**DECODES[10]), Case(**PREFILLS[18])]
+    first = [(c.run(ws).check().out.clone(), c.lse.clone()) for c in cases]
+    for _ in range(2):
+        for c, (o, l) in zip(cases, first):
+            c.out.fill_(5), c.lse.fill_(5)
+            c.run(ws)
+            torch.cuda.synchronize()
+            assert torch.equal(c.out, o) and torch.equal(c.lse, l)
+
+
 def test_paged_prefill_leaves_other_rows_alone():
     """Rows of q past starts[B] are padding: neither their out nor their lse is written; T cuts rows off."""
     from dictionary_sparse_kv_gb300 import fadkv as F
