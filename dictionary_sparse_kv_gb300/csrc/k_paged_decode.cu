@@ -12,7 +12,8 @@
 // without a tail, and a share may begin or end inside a (request, KV head).
 // Such pieces go to the workspace, and the CTA that arrives last at a
 // (request, KV head) joins its pieces in their order: one launch, and results
-// that do not depend on which CTA that was.  Requests of about one length (a
+// that do not depend on which CTA that was (pieces and groups of pieces are
+// the same every time).  Requests of about one length (a
 // full window, say) are cut into equal parts instead, one a CTA, where that
 // fills the grid: a share that begins in one (request, KV head) and ends in the
 // next costs two beginnings and two joins.
@@ -55,7 +56,15 @@ template <int D> struct DecCfg {
     static constexpr int SMEM = kDecWarps * WARP_BYTES + JOIN_BYTES;
 };
 
-static_assert(dec_ctas(64) * sizeof(int) <= kHeadBytes - kDecodeHead && dec_ctas(128) <= dec_ctas(64), "workspace head");
+// Pieces that one CTA joins: more are joined in groups, each by the last CTA
+// of its group, and the groups by the last group.  (32768 tokens of one KV head
+// in 304 pieces: 28.6 us joined by one CTA, 11.6 in groups; 4 requests of up to
+// 2000 tokens with 24 heads over 8, some 20 pieces each: 10.9 at once, 12.7 in
+// groups.)
+constexpr int kAtOnce = 32, kGroup = 16;
+constexpr int kCounters = 512;                     // of first groups, of other groups and of the groups of a (request, heads)
+static_assert(dec_ctas(64) <= kCounters && dec_ctas(128) <= kCounters, "counters");
+static_assert(3 * kCounters * sizeof(int) <= kHeadBytes - kDecodeHead, "workspace head");
 
 // A piece in the workspace: kMaxHeads rows of d sums, then their m and l.
 __host__ __device__ constexpr size_t piece_floats(int d) { return (size_t)kMaxHeads * (d + 2); }
@@ -77,7 +86,7 @@ __device__ __forceinline__ int add_acq_rel(int* p, int v)
 }
 
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kDecThreads)
+__global__ void __launch_bounds__(kDecThreads, dec_ctas(D) / 152)
 paged_decode_kernel(const __grid_constant__ PagedArgs a)
 {
     using Cfg = DecCfg<D>;
@@ -471,27 +480,34 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
                 c0 = (int)(((done.first + 1) * C - 1) / U);
                 c1 = (int)(((done.first + done.nb) * C - 1) / U);
             }
-            if (tid == 0) {
-                int* counter = reinterpret_cast<int*>((unsigned char*)a.ws + kDecodeHead) + c0;
-                s_last = add_acq_rel(counter, 1) == c1 - c0;     // the block's stores before it, the other blocks' after it
-                if (s_last) *counter = 0;
-            }
-            __syncthreads();
-            if (s_last) {
-                // pieces in their order, so that it does not matter who joins them: 4 columns a thread, all rows at once
-                auto piece = [&](int x) { return pieces + (2 * (size_t)x + (x == c0 ? 1 : 0)) * PF; };
-                constexpr int TPR = D / 4;              // threads per row
+            // whether this CTA is the last of n at a counter; the counter is back at zero then
+            auto last_at = [&](int index, int n) {
+                __syncthreads();
+                if (tid == 0) {
+                    int* counter = reinterpret_cast<int*>((unsigned char*)a.ws + kDecodeHead) + index;
+                    s_last = add_acq_rel(counter, 1) == n - 1;   // the block's stores before it, the other blocks' after it
+                    if (s_last) *counter = 0;
+                }
+                __syncthreads();
+                return s_last != 0;
+            };
+            auto piece = [&](int x) { return pieces + (2 * (size_t)x + (x == c0 ? 1 : 0)) * PF; };
+            // joins pieces x0, x0 + step, ... (n of them) in their order, so that it does not matter who does it: four columns
+            // a thread, all rows at once; into the first one, or as the result
+            auto join = [&](int x0, int n, int step, bool result) {
+                constexpr int TPR = D / 4;              // threads per row, all of one warp
                 for (int h = tid / TPR; h < done.hn; h += kDecThreads / TPR) {
                     const int c = tid % TPR * 4;
                     float mh = -INFINITY, lh = 0.f;
                     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
                     // eight pieces at a time, all their loads in flight; past the last one the last one again, with weight 0
-                    for (int x0 = c0; x0 <= c1; x0 += 8) {
+#pragma unroll 1
+                    for (int i0 = 0; i0 < n; i0 += 8) {
                         float pm[8], ll[8];
                         float4 v[8];
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            const float* q = piece(min(x0 + j, c1));
+                            const float* q = piece(x0 + min(i0 + j, n - 1) * step);
                             pm[j] = __ldcg(q + kMaxHeads * D + h);
                             ll[j] = __ldcg(q + kMaxHeads * (D + 1) + h);
                             v[j] = __ldcg(reinterpret_cast<const float4*>(q + h * D + c));
@@ -505,7 +521,7 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
                         y.x *= g, y.y *= g, y.z *= g, y.w *= g;
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            const float f = pm[j] == -INFINITY || x0 + j > c1 ? 0.f : exp2_fast(pm[j] - mh);
+                            const float f = pm[j] == -INFINITY || i0 + j >= n ? 0.f : exp2_fast(pm[j] - mh);
                             lh = fmaf(f, ll[j], lh);
                             y.x = fmaf(f, v[j].x, y.x);
                             y.y = fmaf(f, v[j].y, y.y);
@@ -513,11 +529,37 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
                             y.w = fmaf(f, v[j].w, y.w);
                         }
                     }
-                    const float inv = lh > 0.f ? 1.f / lh : (lh == lh ? 0.f : lh);
-                    T* out = (T*)a.out + (size_t)done.b * a.p.out_stride + (size_t)(done.head0 + h) * D + c;
-                    *reinterpret_cast<uint2*>(out) = make_uint2(Num<T>::pack(y.x * inv, y.y * inv), Num<T>::pack(y.z * inv, y.w * inv));
-                    if (c == 0 && a.lse) a.lse[(size_t)done.b * a.p.Hq + done.head0 + h] = lse_of(mh, lh);
+                    if (result) {
+                        const float inv = lh > 0.f ? 1.f / lh : (lh == lh ? 0.f : lh);
+                        T* out = (T*)a.out + (size_t)done.b * a.p.out_stride + (size_t)(done.head0 + h) * D + c;
+                        *reinterpret_cast<uint2*>(out) = make_uint2(Num<T>::pack(y.x * inv, y.y * inv), Num<T>::pack(y.z * inv, y.w * inv));
+                        if (c == 0 && a.lse) a.lse[(size_t)done.b * a.p.Hq + done.head0 + h] = lse_of(mh, lh);
+                    } else {
+                        float* q = piece(x0);
+                        __syncwarp(__activemask());     // every thread of the row has read its m and l
+                        *reinterpret_cast<float4*>(q + h * D + c) = y;
+                        if (c == 0) {
+                            q[kMaxHeads * D + h] = mh;
+                            q[kMaxHeads * (D + 1) + h] = lh;
+                        }
+                    }
                 }
+            };
+            // (a CTA that begins one (request, heads) may also be within another: their counters lie apart)
+            const int n = c1 - c0 + 1, size = n <= kAtOnce ? kAtOnce : kGroup;
+            const int groups = (n + size - 1) / size, group = ((int)blockIdx.x - c0) / size;
+            int x0 = c0 + group * size, count = min(size, n - group * size), step = 1;
+            int index = group == 0 ? c0 : kCounters + x0;
+            bool result = groups == 1;
+#pragma unroll 1
+            while (last_at(index, count)) {
+                join(x0, count, step, result);
+                if (result) break;
+                result = true;
+                index = 2 * kCounters + c0;
+                x0 = c0;
+                count = groups;
+                step = size;
             }
             __syncthreads();                            // s_last is written again
         }

@@ -68,7 +68,7 @@ namespace paged {
 // that one workspace can serve both calls in turn: the prefill's first, then
 // (from kDecodeHead on) the counters of the single-token call, then what
 // either keeps only while it runs.
-constexpr size_t kDecodeHead = 4096, kHeadBytes = 8192;
+constexpr size_t kDecodeHead = 4096, kHeadBytes = 16384;
 
 constexpr float kLn2 = 0.693147180559945f;
 

@@ -295,6 +295,8 @@ DECODES = [
     dict(lens=[77, 300], Hq=40, Hkv=2, d=64, dt="f16", ps=64),            # two pieces a KV head
     dict(lens=[40, 90, 3], Hq=35, Hkv=5, d=64, dt="f16", ps=128, layout="token"),
     dict(lens=[9000], Hq=2, Hkv=1, d=128, dt="f16", ps=16),               # one request over many CTAs
+    dict(lens=[30000], Hq=1, Hkv=1, d=64, dt="bf16", ps=64),              # more pieces than are joined at once
+    dict(lens=[20000, 3, 9000], Hq=3, Hkv=1, d=128, dt="f16", ps=256),    # the same, in uneven shares
     dict(lens=[5000, 1, 0, 3000, 64], Hq=6, Hkv=2, d=128, dt="bf16", ps=1024),
     dict(lens=[100] * 150, Hq=3, Hkv=3, d=64, dt="f16", ps=16),           # more requests than threads
     dict(lens=EDGES + [500], Hq=6, Hkv=2, d=128, dt="f16", ps=16, window=40, sinks=0),
@@ -335,7 +337,7 @@ def test_paged_attend_without_lse_and_lengths_outside():
 def test_paged_attend_shares_one_workspace_and_repeats_bit_for_bit():
     """Calls of different shapes in turn on one workspace, each run again later: the same bits."""
     ws = torch.zeros(8 << 20, dtype=torch.uint8, device=DEV)
-    cases = [Case(**DECODES[i]) for i in (0, 6, 4, 10, 7)]
+    cases = [Case(**DECODES[i]) for i in (0, 6, 4, 12, 9, 7, 8)]
     first = [(c.run(ws).check().out.clone(), c.lse.clone()) for c in cases]
     for _ in range(3):
         for c, (o, l) in zip(cases, first):
@@ -384,7 +386,7 @@ def test_paged_prefill(i):
 def test_both_calls_share_one_workspace():
     """Single tokens and chunks, cut along their keys and not, in turn on one workspace: the same bits each time."""
     ws = torch.zeros(64 << 20, dtype=torch.uint8, device=DEV)
-    cases = [Case(**DECODES[0]), Case(**PREFILLS[17]), Case(**DECODES[6]), Case(**PREFILLS[2]), Case(**DECODES[10]), Case(**PREFILLS[18])]
+    cases = [Case(**DECODES[0]), Case(**PREFILLS[17]), Case(**DECODES[6]), Case(**PREFILLS[2]), Case(**DECODES[12]), Case(**PREFILLS[18]), Case(**DECODES[8])]
     first = [(c.run(ws).check().out.clone(), c.lse.clone()) for c in cases]
     for _ in range(2):
         for c, (o, l) in zip(cases, first):
