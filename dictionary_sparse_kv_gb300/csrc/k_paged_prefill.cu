@@ -16,7 +16,10 @@
 // row), the tensor cores work on the other tile: per 128 x 128 scores at d =
 // 128 the two products take 1024 cycles of a multiprocessor's tensor cores,
 // the exponentials 512 of its special-function units.  The tensor cores bound
-// it.
+// it: 8192 tokens of 24 heads over 8 of 128 in bfloat16 take 255 us, 1.6 PFLOP/s
+// (280 us, 1.5, in long runs under the power limit).  At d = 64 a step's
+// products take half as long as its softmax: 12001 tokens of 8 heads over 2,
+// window 1024, 57 us.
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 since
 // the last time (p then stays below 2^8, far inside both 16-bit types, and
@@ -32,7 +35,9 @@
 //
 // CTAs are persistent, one a multiprocessor, and take items (two tiles of one
 // request and KV head) from a counter, a request's last tiles, which see the
-// most keys, first.  The next item's queries and first pages are on their way
+// most keys, first, and several requests' tiles in turns of about as many keys,
+// the most first (lengths are known on the device alone, so every CTA walks
+// the requests by itself, a lane each).  The next item's queries and first pages are on their way
 // while the last tiles of the current one are worked on; only the reading of
 // O by the softmax warps stands between two items' products.
 //
@@ -42,8 +47,8 @@
 // workspace, and a second kernel joins them as
 //   m = max m_i,  l = sum 2^(m_i - m) l_i,  o = sum 2^(m_i - m) o_i.
 //
-// Warps: 0 TMA, 1 MMA, 2 TMEM and the items, 4..7 and 8..11 softmax of the two
-// tiles (3 only makes the count whole).  Every wait is bounded; one that runs out sets
+// Warps: 0 TMA, 1 MMA, 2 the items, 3 TMEM, 4..7 and 8..11 softmax of the two
+// tiles.  Every wait is bounded; one that runs out sets
 // FADKV_DEV_TIMEOUT in the workspace's first word, and the CTA drains and
 // returns.
 #include "paged.cuh"
@@ -70,6 +75,17 @@ constexpr int kItemReaders = 10;                   // warps that read an item
 constexpr int kMaxParts = 64;
 constexpr int kLeastTiles = 4;
 constexpr int kSplitSlots = 2 * kPreCtas;          // pieces of all items where items are cut
+
+// Turns in which the tiles of 2 to kSorted requests come, where they are more
+// than the multiprocessors (d = 128; in turns against request by request, us:
+// 16 requests of up to 300 tokens on 4000, 24 heads over 8: 59 against 74; 32 of
+// 64 on 8000: 103 against 119; 40 of 200 on 2000: 81 against 85; 8 of 500 on
+// 4000: 67.3 and 67.4.  Four turns: 60, 102, 81, 68.6; sixteen: 59, 103, 86, 68.1).
+// Every turn walks all requests, so many come one by one (in turns 70 of 64 on
+// 8000 take 189 against 214, 100 of 64 on 4000 166 and 171, but 200 of 20 on
+// 4000 262 against 256 and 500 of 16 on 1000 250 against 210).
+constexpr int kLevels = 8;
+constexpr int kSorted = 96;
 
 // Head of the workspace.
 struct PreHead {
@@ -274,31 +290,24 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     }
     // (waits only: blocks of the join that are let in early slow the last pieces down, 59 against 51 us for 84 tokens on 32768)
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // the items' warp reads its first requests meanwhile
-    int start = 0, cnt = 0, all = 0, upto = 0;         // its lane's request: first row, rows, rows before T is cut off, items up to it
+    // the items' warp reads its first requests meanwhile: a lane each, its first row, its rows, its rows before T is cut
+    // off, its tokens, its pairs of tiles
+    int start = 0, cnt = 0, all = 0, my_len = 0, tiles = 0;
     auto look = [&](int hi) {
         const int b = hi - lane;
-        cnt = start = all = 0;
+        cnt = start = all = my_len = 0;
         if (b >= 0) {
             start = __ldg(a.starts + b);
             const int stop = __ldg(a.starts + b + 1);
+            my_len = clamp_len(__ldg(a.lengths + b), a);
             if (start >= 0 && stop > start) {
                 all = stop - start;
                 cnt = max(0, min(stop, a.p.T) - start);
             }
         }
-        upto = (cnt + per_item - 1) / per_item;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o) upto += y;
-        }
+        tiles = (cnt + per_item - 1) / per_item;
     };
-    int my_len = 0;                                    // its request's tokens
-    if (warp == 2) {
-        look(a.p.B - 1);
-        my_len = a.p.B - 1 - lane >= 0 ? clamp_len(__ldg(a.lengths + a.p.B - 1 - lane), a) : 0;
-    }
+    if (warp == 2) look(a.p.B - 1);
     if (warp == 3) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_taddr)),
                      "r"(512));
@@ -532,47 +541,76 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         // ---------------- items ----------------
         // Item x is heads x % heads of tile x / heads, tiles counted from the last
         // request's last one.  Requests are looked at 32 at a time, a lane each.
+        // Several requests' tiles come in kLevels turns, those that see the most
+        // keys first, so that the multiprocessors end together.
         const int heads = a.p.Hkv * chunks;
+        const float inverse = 1.f / (float)per_item;
         int hi = a.p.B - 1;                                // lane l looks at request hi - l
-        long long base = 0;                                // tiles of the requests above hi
-        auto look_at = [&] {
-            look(hi);
-            my_len = hi - lane >= 0 ? clamp_len(__ldg(a.lengths + hi - lane), a) : 0;
+        long long base = 0;                                // tiles before the requests looked at
+        int level = 0, most = 0;                           // this turn (the last one: 0), the most keys of a tile
+        int t0 = 0, upto = 0;                              // of this lane's request: its first tile of the turn, tiles up to and with it
+        // how many of this lane's tiles come at this level or a later one: about those that see no more than so many keys
+        // (they grow with the positions, up to a window's)
+        auto below = [&](int lv) {
+            const int keys = (int)((long long)most * lv / kLevels), f = my_len - all;
+            if (f + cnt <= keys || (a.p.window > 0 && keys >= a.p.window)) return tiles;
+            return max(0, min(tiles - 1, (int)((float)(keys - f) * inverse)));
+        };
+        auto turn = [&] {
+            int t1 = tiles;
+            t0 = 0;
+            if (most > 0) {
+                if (level < kLevels - 1) t1 = below(level + 1);
+                if (level > 0) t0 = below(level);
+            }
+            upto = t1 - t0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += y;
+            }
         };
         Item it;
         unsigned int parts = 1;
-        if (a.split) {
-            // every CTA comes to the same number of parts
+        const bool sorted = a.p.B > 1 && a.p.B <= kSorted;
+        if (a.split || sorted) {
+            // every CTA comes to the same number of parts, and to the same order
             long long items = 0;
             int longest = 0;
             for (;;) {
-                items += __shfl_sync(0xffffffffu, upto, 31);
-                if (cnt > 0) {                                 // the request's last item sees the most keys
-                    const int t0 = (cnt - 1) / per_item * per_item;
+                items += __reduce_add_sync(0xffffffffu, tiles);
+                if (cnt > 0) most = max(most, a.p.window > 0 ? min(my_len, a.p.window) : my_len);
+                if (a.split && cnt > 0) {                      // the request's last item sees the most keys
+                    const int t = (cnt - 1) / per_item * per_item;
                     it.parts = 1;
                     it.len = my_len;
-                    it.first = my_len - all + t0;
-                    it.nt = cnt - t0;
+                    it.first = my_len - all + t;
+                    it.nt = cnt - t;
                     longest = max(longest, Tiles(it, a).count);
                 }
                 if (hi < 32) break;
                 hi -= 32;
-                look_at();
+                look(hi);
             }
             if (hi != a.p.B - 1) {
                 hi = a.p.B - 1;
-                look_at();
+                look(hi);
             }
             items *= heads;
-            for (int o = 16; o > 0; o >>= 1) longest = max(longest, __shfl_xor_sync(0xffffffffu, longest, o));
-            if (items > 0 && items <= kPreCtas)
-                parts = (unsigned int)max(1, min(min(kMaxParts, longest / kLeastTiles),
-                                                 (items <= kPreCtas / 2 ? kPreCtas : kSplitSlots) / (int)items));
-            if (blockIdx.x == 0 && lane == 0) {
-                head->parts = (int)parts;
-                head->items = (int)min(items, (long long)kPreCtas);
+            most = sorted && items > kPreCtas ? __reduce_max_sync(0xffffffffu, most) : 0;
+            if (most > 0) level = kLevels - 1;
+            if (a.split) {
+                longest = __reduce_max_sync(0xffffffffu, longest);
+                if (items > 0 && items <= kPreCtas)
+                    parts = (unsigned int)max(1, min(min(kMaxParts, longest / kLeastTiles),
+                                                     (items <= kPreCtas / 2 ? kPreCtas : kSplitSlots) / (int)items));
+                if (blockIdx.x == 0 && lane == 0) {
+                    head->parts = (int)parts;
+                    head->items = (int)min(items, (long long)kPreCtas);
+                }
             }
         }
+        turn();
         for (int n = 0; ok; ++n) {
             // the first one by the CTA's number, the others from the counter
             unsigned int x = blockIdx.x;
@@ -588,21 +626,26 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             while (hi >= 0 && u >= base + __shfl_sync(0xffffffffu, upto, 31)) {
                 base += __shfl_sync(0xffffffffu, upto, 31);
                 hi -= 32;
-                look_at();
+                if (hi < 0 && level > 0) {
+                    --level;
+                    hi = a.p.B - 1;
+                }
+                if (hi >= 0 && a.p.B > 32) look(hi);
+                turn();
             }
             it.live = hi >= 0;
             const int at = hi >= 0 ? __ffs(__ballot_sync(0xffffffffu, base + upto > u)) - 1 : 0;   // the lane whose request it is
-            const int t_end = (int)(base + __shfl_sync(0xffffffffu, upto, at) - u);                // tiles from this one to the request's first, this one included
+            const int t = __shfl_sync(0xffffffffu, t0, at) + (int)(base + __shfl_sync(0xffffffffu, upto, at) - u) - 1;
             const int rows = __shfl_sync(0xffffffffu, cnt, at), rows_all = __shfl_sync(0xffffffffu, all, at);
             const int s0 = __shfl_sync(0xffffffffu, start, at);
             it.len = __shfl_sync(0xffffffffu, my_len, at);
             if (it.live) {
-                const int t0 = (t_end - 1) * per_item;
+                const int row = t * per_item;
                 it.b = hi - at;
-                it.row0 = s0 + t0;
-                it.nt = min(per_item, rows - t0);
+                it.row0 = s0 + row;
+                it.nt = min(per_item, rows - row);
                 // positions by the rows that the request has, those cut off at T included
-                it.first = it.len - rows_all + t0;
+                it.first = it.len - rows_all + row;
                 it.hk = kvh / chunks;
                 const int h0 = (kvh % chunks) * gch;
                 it.head0 = it.hk * grp + h0;

@@ -383,6 +383,25 @@ def test_paged_prefill(i):
     Case(**PREFILLS[i]).run().check()
 
 
+# more tiles than multiprocessors and 2 to 96 requests: the tiles come by the keys that they see
+TURNS = [
+    dict(lens=[0, 900, 17, 300, 1000], new=[0, 400, 17, 350, 1], Hq=64, Hkv=1, d=64, dt="f16", ps=16),      # rows before token 0
+    dict(lens=[300, 2000], new=[300, 350], Hq=64, Hkv=1, d=128, dt="bf16", ps=32),
+    dict(lens=[700, 20, 1500], new=[300, 20, 400], Hq=64, Hkv=1, d=64, dt="f16", ps=16, window=200, sinks=7),
+    dict(lens=[40 + 37 * i % 400 for i in range(40)], new=[1 + 29 * i % 40 for i in range(40)], Hq=40, Hkv=5, d=128, dt="f16", ps=16,
+         window=100, sinks=3, layout="token"),
+    dict(lens=[(i > 2) * (60 + 61 * i % 500) for i in range(64)], new=[0] * 3 + [1 + 13 * i % 60 for i in range(61)], Hq=24, Hkv=4, d=64,
+         dt="bf16", ps=16, bad_pages=[(5, 0, -1), (60, 2, 10 ** 6)]),
+    dict(lens=[1 + 11 * i % 250 for i in range(96)], new=[1 + 7 * i % 30 for i in range(96)], Hq=16, Hkv=4, d=64, dt="f16", ps=16),
+    dict(lens=[0] * 33, new=[20] * 33, Hq=8, Hkv=8, d=64, dt="f16", ps=16),                                  # nothing is seen
+]
+
+
+@pytest.mark.parametrize("i", range(len(TURNS)))
+def test_paged_prefill_of_several_requests(i):
+    Case(**TURNS[i]).run().check()
+
+
 def test_both_calls_share_one_workspace():
     """Single tokens and chunks, cut along their keys and not, in turn on one workspace: the same bits each time."""
     ws = torch.zeros(64 << 20, dtype=torch.uint8, device=DEV)
