@@ -345,6 +345,11 @@ def _dtype(t) -> int:
     return {torch.float16: F16, torch.float32: F32, torch.bfloat16: BF16}[t.dtype]
 
 
+def _stride(x, i, dense):
+    """Stride of dimension i; `dense` where it has one element at most (torch may then say anything)."""
+    return x.stride(i) if x.shape[i] > 1 else dense
+
+
 def _pool(pages, layout):
     """(Hkv, page size, page stride, head stride, token stride) of a pool [pages][Hkv][page size][d] (layout
     "head") or [pages][page size][Hkv][d] ("token"); any strides with the last dimension contiguous."""
@@ -353,7 +358,8 @@ def _pool(pages, layout):
     h, t = (1, 2) if layout == "head" else (2, 1)
     if pages.dim() != 4 or pages.stride(3) != 1:
         raise ValueError("a pool has four dimensions, the last one contiguous")
-    return pages.shape[h], pages.shape[t], pages.stride(0), pages.stride(h), pages.stride(t)
+    d = pages.shape[3]
+    return pages.shape[h], pages.shape[t], _stride(pages, 0, d), _stride(pages, h, d), pages.stride(t)
 
 
 def page_params(B: int, page_size: int, num_pages: int, max_pages: int, max_tokens: int) -> PageParams:
@@ -398,8 +404,8 @@ def qk_params(q, k, v, q_out, k_pages, layout: str = "head", eps: float = 1e-6, 
         pages, kvt = k_pages.shape[0], _dtype(k_pages)
     if k.shape != (T, hkv, d) or v.shape != k.shape:
         raise ValueError("k and v are [T][Hkv][d], Hkv as in the pool")
-    return QkParams(T, Hq, hkv, d, _dtype(q), _dtype(q_out), kvt, ps, pages, eps, q.stride(0), k.stride(0), v.stride(0),
-                    *strides)
+    return QkParams(T, Hq, hkv, d, _dtype(q), _dtype(q_out), kvt, ps, pages, eps, _stride(q, 0, Hq * d),
+                    _stride(k, 0, hkv * d), _stride(v, 0, hkv * d), *strides)
 
 
 def qk_norm_rope(p: QkParams, rope: Rope, q, k, v, wq, wk, positions, slots, q_out, k_out, k_pages, v_pages,
@@ -427,7 +433,7 @@ def paged_params(q, out, k_pages, layout: str = "head", block_table=None, window
         if not block_table.is_contiguous():
             raise ValueError("block tables are contiguous")
     return PagedParams(B, T, Hq, hkv, d, _dtype(q), ps, k_pages.shape[0], max_pages, window, sinks,
-                       d ** -0.5 if scale is None else scale, q.stride(0), out.stride(0), *strides)
+                       d ** -0.5 if scale is None else scale, _stride(q, 0, Hq * d), _stride(out, 0, Hq * d), *strides)
 
 
 def paged_attend_workspace_bytes(p: PagedParams) -> int:

@@ -56,6 +56,23 @@ def test_page_plan_refusals(L, monkeypatch):
     assert _status(call) == 4 and "fadkv_page_plan" in F.last_error()
 
 
+def test_strides_of_single_rows_pages_and_heads(L):
+    """One row, page or head: torch's stride of that dimension says nothing and is not refused."""
+    torch = pytest.importorskip("torch")
+    d = 64
+    q = torch.zeros(4, 1, d, dtype=torch.float16).transpose(0, 1)           # [1][4][d], stride(0) = d
+    kv = torch.zeros(1, 2, d, dtype=torch.float16).as_strided((1, 2, d), (7, d, 1))
+    pool = torch.zeros(16 * 2 * d, dtype=torch.float16).as_strided((1, 2, 16, d), (3, 16 * d, d, 1))
+    p = F.qk_params(q, kv, kv, q, pool)
+    assert (p.q_stride, p.k_stride, p.v_stride, p.page_stride, p.head_stride, p.token_stride) == (4 * d, 2 * d, 2 * d, d, 16 * d, d)
+    table = torch.zeros(1, 1, dtype=torch.int32)
+    assert F.paged_attend_workspace_bytes(F.paged_params(q, q, pool, "head", table)) > 0
+    one_head = torch.zeros(3 * 16 * d, dtype=torch.float16).as_strided((3, 1, 16, d), (16 * d, 0, d, 1))
+    p = F.paged_params(q, q, one_head, "head", table)
+    assert p.q_stride == p.out_stride == 4 * d and (p.page_stride, p.head_stride) == (16 * d, d)
+    assert F.paged_prefill_workspace_bytes(p) > 0
+
+
 @pytest.mark.parametrize("scaling", ["plain", "linear", "stretch", "parts"])
 @pytest.mark.parametrize("rd", [16, 32, 128])
 def test_rope_table(L, scaling, rd):
