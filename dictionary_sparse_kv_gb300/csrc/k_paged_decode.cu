@@ -27,9 +27,13 @@
 // columns:
 //   S^T = K Q^T   [16 tokens][8 heads],   O^T += V^T P^T   [d][8 heads],
 // so a group of up to eight heads fills one instruction and nothing is padded
-// to 16 rows of queries.  P enters as two 16-bit terms (hi + lo): the tensor
-// pipe is idle most of the time here, and the output is then as exact as one
-// computed in 32 bits.
+// to 16 rows of queries.  P enters as two 16-bit terms (hi + lo), 22 bits of
+// it in binary16 and 16 in bfloat16: the tensor pipe is idle most of the time
+// here, and the rounding of the output is then all that can be seen of it.
+// Binary16 ends at 2^-24, and on a long cache many small p add up, so P (at
+// most 1) is multiplied by 2^15 for the product and the sums by 2^-15 when the
+// warps join: a p is lost below 2^-40, not 2^-25 (131072 keys 12.1 below one
+// whose value is 0 came out 0.3% small, 32768 keys 17.5 below it as 0).
 //
 // 64 requests of 16384 tokens, 32 heads over 8 of 128 in bfloat16: 0.32 ms,
 // 6.8 TB/s.  Few or short requests are bound by the chain lengths -> block
@@ -49,6 +53,9 @@ constexpr int kBlock = kTile * kDecWarps;          // tokens per unit of work
 // 14.7 us against 16.0 with two CTAs of six stages; d = 128 with three CTAs of two stages: 16 of 4096 34.8 against 27.7 us)
 __host__ __device__ constexpr int dec_ctas(int d) { return d == 128 ? 304 : 456; }
 constexpr int kMaxHeads = 16;                      // query heads per piece; larger groups are several pieces
+
+// What P is multiplied by for the product with V.
+template <typename T> constexpr float kUp = std::is_same<T, __half>::value ? 32768.f : 1.f;
 
 template <int D> struct DecCfg {
     static constexpr int STAGES = 3;
@@ -351,12 +358,13 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
                 const float p2 = exp2_fast(sc[n][2] - m0), p3 = exp2_fast(sc[n][3] - m1);
                 l[n][0] += p0 + p2;
                 l[n][1] += p1 + p3;
-                const uint32_t a0 = Num<T>::pack(p0, p1), a1 = Num<T>::pack(p2, p3);
+                const float e0 = p0 * kUp<T>, e1 = p1 * kUp<T>, e2 = p2 * kUp<T>, e3 = p3 * kUp<T>;
+                const uint32_t a0 = Num<T>::pack(e0, e1), a1 = Num<T>::pack(e2, e3);
                 const float2 r0 = Num<T>::unpack(a0), r1 = Num<T>::unpack(a1);
                 ph[n][0] = transpose8(a0);
                 ph[n][1] = transpose8(a1);
-                pl[n][0] = transpose8(Num<T>::pack(p0 - r0.x, p1 - r0.y));
-                pl[n][1] = transpose8(Num<T>::pack(p2 - r1.x, p3 - r1.y));
+                pl[n][0] = transpose8(Num<T>::pack(e0 - r0.x, e1 - r0.y));
+                pl[n][1] = transpose8(Num<T>::pack(e2 - r1.x, e3 - r1.y));
             }
             {
                 const int r = (lane & 7) + (lane >> 4) * 8, c = (lane >> 3) & 1;
@@ -424,6 +432,7 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
                 for (int x = 0; x < kDecWarps; ++x) {
                     f[x][i] = s_m[x][h] == -INFINITY ? 0.f : exp2_fast(s_m[x][h] - mh[i]);
                     lh[i] = fmaf(f[x][i], s_l[x][h], lh[i]);
+                    f[x][i] *= 1.f / kUp<T>;               // of the sums of p v
                 }
             }
 #pragma unroll
