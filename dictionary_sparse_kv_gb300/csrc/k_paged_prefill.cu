@@ -22,9 +22,12 @@
 // window 1024, 57 us.
 //
 // O is rescaled only when a row's maximum has grown by more than 2^8 since
-// the last time (p then stays below 2^8, far inside both 16-bit types, and
-// o / l is the same), which after the first tiles is rare; the rescale goes
-// through registers in the softmax warps.
+// the last time, which after the first tiles is rare (o / l is the same); the
+// rescale goes through registers in the softmax warps.  m need not be the
+// maximum itself: p = 2^(x - m) with m 7 below it in binary16, where p then
+// reaches 2^15 at most and is lost below 2^-25, that is 2^-32 of the largest
+// (with m the maximum 32768 keys 17.5 below one whose value is 0 came out as
+// 0).  bfloat16 has the exponents of 32 bits, and m is the maximum there.
 //
 // K and V pages come by TMA, one box a page and 64-element half, through one
 // ring of stages; pages outside the pool and pages that no row sees are asked
@@ -66,6 +69,7 @@ constexpr int kKeys = 128;                         // keys per tile
 constexpr int kOkRing = 16;                        // key tiles whose page masks are kept
 constexpr int kPart = 64;                          // keys whose P is handed over first; the rest follows
 constexpr float kGrow = 8.f;                       // growth of the maximum (log2) that rescales
+template <typename T> constexpr float kBelow = std::is_same<T, __half>::value ? 7.f : 0.f;   // m below the maximum (log2)
 
 constexpr int kPreCtas = 152;                      // one per multiprocessor
 constexpr int kItemReaders = 10;                   // warps that read an item
@@ -743,10 +747,11 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                                         __uint_as_float(s[c >> 1][(c & 1) * 16 + j + 1]));
                     mx = max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), fmaxf(x[6], x[7])) * scale;
                 }
-                const bool grow = mx > m + kGrow;
+                const bool grow = mx > m + (kGrow + kBelow<T>);
                 if (__any_sync(0xffffffffu, grow)) {
                     float f = 1.f;
                     if (grow) {
+                        mx -= kBelow<T>;
                         f = exp2_fast(m - mx);
                         m = mx;
                         l *= f;

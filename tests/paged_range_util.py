@@ -33,6 +33,11 @@ def STEPS_DECODE(n):
     return 2 * (n // 64 // 304 + 1) + 40
 
 
+def STEPS_PREFILL(n, cut):
+    """The same of a chunk's call: products of 16 keys, the whole length or (cut into 64 pieces) a piece and the joins."""
+    return n // 16 // 64 + 80 if cut else n // 16 + 16
+
+
 def exponent_error(drops):
     """Relative error of a probability 2^-X, X = drop log2(e): the scale's product and constant and the difference are
     rounded to 32 bits (4 x 2^-24 X), the exponential to two steps."""

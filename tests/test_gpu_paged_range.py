@@ -85,3 +85,19 @@ def test_paged_attend_multiplies_both_terms(dt, d, n):
     e = torch.finfo(TYPES[dt]).eps
     tol = R.two_term_bound(want, drops, n, e)
     assert (np.abs(out - want) <= tol).all(), (np.abs(out - want) / tol).max()
+
+
+PREFILL = [(131072, 3, (12.125, 5.0, 0.0)), (32768, 40, (15.25, 17.5, 14.875)), (1 << 20, 1, (16.5, 14.0, 15.0)),
+           (32768, 12800, (15.25, 17.5, 13.125))]                           # the last one: items are not cut
+
+
+@pytest.mark.parametrize("dt,d,ps,layout", [("f16", 128, 64, "head"), ("f16", 64, 32, "token"), ("bf16", 64, 128, "head")])
+@pytest.mark.parametrize("n,new,drops", PREFILL)
+def test_paged_prefill_keeps_small_probabilities(n, new, drops, dt, d, ps, layout):
+    out, lse, want, wl = _run(drops, n, new, d, dt, ps, layout)
+    steps = R.STEPS_PREFILL(n, new < 10000)
+    rel, e_lse = R.small_bounds(drops, n, steps, 2 ** -32.0 if dt == "f16" else 0.0)
+    e = torch.finfo(TYPES[dt]).eps
+    tol = np.abs(want) * (e + rel[None, :, None]) + 2.0 ** -25               # one rounding of out, one of each probability
+    assert (np.abs(out - want) <= tol).all(), (np.abs(out - want) / tol).max()
+    assert (np.abs(lse - wl) <= e_lse[None]).all()
