@@ -119,7 +119,7 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
 
     // blocks of a request: at least one, so that one which sees nothing is written too
     auto blocks_of = [&](const Seen& s) { return max(1, (s.count + kBlock - 1) / kBlock); };
-    auto blocks = [&](int b) { return blocks_of(seen_of(clamp_len(__ldg(a.lengths + b), a), a)); };
+    auto blocks = [&](int b) { return blocks_of(seen_of(length_of(b, b, a), a)); };
     long long u, u1, U, base;                                          // this CTA's units; all; the first of request cur_b
     int C, cur_b, longest, parts = 0;                                  // parts > 0: (request, heads) in so many equal parts
     // Equal parts: the lengths are within an eighth of the longest one on average, and the parts are at least three
@@ -189,7 +189,7 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
     auto next_work = [&] {
         Work w;
         w.b = cur_b;
-        w.seen = seen_of(clamp_len(__ldg(a.lengths + cur_b), a), a);
+        w.seen = seen_of(length_of(cur_b, cur_b, a), a);
         w.nb = blocks_of(w.seen);
         int seg;
         if (parts > 0) {

@@ -303,10 +303,10 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         if (b >= 0) {
             start = __ldg(a.starts + b);
             const int stop = __ldg(a.starts + b + 1);
-            my_len = clamp_len(__ldg(a.lengths + b), a);
-            if (start >= 0 && stop > start) {
+            if (start >= 0 && stop > start && start < a.p.T) {
                 all = stop - start;
-                cnt = max(0, min(stop, a.p.T) - start);
+                cnt = min(stop, a.p.T) - start;
+                my_len = length_of(b, start, a);
             }
         }
         tiles = (cnt + per_item - 1) / per_item;

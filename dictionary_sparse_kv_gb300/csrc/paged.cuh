@@ -52,6 +52,7 @@ struct PagedArgs {
     const int32_t* table;
     const int32_t* lengths;
     const int32_t* starts;
+    const int32_t* positions;   // or null
     const void* q;
     void* out;
     float* lse;
@@ -199,6 +200,13 @@ __device__ __forceinline__ int clamp_len(int len, const PagedArgs& a)
 {
     const int most = a.p.max_pages << a.shift;
     return len < 0 ? 0 : (len > most ? most : len);
+}
+// The tokens of request b, whose first row is `row` (below T): none for a
+// request that the plan refused, as its rows are not the last ones of those.
+__device__ __forceinline__ int length_of(int b, int row, const PagedArgs& a)
+{
+    const int pos = a.positions ? __ldg(a.positions + row) : 0, len = __ldg(a.lengths + b);
+    return pos < 0 ? 0 : clamp_len(len, a);
 }
 __device__ __forceinline__ Seen seen_of(int len, const PagedArgs& a)
 {

@@ -70,7 +70,8 @@ fadkv_status check_paged(const fadkv_paged_params* p)
 }
 
 PagedArgs paged_args(const fadkv_paged_params& p, const void* k, const void* v, const int32_t* table,
-                     const int32_t* lengths, const int32_t* starts, const void* q, void* out, float* lse, void* ws)
+                     const int32_t* lengths, const int32_t* starts, const int32_t* positions, const void* q, void* out,
+                     float* lse, void* ws)
 {
     PagedArgs a;
     a.p = p;
@@ -83,6 +84,7 @@ PagedArgs paged_args(const fadkv_paged_params& p, const void* k, const void* v, 
     a.table = table;
     a.lengths = lengths;
     a.starts = starts;
+    a.positions = positions;
     a.q = q;
     a.out = out;
     a.lse = lse;
@@ -239,8 +241,8 @@ namespace {
 
 fadkv_status paged_call(const char* name, bool prefill, const fadkv_paged_params* p, const void* k_pages,
                         const void* v_pages, const int32_t* block_table, const int32_t* lengths,
-                        const int32_t* starts, const void* q, void* out, float* lse, void* workspace,
-                        size_t workspace_bytes, void* stream)
+                        const int32_t* starts, const int32_t* positions, const void* q, void* out, float* lse,
+                        void* workspace, size_t workspace_bytes, void* stream)
 {
     const fadkv_status st = check_paged(p);
     if (st != FADKV_OK) return st;
@@ -253,11 +255,11 @@ fadkv_status paged_call(const char* name, bool prefill, const fadkv_paged_params
             (prefill && !starts))
             return FADKV_ERR_INVALID_ARG;
         if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(block_table, 4) || !aligned(lengths, 4) ||
-            !aligned(starts, 4) || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4))
+            !aligned(starts, 4) || !aligned(positions, 4) || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4))
             return FADKV_ERR_INVALID_ARG;
     }
     if (fault_injected()) return cuda_error(name, cudaErrorLaunchFailure);
-    const PagedArgs a = paged_args(*p, k_pages, v_pages, block_table, lengths, starts, q, out, lse, workspace);
+    const PagedArgs a = paged_args(*p, k_pages, v_pages, block_table, lengths, starts, positions, q, out, lse, workspace);
     const cudaError_t e = prefill ? launch_paged_prefill(a, (cudaStream_t)stream)
                                   : launch_paged_attend(a, (cudaStream_t)stream);
     return e == cudaSuccess ? FADKV_OK : cuda_error(name, e);
@@ -271,8 +273,17 @@ fadkv_status fadkv_paged_attend(const fadkv_paged_params* p, const void* k_pages
                                 const int32_t* block_table, const int32_t* lengths, const void* q, void* out,
                                 float* lse, void* workspace, size_t workspace_bytes, void* stream)
 {
-    return paged_call("fadkv_paged_attend", false, p, k_pages, v_pages, block_table, lengths, nullptr, q, out, lse,
-                      workspace, workspace_bytes, stream);
+    return paged_call("fadkv_paged_attend", false, p, k_pages, v_pages, block_table, lengths, nullptr, nullptr, q, out,
+                      lse, workspace, workspace_bytes, stream);
+}
+
+fadkv_status fadkv_paged_attend_planned(const fadkv_paged_params* p, const void* k_pages, const void* v_pages,
+                                        const int32_t* block_table, const int32_t* lengths, const int32_t* positions,
+                                        const void* q, void* out, float* lse, void* workspace,
+                                        size_t workspace_bytes, void* stream)
+{
+    return paged_call("fadkv_paged_attend_planned", false, p, k_pages, v_pages, block_table, lengths, nullptr,
+                      positions, q, out, lse, workspace, workspace_bytes, stream);
 }
 
 fadkv_status fadkv_paged_prefill(const fadkv_paged_params* p, const void* k_pages, const void* v_pages,
@@ -280,8 +291,17 @@ fadkv_status fadkv_paged_prefill(const fadkv_paged_params* p, const void* k_page
                                  const void* q, void* out, float* lse, void* workspace, size_t workspace_bytes,
                                  void* stream)
 {
-    return paged_call("fadkv_paged_prefill", true, p, k_pages, v_pages, block_table, lengths, starts, q, out, lse,
-                      workspace, workspace_bytes, stream);
+    return paged_call("fadkv_paged_prefill", true, p, k_pages, v_pages, block_table, lengths, starts, nullptr, q, out,
+                      lse, workspace, workspace_bytes, stream);
+}
+
+fadkv_status fadkv_paged_prefill_planned(const fadkv_paged_params* p, const void* k_pages, const void* v_pages,
+                                         const int32_t* block_table, const int32_t* lengths, const int32_t* starts,
+                                         const int32_t* positions, const void* q, void* out, float* lse,
+                                         void* workspace, size_t workspace_bytes, void* stream)
+{
+    return paged_call("fadkv_paged_prefill_planned", true, p, k_pages, v_pages, block_table, lengths, starts,
+                      positions, q, out, lse, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -96,27 +96,8 @@ static PyObject* qk_norm_rope(PyObject* self, PyObject* const* args, Py_ssize_t 
     return PyLong_FromLong(rc);
 }
 
-/* (function, params, 7 arrays, workspace, bytes, stream) */
-static PyObject* paged_attend(PyObject* self, PyObject* const* args, Py_ssize_t n)
-{
-    void *f, *p[8], *st;
-    const void* params;
-    (void)self;
-    if (arity(n, 12) || address(args[0], &f) || structure(args[1], sizeof(fadkv_paged_params), &params) ||
-        pointers(args + 2, 8, p) || address(args[11], &st))
-        return NULL;
-    const size_t bytes = PyLong_AsSize_t(args[10]);
-    if (PyErr_Occurred()) return NULL;
-    __typeof__(&fadkv_paged_attend) call = (__typeof__(&fadkv_paged_attend))f;
-    fadkv_status rc;
-    Py_BEGIN_ALLOW_THREADS
-    rc = call(params, p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], bytes, st);
-    Py_END_ALLOW_THREADS
-    return PyLong_FromLong(rc);
-}
-
 /* (function, params, 8 arrays, workspace, bytes, stream) */
-static PyObject* paged_prefill(PyObject* self, PyObject* const* args, Py_ssize_t n)
+static PyObject* paged_attend(PyObject* self, PyObject* const* args, Py_ssize_t n)
 {
     void *f, *p[9], *st;
     const void* params;
@@ -126,10 +107,29 @@ static PyObject* paged_prefill(PyObject* self, PyObject* const* args, Py_ssize_t
         return NULL;
     const size_t bytes = PyLong_AsSize_t(args[11]);
     if (PyErr_Occurred()) return NULL;
-    __typeof__(&fadkv_paged_prefill) call = (__typeof__(&fadkv_paged_prefill))f;
+    __typeof__(&fadkv_paged_attend_planned) call = (__typeof__(&fadkv_paged_attend_planned))f;
     fadkv_status rc;
     Py_BEGIN_ALLOW_THREADS
     rc = call(params, p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8], bytes, st);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+/* (function, params, 9 arrays, workspace, bytes, stream) */
+static PyObject* paged_prefill(PyObject* self, PyObject* const* args, Py_ssize_t n)
+{
+    void *f, *p[10], *st;
+    const void* params;
+    (void)self;
+    if (arity(n, 14) || address(args[0], &f) || structure(args[1], sizeof(fadkv_paged_params), &params) ||
+        pointers(args + 2, 10, p) || address(args[13], &st))
+        return NULL;
+    const size_t bytes = PyLong_AsSize_t(args[12]);
+    if (PyErr_Occurred()) return NULL;
+    __typeof__(&fadkv_paged_prefill_planned) call = (__typeof__(&fadkv_paged_prefill_planned))f;
+    fadkv_status rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = call(params, p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8], p[9], bytes, st);
     Py_END_ALLOW_THREADS
     return PyLong_FromLong(rc);
 }

@@ -146,8 +146,10 @@ _SIGS = {
     "fadkv_rope_init": ([C.POINTER(RopeParams), C.POINTER(Rope)], C.c_int),
     "fadkv_qk_norm_rope": ([C.POINTER(QkParams), C.POINTER(Rope)] + [C.c_void_p] * 12, C.c_int),
     "fadkv_paged_attend": ([C.POINTER(PagedParams)] + [C.c_void_p] * 8 + [C.c_size_t, C.c_void_p], C.c_int),
+    "fadkv_paged_attend_planned": ([C.POINTER(PagedParams)] + [C.c_void_p] * 9 + [C.c_size_t, C.c_void_p], C.c_int),
     "fadkv_paged_attend_workspace_bytes": ([C.POINTER(PagedParams), C.POINTER(C.c_size_t)], C.c_int),
     "fadkv_paged_prefill": ([C.POINTER(PagedParams)] + [C.c_void_p] * 9 + [C.c_size_t, C.c_void_p], C.c_int),
+    "fadkv_paged_prefill_planned": ([C.POINTER(PagedParams)] + [C.c_void_p] * 10 + [C.c_size_t, C.c_void_p], C.c_int),
     "fadkv_paged_prefill_workspace_bytes": ([C.POINTER(PagedParams), C.POINTER(C.c_size_t)], C.c_int),
     "fadkv_profile_enable": ([C.c_void_p, C.c_int32], C.c_int),
     "fadkv_profile_select": ([C.c_void_p, C.c_uint32], C.c_int),
@@ -193,8 +195,9 @@ def _load_calls():
             loader = importlib.machinery.ExtensionFileLoader("_fadkv_calls", CALLS_PATH)
             m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fadkv_calls", loader))
             loader.exec_module(m)
-            for name in ("page_plan", "qk_norm_rope", "paged_attend", "paged_prefill"):
-                _direct[name] = C.cast(getattr(L, "fadkv_" + name), C.c_void_p).value
+            for name, function in (("page_plan", "page_plan"), ("qk_norm_rope", "qk_norm_rope"),
+                                   ("paged_attend", "paged_attend_planned"), ("paged_prefill", "paged_prefill_planned")):
+                _direct[name] = C.cast(getattr(L, "fadkv_" + function), C.c_void_p).value
             _calls = m
     return _calls
 
@@ -452,21 +455,25 @@ def _nbytes(workspace) -> int:
     return 0 if workspace is None else workspace.nbytes
 
 
-def paged_attend(p: PagedParams, k_pages, v_pages, block_table, lengths, q, out, lse, workspace, stream=None) -> None:
+def paged_attend(p: PagedParams, k_pages, v_pages, block_table, lengths, q, out, lse, workspace, stream=None,
+                 positions=None) -> None:
     """Attention of one new token per request over the pages (see fadkv_paged_attend).  The workspace is
-    zero-filled before its first use."""
-    rc = (_calls or _load_calls()).paged_attend(_direct["paged_attend"], p, k_pages, v_pages, block_table, lengths, q, out,
-                                                lse, workspace, _nbytes(workspace), _stream(stream, q, out))
+    zero-filled before its first use.  With a plan's positions, requests that it refused see nothing
+    (fadkv_paged_attend_planned)."""
+    rc = (_calls or _load_calls()).paged_attend(_direct["paged_attend"], p, k_pages, v_pages, block_table, lengths, positions, q,
+                                                out, lse, workspace, _nbytes(workspace), _stream(stream, q, out))
     if rc:
         _check("fadkv_paged_attend", rc)
 
 
 def paged_prefill(p: PagedParams, k_pages, v_pages, block_table, lengths, starts, q, out, lse=None, workspace=None,
-                  stream=None) -> None:
+                  stream=None, positions=None) -> None:
     """Attention of each request's last tokens over the pages (see fadkv_paged_prefill).  The workspace is
-    zero-filled before its first use."""
+    zero-filled before its first use.  With a plan's positions, requests that it refused see nothing
+    (fadkv_paged_prefill_planned)."""
     rc = (_calls or _load_calls()).paged_prefill(_direct["paged_prefill"], p, k_pages, v_pages, block_table, lengths, starts,
-                                                 q, out, lse, workspace, _nbytes(workspace), _stream(stream, q, out))
+                                                 positions, q, out, lse, workspace, _nbytes(workspace),
+                                                 _stream(stream, q, out))
     if rc:
         _check("fadkv_paged_prefill", rc)
 

@@ -76,12 +76,12 @@ class Layer:
         self.dict.step(x, c)
         F.store_codes(2, self.R, HKV, TERMS, N_ATOMS, c.idx, c.coef, c.repl_id, c.repl_coef, pos, self.cache, self.longest)
 
-    def attend(self, q, window=0, sinks=0):
-        """One query token a request over the pages."""
+    def attend(self, q, window=0, sinks=0, positions=None):
+        """One query token a request over the pages; with the step's positions, requests that its plan refused see nothing."""
         out = torch.empty_like(q)
         p = F.paged_params(q, out, self.k_pages, "head", self.table, window, sinks)
         ws = self.workspace("decode", F.paged_attend_workspace_bytes(p))
-        F.paged_attend(p, self.k_pages, self.v_pages, self.table, self.lengths, q, out, None, ws)
+        F.paged_attend(p, self.k_pages, self.v_pages, self.table, self.lengths, q, out, None, ws, positions=positions)
         return out
 
     def prefill(self, q, window=0, sinks=0):
@@ -89,7 +89,8 @@ class Layer:
         out = torch.empty_like(q)
         p = F.paged_params(q, out, self.k_pages, "head", self.table, window, sinks)
         ws = self.workspace("prefill", F.paged_prefill_workspace_bytes(p))
-        F.paged_prefill(p, self.k_pages, self.v_pages, self.table, self.lengths, self.starts, q, out, None, ws)
+        F.paged_prefill(p, self.k_pages, self.v_pages, self.table, self.lengths, self.starts, q, out, None, ws,
+                        positions=self.positions)
         return out
 
     def attend_codes(self, q):
@@ -127,8 +128,9 @@ def main(argv=None):
     for _ in range(a.steps):
         q, k, v = layer.append(one)
         layer.code(k, v, layer.lengths - 1)
-        full = layer.attend(q).float()
-        for name, other in (("window", layer.attend(q, a.window, a.sinks).float()), ("codes", layer.attend_codes(q))):
+        full = layer.attend(q, positions=layer.positions).float()
+        recent = layer.attend(q, a.window, a.sinks, layer.positions).float()
+        for name, other in (("window", recent), ("codes", layer.attend_codes(q))):
             diff.setdefault(name, []).append(((other - full).norm() / full.norm()).item())
     torch.cuda.synchronize()
     result = {"tokens": layer.lengths.tolist(), "refused": int(layer.refused), "pages left": int(layer.free_count),

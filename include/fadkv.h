@@ -562,6 +562,15 @@ fadkv_status fadkv_paged_attend(const fadkv_paged_params* params, const void* k_
                                 const int32_t* block_table, const int32_t* lengths, const void* q, void* out,
                                 float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
+/* The same after a plan: positions [T] as fadkv_page_plan writes them (or
+   null: none refused).  A request whose row has a negative position was
+   refused in this step; its lengths entry is that of the tokens before, which
+   the row does not follow.  It sees nothing (out = 0, lse = -inf). */
+fadkv_status fadkv_paged_attend_planned(const fadkv_paged_params* params, const void* k_pages, const void* v_pages,
+                                        const int32_t* block_table, const int32_t* lengths,
+                                        const int32_t* positions, const void* q, void* out, float* lse,
+                                        void* workspace, size_t workspace_bytes, void* stream);
+
 /* Device workspace fadkv_paged_attend needs (host-only; writes *bytes).
    Errors: INVALID_ARG, UNSUPPORTED. */
 fadkv_status fadkv_paged_attend_workspace_bytes(const fadkv_paged_params* params, size_t* bytes);
@@ -573,7 +582,9 @@ fadkv_status fadkv_paged_attend_workspace_bytes(const fadkv_paged_params* params
      starts      [B+1] int32 as fadkv_page_plan writes them: 0, ascending; rows
                  at and past T are left out.  Rows of q past starts[B] are not
                  read and their out and lse not written.
-   Rows at a negative position see nothing (out = 0, lse = -inf).  What the
+   Rows whose position lengths[b] - n + i is negative see nothing (out = 0,
+   lse = -inf).  The rows of a request that a plan refused are not its last
+   tokens: use fadkv_paged_prefill_planned, or give it a length of 0.  What the
    pools hold where no row sees it is never used; a value that is not finite
    and that one row sees may reach other rows of its request.  The
    probabilities enter the product with the values in the type of the pools.
@@ -587,6 +598,14 @@ fadkv_status fadkv_paged_prefill(const fadkv_paged_params* params, const void* k
                                  const int32_t* block_table, const int32_t* lengths, const int32_t* starts,
                                  const void* q, void* out, float* lse, void* workspace,
                                  size_t workspace_bytes, void* stream);
+
+/* The same after a plan: positions [T] as fadkv_page_plan writes them (or
+   null: none refused).  A request whose first row has a negative position was
+   refused in this step: its rows see nothing (out = 0, lse = -inf). */
+fadkv_status fadkv_paged_prefill_planned(const fadkv_paged_params* params, const void* k_pages, const void* v_pages,
+                                         const int32_t* block_table, const int32_t* lengths, const int32_t* starts,
+                                         const int32_t* positions, const void* q, void* out, float* lse,
+                                         void* workspace, size_t workspace_bytes, void* stream);
 fadkv_status fadkv_paged_prefill_workspace_bytes(const fadkv_paged_params* params, size_t* bytes);
 
 /* Kernel classes reported by fadkv_profile_read. */
