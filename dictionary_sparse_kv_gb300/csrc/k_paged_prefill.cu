@@ -53,7 +53,8 @@
 // Warps: 0 TMA, 1 MMA, 2 the items, 3 TMEM, 4..7 and 8..11 softmax of the two
 // tiles.  Every wait is bounded; one that runs out sets
 // FADKV_DEV_TIMEOUT in the workspace's first word, and the CTA drains and
-// returns.
+// returns: the copies, the products and the stores to TMEM that its warps
+// issued are waited for before TMEM is given back.
 #include "paged.cuh"
 #include "tc_common.cuh"
 
@@ -98,14 +99,14 @@ struct PreHead {
     int parts, items;                              // of this call, for the join
     struct { int row0, nt, head0, hn; } item[kPreCtas];
 };
-static_assert(sizeof(PreHead) <= kDecodeHead, "workspace head");
+static_assert(sizeof(PreHead) <= kDecodeHead && offsetof(PreHead, status) == 0, "workspace head");
 __host__ __device__ constexpr size_t slot_floats(int d) { return (size_t)kRows * (d + 2); }   // a tile's rows: o by column, m, l
 
 template <int D> struct PreCfg {
     static constexpr int NST = D == 128 ? 5 : 8;   // stages of the K / V ring
     static constexpr int TILE = kRows * D * 2;     // bytes of a Q, K or V tile
     static constexpr int bar_off = (2 + NST) * TILE;
-    static constexpr int n_bars = 2 * NST + 18;
+    static constexpr int n_bars = 2 * NST + 19;
     static constexpr int ok_off = bar_off + n_bars * 8;
     static constexpr int alloc = ok_off + kOkRing * 20 + 16 + 1024;
     static_assert(alloc <= 227 * 1024 - 256, "shared memory");
@@ -264,7 +265,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     auto qfull = [&](int q) { return bar(8 + q); };
     auto qempty = [&](int q) { return bar(10 + q); };
     auto pfull = [&](int q, int part) { return bar(12 + 2 * q + part); };
-    const uint32_t ifull = bar(16), iempty = bar(17);
+    const uint32_t ifull = bar(16), iempty = bar(17), drained = bar(18);
     PreHead* head = reinterpret_cast<PreHead*>(a.ws);
     unsigned long long* status = &head->status;
 
@@ -290,6 +291,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         }
         mbar_init(ifull, 1);
         mbar_init(iempty, kItemReaders);
+        mbar_init(drained, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     // (waits only: blocks of the join that are let in early slow the last pieces down, 59 against 51 us for 84 tokens on 32768)
@@ -324,7 +326,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
 
     bool ok = true;                                    // no wait of this warp has run out
     auto wait = [&](uint32_t b, uint32_t parity) {
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(b, parity, status));
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(b, parity, status, a.wait_ns));
         return ok;
     };
     // the n-th item of this CTA, read by a whole warp; false when there is none.  The TMA warp hands the slot back
@@ -534,11 +536,10 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             }
             for (int q = 0; q < nq; ++q) ++uses[q];
         }
-        // drain: the last products of each tile are complete before TMEM is freed
-        for (int q = 0; q < 2; ++q) {
-            if (qks[q] > 0) mbar_wait(sfull(q), (uint32_t)(qks[q] - 1) & 1u, status);
-            if (pvs[q] > 0) mbar_wait(pvdone(q), (uint32_t)(pvs[q] - 1) & 1u, status);
-        }
+        // drain: every product that was issued (after a wait that ran out that may be half of a tile's, which no other
+        // barrier tells of) is complete before TMEM is freed
+        if (leader) mma_commit(drained);
+        mbar_wait(drained, 0u, status);
         __syncwarp();
     } else if (warp == 2) {
         regs_dec();
@@ -874,6 +875,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                     if (orow[k]) *reinterpret_cast<uint4*>(orow[k] + c * 32) = make_uint4(v[k][0], v[k][1], v[k][2], v[k][3]);
             }
         }
+        if (!ok) tmem_st_wait();                       // drain: as above, but that nothing waited for these
     }
 
     fence_before();
@@ -1011,6 +1013,7 @@ cudaError_t launch_t(const PagedArgs& args, cudaStream_t st)
     PagedArgs a = args;
     const PreShape s = pre_shape(a.p);
     a.split = s.split;
+    a.wait_ns = a.wait_ns ? a.wait_ns : kWaitNs;
     CUtensorMap mq, mk, mv;
     if (!query_map(&mq, a, s.gch, s.tq) || !pool_map(&mk, a.k, a) || !pool_map(&mv, a.v, a)) return cudaErrorInvalidValue;
     if (s.items > 0x7fffffffll) return cudaErrorInvalidValue;

@@ -46,6 +46,7 @@ struct PagedArgs {
     fadkv_paged_params p;
     int shift, grp;           // page_size = 1 << shift; query heads per KV head
     int split;                // prefill: whether items may be cut along their keys (the launcher sets it)
+    unsigned long long wait_ns;   // prefill: limit of the waits (0: the launcher sets the default)
     float scale_log2;         // scale * log2(e): scores in units of powers of two
     const void* k;
     const void* v;

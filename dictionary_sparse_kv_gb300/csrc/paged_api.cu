@@ -5,11 +5,15 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <atomic>
+
 #include "paged.cuh"
 
 using namespace fadkv;
 
 namespace {
+
+std::atomic<uint64_t> g_wait_ns{0};    // fadkv_debug_paged_wait_limit
 
 bool aligned(const void* ptr, size_t a) { return ((uintptr_t)ptr % a) == 0; }
 
@@ -78,6 +82,7 @@ PagedArgs paged_args(const fadkv_paged_params& p, const void* k, const void* v, 
     a.shift = log2_exact(p.page_size);
     a.grp = p.Hq / p.Hkv;
     a.split = 0;
+    a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
     a.scale_log2 = p.scale * 1.44269504088896f;
     a.k = k;
     a.v = v;
@@ -232,6 +237,23 @@ fadkv_status fadkv_paged_prefill_workspace_bytes(const fadkv_paged_params* p, si
     if (st != FADKV_OK) return st;
     if (!bytes) return FADKV_ERR_INVALID_ARG;
     *bytes = paged_prefill_workspace(*p);
+    return FADKV_OK;
+}
+
+fadkv_status fadkv_paged_status(void* workspace, uint64_t* host_out, int32_t clear, void* stream)
+{
+    if (!workspace || !aligned(workspace, 256) || !host_out) return FADKV_ERR_INVALID_ARG;
+    if (fault_injected()) return cuda_error("fadkv_paged_status", cudaErrorLaunchFailure);
+    cudaStream_t st = (cudaStream_t)stream;
+    cudaError_t e = cudaMemcpyAsync(host_out, workspace, sizeof(uint64_t), cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess && clear) e = cudaMemsetAsync(workspace, 0, sizeof(uint64_t), st);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+    return e == cudaSuccess ? FADKV_OK : cuda_error("fadkv_paged_status", e);
+}
+
+fadkv_status fadkv_debug_paged_wait_limit(uint64_t limit_ns)
+{
+    g_wait_ns.store(limit_ns, std::memory_order_relaxed);
     return FADKV_OK;
 }
 

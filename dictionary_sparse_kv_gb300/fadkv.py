@@ -28,6 +28,7 @@ STATS_FIELDS = 8
 STATS_NAMES = ("encoded", "replaced", "flagged", "overflow", "nonfinite", "topn_slow_path", "status", "reserved")
 DEV_NONFINITE_INPUT = 0x1
 DEV_NOT_SPD = 0x2
+DEV_TIMEOUT = 0x4
 MAX_DICTS = 256
 
 STATUS = {0: "FADKV_OK", 1: "FADKV_ERR_INVALID_ARG", 2: "FADKV_ERR_UNSUPPORTED", 3: "FADKV_ERR_SEQUENCE",
@@ -151,6 +152,8 @@ _SIGS = {
     "fadkv_paged_prefill": ([C.POINTER(PagedParams)] + [C.c_void_p] * 9 + [C.c_size_t, C.c_void_p], C.c_int),
     "fadkv_paged_prefill_planned": ([C.POINTER(PagedParams)] + [C.c_void_p] * 10 + [C.c_size_t, C.c_void_p], C.c_int),
     "fadkv_paged_prefill_workspace_bytes": ([C.POINTER(PagedParams), C.POINTER(C.c_size_t)], C.c_int),
+    "fadkv_paged_status": ([C.c_void_p, C.POINTER(C.c_uint64), C.c_int32, C.c_void_p], C.c_int),
+    "fadkv_debug_paged_wait_limit": ([C.c_uint64], C.c_int),
     "fadkv_profile_enable": ([C.c_void_p, C.c_int32], C.c_int),
     "fadkv_profile_select": ([C.c_void_p, C.c_uint32], C.c_int),
     "fadkv_profile_read": ([C.c_void_p, C.POINTER(C.c_int64), C.POINTER(C.c_double), C.c_int32], C.c_int),
@@ -476,6 +479,20 @@ def paged_prefill(p: PagedParams, k_pages, v_pages, block_table, lengths, starts
                                                  _stream(stream, q, out))
     if rc:
         _check("fadkv_paged_prefill", rc)
+
+
+def paged_status(workspace, clear: bool = True, stream=None) -> int:
+    """The status word of a paged_prefill workspace (DEV_TIMEOUT: a call on it gave up and its out is not complete), read
+    and, with clear, zeroed; synchronises the stream."""
+    word = C.c_uint64(0)
+    _check("fadkv_paged_status", lib().fadkv_paged_status(_addr(workspace), C.byref(word), 1 if clear else 0,
+                                                          _stream(stream, workspace)))
+    return word.value
+
+
+def debug_paged_wait_limit(limit_ns: int) -> None:
+    """Test hook: limit of the pipeline's waits of paged_prefill calls from now on (0 = default)."""
+    _check("fadkv_debug_paged_wait_limit", lib().fadkv_debug_paged_wait_limit(int(limit_ns)))
 
 
 def reconstruct(h: int, V: int, idx, coef, repl_id, repl_coef, xhat, stream=None) -> None:

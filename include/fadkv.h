@@ -592,7 +592,7 @@ fadkv_status fadkv_paged_attend_workspace_bytes(const fadkv_paged_params* params
                ZERO-FILLED before its first use.  Its first 8 bytes are a
                status word: FADKV_DEV_TIMEOUT is set in it if a kernel gave
                up waiting on its own pipeline (that call's out is then not
-               complete)
+               complete).  No call clears it: fadkv_paged_status reads it
    Other arguments and errors as for fadkv_paged_attend. */
 fadkv_status fadkv_paged_prefill(const fadkv_paged_params* params, const void* k_pages, const void* v_pages,
                                  const int32_t* block_table, const int32_t* lengths, const int32_t* starts,
@@ -606,6 +606,19 @@ fadkv_status fadkv_paged_prefill_planned(const fadkv_paged_params* params, const
                                          const int32_t* block_table, const int32_t* lengths, const int32_t* starts,
                                          const int32_t* positions, const void* q, void* out, float* lse,
                                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* The status word of a workspace of fadkv_paged_prefill, copied to HOST memory
+   *host_out and, if clear is set, zeroed; synchronises the stream.  A kernel
+   that gave up has waited for every copy and product that it issued and left
+   the workspace fit for the next call.
+   Errors: INVALID_ARG, CUDA. */
+fadkv_status fadkv_paged_status(void* workspace, uint64_t* host_out, int32_t clear, void* stream);
+
+/* Test hook: the wall-clock limit, in nanoseconds, of the waits inside the
+   pipeline of the fadkv_paged_prefill calls made from now on, in the whole
+   process (0 = the default, 200 ms).  Host-only. */
+fadkv_status fadkv_debug_paged_wait_limit(uint64_t limit_ns);
+
 fadkv_status fadkv_paged_prefill_workspace_bytes(const fadkv_paged_params* params, size_t* bytes);
 
 /* Kernel classes reported by fadkv_profile_read. */

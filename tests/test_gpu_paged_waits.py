@@ -1,0 +1,76 @@
+"""The bounded waits of the prefill over pages, made to run out (needs a GPU).
+
+The limit is set to one nanosecond, so that waits give up while copies and
+products are in flight.  The kernel still waits for those (with the full
+limit), gives its tensor memory back and leaves the workspace's counters at
+zero: no CUDA error, the status word says what happened, and the next call on
+the workspace is right.
+"""
+import pytest
+
+from tests.test_gpu_paged import DEV, PREFILLS, TURNS, Case, _i32
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from dictionary_sparse_kv_gb300 import build as B
+    from dictionary_sparse_kv_gb300 import fadkv as F
+    B.build()
+    yield
+    F.debug_paged_wait_limit(0)
+
+
+def _long(length, new, others, d, dt, ps=1024):
+    """One request of `length` tokens (one page over and over) and `others` of one token: q, out, lse, pools, tables."""
+    B, T, Hq = 1 + others, new + others, 2
+    g = torch.Generator(device=DEV).manual_seed(d)
+    k, v = (torch.randn((2, 1, ps, d), generator=g, device=DEV).to(dt) for _ in range(2))
+    q = torch.randn((T, Hq, d), generator=g, device=DEV).to(dt)
+    table = torch.ones((B, -(-length // ps)), dtype=torch.int32, device=DEV)
+    lens, starts = _i32([length] + [1] * others), _i32([0] + [new + i for i in range(others + 1)])
+    return q, torch.full_like(q, 9), torch.full((T, Hq), 9.0, device=DEV), k, v, table, lens, starts
+
+
+@pytest.mark.parametrize("d,dt", [(128, torch.float16), (64, torch.bfloat16)])
+@pytest.mark.parametrize("length,new,others", [(1 << 20, 300, 256), (1 << 25, 3, 0), (1 << 25, 90, 0)])
+def test_waits_run_out_drain_and_the_workspace_recovers(length, new, others, d, dt):
+    """More than 256 requests: items are walked whole; fewer: cut into 64 pieces and joined.  A wait gives up after 256
+    looks at its barrier at least, so each item or piece is some thousand key tiles, several milliseconds, long."""
+    from dictionary_sparse_kv_gb300 import fadkv as F
+    q, out, lse, k, v, table, lens, starts = _long(length, new, others, d, dt)
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device=DEV)
+    p = F.paged_params(q, out, k, "head", table)
+    call = lambda: F.paged_prefill(p, k, v, table, lens, starts, q, out, lse, ws)
+    call()
+    assert F.paged_status(ws) == 0
+    want, wl = out.clone(), lse.clone()
+    F.debug_paged_wait_limit(1)
+    for _ in range(3):
+        call()
+    assert F.paged_status(ws, clear=False) == F.DEV_TIMEOUT
+    assert F.paged_status(ws) == F.DEV_TIMEOUT and F.paged_status(ws) == 0
+    F.debug_paged_wait_limit(0)
+    out.fill_(5), lse.fill_(5)
+    call()
+    assert F.paged_status(ws) == 0
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+
+
+def test_short_calls_with_waits_that_give_up():
+    """Waits of these may or may not run out; either way nothing faults and the workspace stays fit."""
+    from dictionary_sparse_kv_gb300 import fadkv as F
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device=DEV)
+    cases = [Case(**PREFILLS[i]) for i in (2, 3, 6, 10, 17, 18)] + [Case(**TURNS[i]) for i in (0, 3)]
+    F.debug_paged_wait_limit(1)
+    for c in cases:
+        c.run(ws)
+    assert F.paged_status(ws) in (0, F.DEV_TIMEOUT)
+    F.debug_paged_wait_limit(0)
+    for c in cases:
+        c.out.fill_(5), c.lse.fill_(5)
+        c.run(ws).check()

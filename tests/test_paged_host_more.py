@@ -33,3 +33,13 @@ def test_planned_calls_refuse(L, name, arrays, positions, monkeypatch):
     monkeypatch.setenv("FADKV_FAULT", "cuda")
     assert fn(C.byref(_paged()), *[FAKE] * (arrays + 1), 1 << 30, None) == 4
     assert f"fadkv_paged_{name}_planned" in F.last_error()
+
+
+def test_status_refusals(L, monkeypatch):
+    word = C.c_uint64(7)
+    for ws in (None, FAKE + 16):
+        assert L.fadkv_paged_status(ws, C.byref(word), 1, None) == 1
+    assert L.fadkv_paged_status(FAKE, None, 1, None) == 1
+    monkeypatch.setenv("FADKV_FAULT", "cuda")
+    assert L.fadkv_paged_status(FAKE, C.byref(word), 1, None) == 4 and "fadkv_paged_status" in F.last_error()
+    assert word.value == 7
