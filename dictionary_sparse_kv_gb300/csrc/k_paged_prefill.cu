@@ -75,6 +75,11 @@ template <typename T> constexpr float kBelow = std::is_same<T, __half>::value ? 
 constexpr int kPreCtas = 152;                      // one per multiprocessor
 constexpr int kItemReaders = 10;                   // warps that read an item
 
+// Waits for the next item last as long as the current one: a key tile takes
+// 0.7 to 1.3 us, so that the 200 ms of a wait are over after 20 to 35 million keys.
+// Those waits get this much more for each tile of the item.
+constexpr unsigned int kTileNs = 8000;
+
 // Pieces of an item: at most so many, and none shorter than so many key tiles
 // (a piece costs about two tiles' time to begin, write out and join).
 constexpr int kMaxParts = 64;
@@ -252,6 +257,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint32_t s_taddr;
     __shared__ Item s_item;
+    __shared__ unsigned long long s_item_ns;           // what waits for the end of this item are given
     unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sQ = smem_u32(smem), sR = sQ + 2 * TILE, bar0 = sQ + C::bar_off;
     uint32_t* ok_ring = reinterpret_cast<uint32_t*>(smem + C::ok_off);   // [kOkRing][5]: all ok, four words of key bits
@@ -292,6 +298,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
         mbar_init(ifull, 1);
         mbar_init(iempty, kItemReaders);
         mbar_init(drained, 1);
+        s_item_ns = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     // (waits only: blocks of the join that are let in early slow the last pieces down, 59 against 51 us for 84 tokens on 32768)
@@ -333,7 +340,9 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     // only after its last load for the item: the next one is then taken, late enough for an even share of a short
     // list and early enough to be hidden behind the tiles in flight.
     auto next_item = [&](int n, Item& it) {
-        if (!wait(ifull, (uint32_t)n & 1u)) return false;
+        const unsigned long long limit = a.wait_ns + *(volatile unsigned long long*)&s_item_ns;
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(ifull, (uint32_t)n & 1u, status, limit));
+        if (!ok) return false;
         it = s_item;
         __syncwarp();
         if (warp != 0 && lane == 0) mbar_arrive(iempty);
@@ -656,6 +665,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 it.head0 = it.hk * grp + h0;
                 it.hn = min(gch, grp - h0);
             }
+            const unsigned long long item_ns = it.live ? (unsigned long long)Tiles(it, a).count * a.tile_ns : 0ull;
             if (lane == 0) {
                 if (it.live && it.parts > 1 && it.piece == 0) {
                     head->item[it.index].row0 = it.row0;
@@ -664,10 +674,12 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                     head->item[it.index].hn = it.hn;
                 }
                 s_item = it;
+                s_item_ns = item_ns;
                 mbar_arrive(ifull);
             }
             __syncwarp();
-            if (!it.live || !wait(iempty, (uint32_t)n & 1u)) break;
+            if (!it.live) break;
+            ok = __all_sync(0xffffffffu, mbar_wait(iempty, (uint32_t)n & 1u, status, a.wait_ns + item_ns));
         }
         // the last CTA to stop leaves the counters at zero for the next call
         if (lane == 0) {
@@ -1013,6 +1025,7 @@ cudaError_t launch_t(const PagedArgs& args, cudaStream_t st)
     PagedArgs a = args;
     const PreShape s = pre_shape(a.p);
     a.split = s.split;
+    a.tile_ns = a.wait_ns ? 0 : kTileNs;               // (a test's limit is the whole limit)
     a.wait_ns = a.wait_ns ? a.wait_ns : kWaitNs;
     CUtensorMap mq, mk, mv;
     if (!query_map(&mq, a, s.gch, s.tq) || !pool_map(&mk, a.k, a) || !pool_map(&mv, a.v, a)) return cudaErrorInvalidValue;

@@ -47,6 +47,7 @@ struct PagedArgs {
     int shift, grp;           // page_size = 1 << shift; query heads per KV head
     int split;                // prefill: whether items may be cut along their keys (the launcher sets it)
     unsigned long long wait_ns;   // prefill: limit of the waits (0: the launcher sets the default)
+    unsigned int tile_ns;         // prefill: what waits for an item's end are given for each of its key tiles
     float scale_log2;         // scale * log2(e): scores in units of powers of two
     const void* k;
     const void* v;

@@ -83,6 +83,7 @@ PagedArgs paged_args(const fadkv_paged_params& p, const void* k, const void* v, 
     a.grp = p.Hq / p.Hkv;
     a.split = 0;
     a.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+    a.tile_ns = 0;
     a.scale_log2 = p.scale * 1.44269504088896f;
     a.k = k;
     a.v = v;

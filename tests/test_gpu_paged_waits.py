@@ -6,6 +6,8 @@ limit), gives its tensor memory back and leaves the workspace's counters at
 zero: no CUDA error, the status word says what happened, and the next call on
 the workspace is right.
 """
+import math
+
 import pytest
 
 from tests.test_gpu_paged import DEV, PREFILLS, TURNS, Case, _i32
@@ -74,3 +76,27 @@ def test_short_calls_with_waits_that_give_up():
     for c in cases:
         c.out.fill_(5), c.lse.fill_(5)
         c.run(ws).check()
+
+
+def test_an_item_may_take_longer_than_a_wait():
+    """One token on 60 million cached (a page over and over) beside 256 requests of one: its item, which is walked whole,
+    takes more than the 200 ms of a wait, and is no reason to give up."""
+    from dictionary_sparse_kv_gb300 import fadkv as F
+    length, ps, d, dt = 60_000_000, 1024, 64, torch.float16
+    length -= length % ps
+    q, out, lse, k, v, table, lens, starts = _long(length, 1, 256, d, dt, ps)
+    p = F.paged_params(q, out, k, "head", table)
+    ws = torch.zeros(F.paged_prefill_workspace_bytes(p), dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    begin.record()
+    F.paged_prefill(p, k, v, table, lens, starts, q, out, lse, ws)
+    end.record()
+    assert F.paged_status(ws) == 0
+    assert begin.elapsed_time(end) > 200
+    # every page holds the same tokens: the sum over one page times the pages.  The sum in 32 bits has one addition for each
+    # key tile, off by half a step (2^-24) at most
+    x = (q[0].double() @ k[1, 0].double().T) * d ** -0.5
+    want = torch.logsumexp(x, -1) + math.log(length / ps)
+    assert ((lse[0].double() - want).abs() <= length / 128 * 2.0 ** -24 + 1e-4).all()
+    assert torch.equal(out[1:], v[1, 0, 0].expand_as(out[1:]))                # requests of one token: its value
