@@ -368,6 +368,19 @@ def _pool(pages, layout):
     return pages.shape[h], pages.shape[t], _stride(pages, 0, d), _stride(pages, h, d), pages.stride(t)
 
 
+def _check_pools(k_pages, v_pages):
+    if v_pages is not None and (v_pages.shape != k_pages.shape or v_pages.dtype != k_pages.dtype or
+                                any(n > 1 and a != b for n, a, b in zip(k_pages.shape, k_pages.stride(), v_pages.stride()))):
+        raise ValueError("the two pools have one shape, layout and type")
+
+
+def _check_dense(name, t, shape, dtype):
+    """What the kernels take as dense rows, shape[0] of them (there may be more)."""
+    if t is not None and (t.dim() != len(shape) or t.shape[0] < shape[0] or tuple(t.shape[1:]) != tuple(shape[1:]) or
+                          t.dtype != dtype or not t.is_contiguous()):
+        raise ValueError(f"{name} is a contiguous {list(shape)} tensor of {dtype}")
+
+
 def page_params(B: int, page_size: int, num_pages: int, max_pages: int, max_tokens: int) -> PageParams:
     return PageParams(B, page_size, num_pages, max_pages, max_tokens)
 
@@ -393,9 +406,11 @@ def rope_init(d: int, rotary_dim: int, interleaved: bool = False, base: float = 
     return out
 
 
-def qk_params(q, k, v, q_out, k_pages, layout: str = "head", eps: float = 1e-6, kv_dtype=None) -> QkParams:
+def qk_params(q, k, v, q_out, k_pages, layout: str = "head", eps: float = 1e-6, kv_dtype=None, k_out=None, v_pages=None,
+              wq=None, wk=None) -> QkParams:
     """Parameters of qk_norm_rope from tensors q [T][Hq][d], k, v [T][Hkv][d] (heads contiguous, rows at any
-    stride), q_out and a pool.  Without a pool (k_pages None) kv_dtype says the type of k_out."""
+    stride), q_out (contiguous, q's shape or more rows) and a pool.  Without a pool (k_pages None) kv_dtype says the type of k_out.
+    The call itself sees addresses alone: k_out, v_pages, wq and wk, where given, are checked here."""
     for x in (q, k, v):
         if x.dim() != 3 or x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2]):
             raise ValueError("q, k and v are [rows][heads][d] with the heads back to back")
@@ -408,8 +423,18 @@ def qk_params(q, k, v, q_out, k_pages, layout: str = "head", eps: float = 1e-6, 
     else:
         hkv, ps, *strides = _pool(k_pages, layout)
         pages, kvt = k_pages.shape[0], _dtype(k_pages)
+        if k_pages.shape[3] != d:
+            raise ValueError("the pool has the heads' dimension")
+        _check_pools(k_pages, v_pages)
     if k.shape != (T, hkv, d) or v.shape != k.shape:
         raise ValueError("k and v are [T][Hkv][d], Hkv as in the pool")
+    _check_dense("q_out", q_out, q.shape, q_out.dtype)
+    if k_out is not None:
+        if _dtype(k_out) != kvt:
+            raise ValueError("k_out has the pool's type")
+        _check_dense("k_out", k_out, k.shape, k_out.dtype)
+    for name, w in (("wq", wq), ("wk", wk)):
+        _check_dense(name, w, (d,), q.dtype)
     return QkParams(T, Hq, hkv, d, _dtype(q), _dtype(q_out), kvt, ps, pages, eps, _stride(q, 0, Hq * d),
                     _stride(k, 0, hkv * d), _stride(v, 0, hkv * d), *strides)
 
@@ -424,9 +449,10 @@ def qk_norm_rope(p: QkParams, rope: Rope, q, k, v, wq, wk, positions, slots, q_o
 
 
 def paged_params(q, out, k_pages, layout: str = "head", block_table=None, window: int = 0, sinks: int = 0,
-                 scale=None, B=None, max_pages=None) -> PagedParams:
+                 scale=None, B=None, max_pages=None, v_pages=None, lse=None) -> PagedParams:
     """Parameters of paged_attend / paged_prefill from tensors q, out [T][Hq][d] (heads contiguous), a pool and the
-    block tables [B][max_pages]."""
+    block tables [B][max_pages] (int32).  The calls themselves see addresses alone: v_pages and lse, where given, are
+    checked here."""
     for x in (q, out):
         if x.dim() != 3 or x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2]):
             raise ValueError("q and out are [rows][heads][d] with the heads back to back")
@@ -434,10 +460,15 @@ def paged_params(q, out, k_pages, layout: str = "head", block_table=None, window
         raise ValueError("q, out and the pool have one type and head dimension, q and out one shape")
     T, Hq, d = q.shape
     hkv, ps, *strides = _pool(k_pages, layout)
+    _check_pools(k_pages, v_pages)
+    if lse is not None:
+        import torch
+        _check_dense("lse", lse, (T, Hq), torch.float32)
     if block_table is not None:
+        import torch
+        if block_table.dim() != 2 or block_table.dtype != torch.int32 or not block_table.is_contiguous():
+            raise ValueError("block tables are contiguous [B][max_pages] int32")
         B, max_pages = block_table.shape
-        if not block_table.is_contiguous():
-            raise ValueError("block tables are contiguous")
     return PagedParams(B, T, Hq, hkv, d, _dtype(q), ps, k_pages.shape[0], max_pages, window, sinks,
                        d ** -0.5 if scale is None else scale, _stride(q, 0, Hq * d), _stride(out, 0, Hq * d), *strides)
 

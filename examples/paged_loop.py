@@ -65,7 +65,7 @@ class Layer:
                     self.positions, self.slots, self.refused)
         q, k, v = self.project(T)
         q_out, k_out = torch.empty((T, HQ, D), dtype=torch.float16, device=self.dev), torch.empty((T, HKV, D), dtype=torch.float16, device=self.dev)
-        F.qk_norm_rope(F.qk_params(q, k, v, q_out, self.k_pages), self.rope, q, k, v, self.wq, self.wk, self.positions, self.slots,
+        F.qk_norm_rope(F.qk_params(q, k, v, q_out, self.k_pages, k_out=k_out, v_pages=self.v_pages, wq=self.wq, wk=self.wk), self.rope, q, k, v, self.wq, self.wk, self.positions, self.slots,
                        q_out, k_out, self.k_pages, self.v_pages)
         return q_out, k_out, v
 
@@ -79,7 +79,7 @@ class Layer:
     def attend(self, q, window=0, sinks=0, positions=None):
         """One query token a request over the pages; with the step's positions, requests that its plan refused see nothing."""
         out = torch.empty_like(q)
-        p = F.paged_params(q, out, self.k_pages, "head", self.table, window, sinks)
+        p = F.paged_params(q, out, self.k_pages, "head", self.table, window, sinks, v_pages=self.v_pages)
         ws = self.workspace("decode", F.paged_attend_workspace_bytes(p))
         F.paged_attend(p, self.k_pages, self.v_pages, self.table, self.lengths, q, out, None, ws, positions=positions)
         return out
@@ -87,7 +87,7 @@ class Layer:
     def prefill(self, q, window=0, sinks=0):
         """The new tokens' queries (rows starts[b] .. starts[b + 1]) over the pages."""
         out = torch.empty_like(q)
-        p = F.paged_params(q, out, self.k_pages, "head", self.table, window, sinks)
+        p = F.paged_params(q, out, self.k_pages, "head", self.table, window, sinks, v_pages=self.v_pages)
         ws = self.workspace("prefill", F.paged_prefill_workspace_bytes(p))
         F.paged_prefill(p, self.k_pages, self.v_pages, self.table, self.lengths, self.starts, q, out, None, ws,
                         positions=self.positions)

@@ -43,3 +43,42 @@ def test_status_refusals(L, monkeypatch):
     monkeypatch.setenv("FADKV_FAULT", "cuda")
     assert L.fadkv_paged_status(FAKE, C.byref(word), 1, None) == 4 and "fadkv_paged_status" in F.last_error()
     assert word.value == 7
+
+
+def _rows(T, H, d, dtype=torch.float16):
+    return torch.zeros((T, H, d), dtype=dtype)
+
+
+def test_qk_params_refuses_outputs_that_the_kernel_would_overrun():
+    """q_out and k_out are written as dense rows of q's and k's shape: fewer heads or rows, padded rows and other types
+    are refused, as are a pool of another head dimension and pools that differ."""
+    T, d = 4, 128
+    q, k, pool = _rows(T, 24, d), _rows(T, 8, d), torch.zeros((10, 8, 16, d), dtype=torch.float16)
+    ok = dict(q=q, k=k, v=k, q_out=_rows(T, 24, d, torch.float32), k_pages=pool)
+    padded = torch.zeros((T, 24 * d + 64), dtype=torch.float16)[:, :24 * d].view(T, 24, d)
+    for bad in (dict(q_out=_rows(T, 12, d)), dict(q_out=_rows(T - 1, 24, d)), dict(q_out=padded), dict(q_out=_rows(T, 24, 64)),
+                dict(k_pages=torch.zeros((10, 8, 16, 64), dtype=torch.float16)),
+                dict(k_pages=torch.zeros((10, 8, 16, 256), dtype=torch.float16)),
+                dict(v_pages=pool[:9]), dict(v_pages=pool.bfloat16()), dict(v_pages=pool.transpose(1, 2).contiguous().transpose(1, 2)),
+                dict(k_out=_rows(T, 7, d)), dict(k_out=_rows(T, 8, d, torch.float32)), dict(k_out=padded[:, :8]),
+                dict(wq=torch.zeros(d)), dict(wk=torch.zeros(64, dtype=torch.float16)), dict(wk=torch.zeros(2 * d, dtype=torch.float16)[::2])):
+        with pytest.raises(ValueError):
+            F.qk_params(**{**ok, **bad})
+    w = torch.zeros(d, dtype=torch.float16)
+    p = F.qk_params(**ok, k_out=_rows(T, 8, d), v_pages=torch.zeros_like(pool), wq=w, wk=w)
+    assert bytes(p) == bytes(F.qk_params(**ok)) == bytes(F.qk_params(**{**ok, "q_out": _rows(T + 3, 24, d, torch.float32)}))
+    one = torch.zeros((1, 8, 16, d), dtype=torch.float16)                     # a single page: its stride says nothing
+    F.qk_params(**{**ok, "k_pages": one}, v_pages=one.as_strided(one.shape, (8, 16 * d, d, 1)))
+    assert F.qk_params(q, k, k, ok["q_out"], None, kv_dtype=F.BF16, k_out=_rows(T, 8, d, torch.bfloat16)).kv_dtype == F.BF16
+
+
+def test_paged_params_refuses_other_tables_and_pools():
+    q, pool, table = _rows(4, 24, 128), torch.zeros((10, 8, 16, 128), dtype=torch.float16), torch.zeros((4, 3), dtype=torch.int32)
+    ok = dict(q=q, out=torch.empty_like(q), k_pages=pool, block_table=table)
+    for bad in (dict(block_table=table.long()), dict(block_table=table[0]), dict(v_pages=pool[:9]), dict(v_pages=pool.bfloat16()),
+                dict(v_pages=pool.transpose(1, 2).contiguous().transpose(1, 2)), dict(lse=torch.zeros(4, 8)),
+                dict(lse=torch.zeros(4, 24, dtype=torch.float64)), dict(lse=torch.zeros(24, 4).T)):
+        with pytest.raises(ValueError):
+            F.paged_params(**{**ok, **bad})
+    p = F.paged_params(**ok, v_pages=torch.zeros_like(pool), lse=torch.zeros(4, 24))
+    assert bytes(p) == bytes(F.paged_params(**ok))
