@@ -5,14 +5,35 @@
    tensor in Python come to about 3 us of a call, this module's arguments to
    about 1 us (2 us are the launch).  It marshals arguments and nothing else:
    tensors by their data_ptr(), None as a null pointer, integers as addresses,
-   the parameter structs (ctypes.Structure) by their buffers.  The functions'
-   own addresses come from the loaded library. */
+   the parameter structs by their buffers, each of the class that types() was
+   given for it (two of them are of one size).  The functions' own addresses
+   come from the loaded library. */
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include "fadkv.h"
 
 static PyObject* s_data_ptr;
+enum { PAGE, QK, ROPE, PAGED, TYPES };
+static PyTypeObject* s_types[TYPES];
+
+/* types(PageParams, QkParams, Rope, PagedParams): the structs' classes. */
+static PyObject* types(PyObject* self, PyObject* const* args, Py_ssize_t n)
+{
+    (void)self;
+    for (Py_ssize_t i = 0; i < n; ++i)
+        if (n != TYPES || !PyType_Check(args[i])) n = -1;
+    if (n != TYPES) {
+        PyErr_SetString(PyExc_TypeError, "four classes wanted");
+        return NULL;
+    }
+    for (int i = 0; i < TYPES; ++i) {
+        Py_INCREF(args[i]);
+        Py_XDECREF((PyObject*)s_types[i]);
+        s_types[i] = (PyTypeObject*)args[i];
+    }
+    Py_RETURN_NONE;
+}
 
 /* Address of a tensor, an integer or None; 0 on success. */
 static int address(PyObject* o, void** out)
@@ -32,13 +53,17 @@ static int address(PyObject* o, void** out)
     return PyErr_Occurred() ? -1 : 0;
 }
 
-/* The bytes of a ctypes struct of the expected size; null for None. */
-static int structure(PyObject* o, size_t size, const void** out)
+/* The bytes of a struct of the expected class and size; null for None. */
+static int structure(PyObject* o, int type, size_t size, const void** out)
 {
     Py_buffer b;
     if (o == Py_None) {
         *out = NULL;
         return 0;
+    }
+    if (!s_types[type] || !PyObject_TypeCheck(o, s_types[type])) {
+        PyErr_SetString(PyExc_TypeError, "wrong parameter struct");
+        return -1;
     }
     if (PyObject_GetBuffer(o, &b, PyBUF_SIMPLE) != 0) return -1;
     *out = b.buf;
@@ -68,7 +93,7 @@ static PyObject* page_plan(PyObject* self, PyObject* const* args, Py_ssize_t n)
     void *f, *p[12];
     const void* params;
     (void)self;
-    if (arity(n, 14) || address(args[0], &f) || structure(args[1], sizeof(fadkv_page_params), &params) ||
+    if (arity(n, 14) || address(args[0], &f) || structure(args[1], PAGE, sizeof(fadkv_page_params), &params) ||
         pointers(args + 2, 12, p))
         return NULL;
     __typeof__(&fadkv_page_plan) call = (__typeof__(&fadkv_page_plan))f;
@@ -85,8 +110,8 @@ static PyObject* qk_norm_rope(PyObject* self, PyObject* const* args, Py_ssize_t 
     void *f, *p[12];
     const void *params, *rope;
     (void)self;
-    if (arity(n, 15) || address(args[0], &f) || structure(args[1], sizeof(fadkv_qk_params), &params) ||
-        structure(args[2], sizeof(fadkv_rope), &rope) || pointers(args + 3, 12, p))
+    if (arity(n, 15) || address(args[0], &f) || structure(args[1], QK, sizeof(fadkv_qk_params), &params) ||
+        structure(args[2], ROPE, sizeof(fadkv_rope), &rope) || pointers(args + 3, 12, p))
         return NULL;
     __typeof__(&fadkv_qk_norm_rope) call = (__typeof__(&fadkv_qk_norm_rope))f;
     fadkv_status rc;
@@ -102,7 +127,7 @@ static PyObject* paged_attend(PyObject* self, PyObject* const* args, Py_ssize_t 
     void *f, *p[9], *st;
     const void* params;
     (void)self;
-    if (arity(n, 13) || address(args[0], &f) || structure(args[1], sizeof(fadkv_paged_params), &params) ||
+    if (arity(n, 13) || address(args[0], &f) || structure(args[1], PAGED, sizeof(fadkv_paged_params), &params) ||
         pointers(args + 2, 9, p) || address(args[12], &st))
         return NULL;
     const size_t bytes = PyLong_AsSize_t(args[11]);
@@ -121,7 +146,7 @@ static PyObject* paged_prefill(PyObject* self, PyObject* const* args, Py_ssize_t
     void *f, *p[10], *st;
     const void* params;
     (void)self;
-    if (arity(n, 14) || address(args[0], &f) || structure(args[1], sizeof(fadkv_paged_params), &params) ||
+    if (arity(n, 14) || address(args[0], &f) || structure(args[1], PAGED, sizeof(fadkv_paged_params), &params) ||
         pointers(args + 2, 10, p) || address(args[13], &st))
         return NULL;
     const size_t bytes = PyLong_AsSize_t(args[12]);
@@ -135,6 +160,7 @@ static PyObject* paged_prefill(PyObject* self, PyObject* const* args, Py_ssize_t
 }
 
 static PyMethodDef methods[] = {
+    {"types", (PyCFunction)(void (*)(void))types, METH_FASTCALL, NULL},
     {"page_plan", (PyCFunction)(void (*)(void))page_plan, METH_FASTCALL, NULL},
     {"qk_norm_rope", (PyCFunction)(void (*)(void))qk_norm_rope, METH_FASTCALL, NULL},
     {"paged_attend", (PyCFunction)(void (*)(void))paged_attend, METH_FASTCALL, NULL},

@@ -198,6 +198,7 @@ def _load_calls():
             loader = importlib.machinery.ExtensionFileLoader("_fadkv_calls", CALLS_PATH)
             m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fadkv_calls", loader))
             loader.exec_module(m)
+            m.types(PageParams, QkParams, Rope, PagedParams)
             for name, function in (("page_plan", "page_plan"), ("qk_norm_rope", "qk_norm_rope"),
                                    ("paged_attend", "paged_attend_planned"), ("paged_prefill", "paged_prefill_planned")):
                 _direct[name] = C.cast(getattr(L, "fadkv_" + function), C.c_void_p).value

@@ -82,3 +82,25 @@ def test_paged_params_refuses_other_tables_and_pools():
             F.paged_params(**{**ok, **bad})
     p = F.paged_params(**ok, v_pages=torch.zeros_like(pool), lse=torch.zeros(4, 24))
     assert bytes(p) == bytes(F.paged_params(**ok))
+
+
+def test_structs_of_one_size_are_told_apart(L):
+    """QkParams and PagedParams have as many bytes; the direct calls take each for what it is."""
+    from tests.test_paged_host import _qk
+    assert C.sizeof(F.QkParams) == C.sizeof(F.PagedParams)
+    rope = F.rope_init(128, 128)
+    with pytest.raises(TypeError):
+        F.qk_norm_rope(_paged(T=0), rope, *[FAKE] * 11, stream=0)
+    for call, arrays in ((F.paged_attend, 8), (F.paged_prefill, 9)):
+        with pytest.raises(TypeError):
+            call(_qk(T=0), *[FAKE] * (arrays - 1), workspace=torch.zeros(1), stream=0)
+    with pytest.raises(TypeError):
+        F._calls.types(F.PageParams, F.QkParams, F.Rope)
+    with pytest.raises(TypeError):
+        F._calls.types(F.PageParams, F.QkParams, F.Rope, 5)
+
+    class Mine(F.QkParams):
+        pass
+
+    p = Mine.from_buffer_copy(bytes(_qk(T=0)))                # a class derived from it is one
+    F.qk_norm_rope(p, rope, *[FAKE] * 11, stream=0)
