@@ -207,7 +207,7 @@ def _load_calls():
 
 
 def _addr(t):
-    return t if t is None or type(t) is int else t.data_ptr()
+    return t if t is None or isinstance(t, int) else t.data_ptr()
 
 
 _raw_stream = None       # torch's current stream of a device as an integer
@@ -222,10 +222,13 @@ def _stream(stream, *tensors):
         _raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None) or
                        (lambda d: torch.cuda.current_stream(d).cuda_stream))
     for t in tensors:
-        if t is not None and type(t) is not int:
+        if hasattr(t, "get_device"):                 # a tensor, and no address
             dev = t.get_device()
             if dev >= 0:
                 return _raw_stream(dev)
+        elif hasattr(t, "device") and t.device.type == "cuda":
+            import torch
+            return torch.cuda.current_stream(t.device).cuda_stream
     import torch
     return torch.cuda.current_stream().cuda_stream
 

@@ -104,3 +104,30 @@ def test_structs_of_one_size_are_told_apart(L):
 
     p = Mine.from_buffer_copy(bytes(_qk(T=0)))                # a class derived from it is one
     F.qk_norm_rope(p, rope, *[FAKE] * 11, stream=0)
+
+
+def test_addresses_and_streams_of_other_objects(L, monkeypatch):
+    """Integers of any class are addresses; objects without a device are passed over in the search for a stream."""
+    import enum
+
+    class Place(enum.IntEnum):
+        A = 0x1000
+
+    class Array:                                              # an address and nothing else
+        def data_ptr(self):
+            return 0x2000
+
+    class Cuda:                                               # a device, but not a tensor's way to ask for it
+        device = torch.device("cuda", 0)
+
+    assert F._addr(Place.A) == 0x1000 and F._addr(True) == 1 and F._addr(Array()) == 0x2000 and F._addr(None) is None
+    stream = type("S", (), {"cuda_stream": 77})()
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: stream)
+    assert F._stream(None, Place.A, None, 5, Array(), torch.zeros(1)) == 77
+    assert F._stream(None, Array(), Cuda()) == 77
+    assert F._stream(stream, Array()) == 77 and F._stream(3) == 3
+    class Tensor:
+        def get_device(self):
+            return 2
+    monkeypatch.setattr(F, "_raw_stream", lambda d: 1000 + d)
+    assert F._stream(None, None, Array(), torch.zeros(1), Tensor()) == 1002
