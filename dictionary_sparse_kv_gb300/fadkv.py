@@ -489,8 +489,11 @@ def paged_prefill_workspace_bytes(p: PagedParams) -> int:
     return out.value
 
 
-def _nbytes(workspace) -> int:
-    return 0 if workspace is None else workspace.nbytes
+def _nbytes(workspace, ask, p) -> int:
+    """Bytes of a workspace; of one given as an address those that the call needs."""
+    if workspace is None:
+        return 0
+    return ask(p) if isinstance(workspace, int) else workspace.nbytes
 
 
 def paged_attend(p: PagedParams, k_pages, v_pages, block_table, lengths, q, out, lse, workspace, stream=None,
@@ -499,7 +502,8 @@ def paged_attend(p: PagedParams, k_pages, v_pages, block_table, lengths, q, out,
     zero-filled before its first use.  With a plan's positions, requests that it refused see nothing
     (fadkv_paged_attend_planned)."""
     rc = (_calls or _load_calls()).paged_attend(_direct["paged_attend"], p, k_pages, v_pages, block_table, lengths, positions, q,
-                                                out, lse, workspace, _nbytes(workspace), _stream(stream, q, out))
+                                                out, lse, workspace, _nbytes(workspace, paged_attend_workspace_bytes, p),
+                                                _stream(stream, q, out))
     if rc:
         _check("fadkv_paged_attend", rc)
 
@@ -510,7 +514,8 @@ def paged_prefill(p: PagedParams, k_pages, v_pages, block_table, lengths, starts
     zero-filled before its first use.  With a plan's positions, requests that it refused see nothing
     (fadkv_paged_prefill_planned)."""
     rc = (_calls or _load_calls()).paged_prefill(_direct["paged_prefill"], p, k_pages, v_pages, block_table, lengths, starts,
-                                                 positions, q, out, lse, workspace, _nbytes(workspace),
+                                                 positions, q, out, lse, workspace,
+                                                 _nbytes(workspace, paged_prefill_workspace_bytes, p),
                                                  _stream(stream, q, out))
     if rc:
         _check("fadkv_paged_prefill", rc)

@@ -131,3 +131,15 @@ def test_addresses_and_streams_of_other_objects(L, monkeypatch):
             return 2
     monkeypatch.setattr(F, "_raw_stream", lambda d: 1000 + d)
     assert F._stream(None, None, Array(), torch.zeros(1), Tensor()) == 1002
+
+
+def test_workspaces_given_as_addresses(L, monkeypatch):
+    """As for the other arrays: an integer is an address, its size what the call needs."""
+    monkeypatch.setenv("FADKV_FAULT", "cuda")                 # every check is passed, nothing is launched
+    for call, arrays in ((F.paged_attend, 7), (F.paged_prefill, 8)):
+        with pytest.raises(F.FadkvError) as e:
+            call(_paged(), *[FAKE] * arrays, workspace=FAKE, stream=0)
+        assert e.value.status == 4
+        with pytest.raises(F.FadkvError) as e:
+            call(_paged(), *[FAKE] * arrays, workspace=None, stream=0)
+        assert e.value.status == 5
