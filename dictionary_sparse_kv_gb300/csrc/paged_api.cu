@@ -147,7 +147,7 @@ fadkv_status fadkv_rope_init(const fadkv_rope_params* p, fadkv_rope* out)
 {
     if (!p || !out) return FADKV_ERR_INVALID_ARG;
     if (p->rotary_dim < 0 || p->rotary_dim > p->d || !(p->base > 1.0) || !isfinite(p->base) ||
-        !isfinite(p->amplitude) || p->scaling < FADKV_ROPE_PLAIN || p->scaling > FADKV_ROPE_PARTS)
+        !isfinite((float)p->amplitude) || p->scaling < FADKV_ROPE_PLAIN || p->scaling > FADKV_ROPE_PARTS)
         return FADKV_ERR_INVALID_ARG;
     if ((p->d != 64 && p->d != 128) || p->rotary_dim % 16 != 0) return FADKV_ERR_UNSUPPORTED;
     if (p->scaling != FADKV_ROPE_PLAIN && !(p->factor >= 1.0 && isfinite(p->factor))) return FADKV_ERR_INVALID_ARG;

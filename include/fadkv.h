@@ -472,7 +472,7 @@ typedef struct {
     double factor;        /* >= 1 (LINEAR, STRETCH, PARTS) */
     double original;      /* > 0, trained length (PARTS) */
     double slow, fast;    /* slow < fast (PARTS) */
-    double amplitude;     /* finite */
+    double amplitude;     /* finite in 32 bits */
 } fadkv_rope_params;
 
 /* The rotation as the kernel reads it: a plain host struct, filled by

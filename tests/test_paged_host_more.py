@@ -143,3 +143,11 @@ def test_workspaces_given_as_addresses(L, monkeypatch):
         with pytest.raises(F.FadkvError) as e:
             call(_paged(), *[FAKE] * arrays, workspace=None, stream=0)
         assert e.value.status == 5
+
+
+def test_rope_amplitude_has_to_be_finite_in_32_bits(L):
+    for amplitude in (1e39, -1e39, math.inf, math.nan):
+        with pytest.raises(F.FadkvError) as e:
+            F.rope_init(128, 64, amplitude=amplitude)
+        assert e.value.status == 1
+    assert F.rope_init(128, 64, amplitude=3e38).amplitude == pytest.approx(3e38)
