@@ -556,7 +556,12 @@ typedef struct {
                  the larger size, may serve fadkv_paged_prefill too); not to be
                  shared by calls that may run concurrently
    Scores, softmax and sums in 32 bits; the probabilities enter the product
-   with the values as two 16-bit terms each.
+   with the values as two 16-bit terms each (22 bits with binary16 pools, where
+   one below 2^-40 of the largest is lost; 16 bits with bfloat16).  A seen value
+   that is infinite makes that element of the heads that read it infinite or
+   NaN (the two terms may differ in sign, or one be 0), a NaN makes it NaN; a
+   score that is NaN or +inf makes the head's row and lse NaN.  Nothing else is
+   touched by them.
    Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
 fadkv_status fadkv_paged_attend(const fadkv_paged_params* params, const void* k_pages, const void* v_pages,
                                 const int32_t* block_table, const int32_t* lengths, const void* q, void* out,
@@ -587,7 +592,8 @@ fadkv_status fadkv_paged_attend_workspace_bytes(const fadkv_paged_params* params
    tokens: use fadkv_paged_prefill_planned, or give it a length of 0.  What the
    pools hold where no row sees it is never used; a value that is not finite
    and that one row sees may reach other rows of its request.  The
-   probabilities enter the product with the values in the type of the pools.
+   probabilities enter the product with the values in the type of the pools,
+   rounded once; with binary16 one below 2^-32 of the largest may be lost.
    workspace   >= fadkv_paged_prefill_workspace_bytes bytes, 256-byte aligned,
                ZERO-FILLED before its first use.  Its first 8 bytes are a
                status word: FADKV_DEV_TIMEOUT is set in it if a kernel gave
