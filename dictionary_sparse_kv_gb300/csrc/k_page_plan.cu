@@ -49,12 +49,6 @@ __device__ __forceinline__ int owner(const int* pre, int n, int v)
 
 __device__ __forceinline__ int saturate(long long v) { return v > 0x7fffffffll ? 0x7fffffff : (int)v; }
 
-__device__ __forceinline__ void write_row(const PlanArgs& a, int t, int pos, int page)
-{
-    a.positions[t] = pos;
-    a.slots[t] = pos >= 0 && page >= 0 && page < a.num_pages ? (page << a.shift) + (pos & ((1 << a.shift) - 1)) : -1;
-}
-
 template <int THREADS, int PART>
 __global__ void __launch_bounds__(THREADS)
 page_plan_kernel(PlanArgs a)

@@ -49,8 +49,9 @@ constexpr int kDecThreads = 128;
 constexpr int kDecWarps = kDecThreads / 32;
 constexpr int kTile = 16;                          // tokens per warp step
 constexpr int kBlock = kTile * kDecWarps;          // tokens per unit of work
-// CTAs: two per multiprocessor (152), three at d = 64, whose buffers are half as large (113 requests, window 1024, d = 64:
-// 14.7 us against 16.0 with two CTAs of six stages; d = 128 with three CTAs of two stages: 16 of 4096 34.8 against 27.7 us)
+// CTAs: two per multiprocessor (152), three at d = 64, whose buffers are half as large (us on the device, against two CTAs
+// of six stages at d = 64: 113 requests of 1024 tokens, two KV heads, 12.2 and 12.9; 16 of up to 4096, eight KV heads, 15.8
+// and 18.9; 64 of up to 16384 162 and 168; d = 128 with three CTAs of two stages: 16 of 4096 34.8 against 27.7)
 __host__ __device__ constexpr int dec_ctas(int d) { return d == 128 ? 304 : 456; }
 constexpr int kMaxHeads = 16;                      // query heads per piece; larger groups are several pieces
 
@@ -123,7 +124,12 @@ paged_decode_kernel(const __grid_constant__ PagedArgs a)
     long long u, u1, U, base;                                          // this CTA's units; all; the first of request cur_b
     int C, cur_b, longest, parts = 0;                                  // parts > 0: (request, heads) in so many equal parts
     // Equal parts: the lengths are within an eighth of the longest one on average, and the parts are at least three
-    // fifths of the grid.  (113 requests, window 1024, two KV heads of 64: 14.0 us in equal parts, 16.6 in shares.)
+    // fifths of the grid.  Measured over 1 to 152 requests of 500 to 20000 tokens, us on the device in equal parts and in
+    // shares: of one length 113 requests of 1024 tokens with two KV heads of 64 12.0 and 14.0, 4 of 4096 with eight of 128
+    // 12.5 and 14.3, 64 of 3000 with four of 128 59.5 and 64.2, 152 of 20000 with one of 128 227 and 227.  With a mean of
+    // 7/8 of the longest 11.6 and 13.6, 12.3 and 14.0, 55.6 and 55.8, 197 and 197; of 3/4, where shares are taken, 11.5
+    // and 13.0, 12.3 and 13.2, 49.5 and 48.5, 178 and 166.  Below three fifths of the grid (60 requests of 1100 with four KV
+    // heads of 64, 240 parts on 456 places): 16.6 and 14.7.
     auto share = [&] {
         const int pieces = B * segs, grid = (int)gridDim.x;
         C = (int)min((long long)grid, U);

@@ -388,7 +388,10 @@ fadkv_status fadkv_attend_workspace_bytes(const fadkv_attn_params* params, size_
 /* ---------------------------------------------------------------------------
    The paged cache of full key/value vectors: what a decode loop keeps of the
    vectors that are not coded (a prompt before its encode, the recent window
-   and the first tokens, or the whole cache in a full-KV run).  Handle-free:
+   and the first tokens, or the whole cache in a full-KV run).  Attention over
+   pages and over codes are separate answers: fadkv_attend takes no range of
+   tokens and returns no log-sum-exp, so a window here and the codes of the
+   other tokens do not join into one softmax.  Handle-free:
    every call works on caller-owned buffers only, asynchronously on `stream`,
    and can be captured into a CUDA graph.
 
@@ -454,6 +457,8 @@ fadkv_status fadkv_page_plan(const fadkv_page_params* params, const int32_t* add
      FADKV_ROPE_PARTS    with r = original * f_i / (2 pi) turns over the original
                          length and g = clamp((r - slow) / (fast - slow), 0, 1):
                          f_i * (g + (1 - g) / factor)
+                         (linear in r; a checkpoint whose ramp is linear in the
+                         pair's number i is another rotation)
    The rotated part is multiplied by amplitude (1 for none). */
 #define FADKV_ROPE_MAX_PAIRS 64
 typedef enum {
@@ -539,7 +544,9 @@ typedef struct {
     int64_t page_stride, head_stride, token_stride;   /* of the pools */
 } fadkv_paged_params;
 
-/* Attention of one new token per request over the paged cache (T = B):
+/* Attention of one new token per request over the paged cache (T = B, row b is
+   request b's; a step in which some requests bring none goes through
+   fadkv_paged_prefill):
      out[b][h] = sum_j p_j v_j,  p = softmax_j(scale <q[b][h], k_j>),
      lse[b][h] = log sum_j exp(scale <q[b][h], k_j>),
    over the tokens j < lengths[b] that the query at position lengths[b] - 1
