@@ -215,7 +215,7 @@ struct Tiles {
     {
         first = it.first;
         last = it.first + it.nt - 1;
-        W = min(a.p.window, 1 << 30);
+        W = a.p.window;        // below 2^31 - 4096 (the launcher); an item with keys to see begins at position -256 or later
         S = min(a.p.sinks, it.len);
         const int to = last >= 0 ? last / kKeys + 1 : 0;
         from = W > 0 ? max(0, first - W + 1) / kKeys : 0;
@@ -745,7 +745,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                     for (int c = 0; c < 4; ++c) {
                         const int k = k0 + c * 32;
                         uint32_t bits = low_bits(pos - k + 1);
-                        if (ts.W > 0) bits &= ~low_bits(pos - ts.W - k + 1) | low_bits(ts.S - k);
+                        // (unsigned: wraps around for rows that see nothing)
+                        if (ts.W > 0) bits &= ~low_bits((int)((uint32_t)(pos - k + 1) - (uint32_t)ts.W)) | low_bits(ts.S - k);
                         if (!all_ok) bits &= okr[1 + c];
                         if (__all_sync(0xffffffffu, bits == 0xffffffffu)) continue;
 #pragma unroll
@@ -1032,6 +1033,7 @@ cudaError_t launch_t(const PagedArgs& args, cudaStream_t st)
     PagedArgs a = args;
     const PreShape s = pre_shape(a.p);
     a.split = s.split;
+    if (a.p.window >= a.p.max_pages << a.shift) a.p.window = 0;   // hides nothing
     a.tile_ns = a.wait_ns ? 0 : kTileNs;               // (a test's limit is the whole limit)
     a.wait_ns = a.wait_ns ? a.wait_ns : kWaitNs;
     CUtensorMap mq, mk, mv;

@@ -100,3 +100,19 @@ def test_an_item_may_take_longer_than_a_wait():
     want = torch.logsumexp(x, -1) + math.log(length / ps)
     assert ((lse[0].double() - want).abs() <= length / 128 * 2.0 ** -24 + 1e-4).all()
     assert torch.equal(out[1:], v[1, 0, 0].expand_as(out[1:]))                # requests of one token: its value
+
+
+def test_a_window_of_more_than_a_billion_tokens():
+    """One token on 1.2 billion cached (a page over and over) with a window of 1.1 billion: every page in it counts."""
+    from dictionary_sparse_kv_gb300 import fadkv as F
+    ps, d, dt = 1024, 64, torch.float16
+    length, window = 1_200_000 * ps, 1_100_000 * ps
+    q, out, lse, k, v, table, lens, starts = _long(length, 1, 0, d, dt, ps)
+    p = F.paged_params(q, out, k, "head", table, window=window)
+    ws = torch.zeros(F.paged_prefill_workspace_bytes(p), dtype=torch.uint8, device=DEV)
+    F.paged_prefill(p, k, v, table, lens, starts, q, out, lse, ws)
+    assert F.paged_status(ws) == 0
+    x = (q[0].double() @ k[1, 0].double().T) * d ** -0.5
+    want = torch.logsumexp(x, -1) + math.log(window / ps)
+    # 64 pieces, each with one addition in 32 bits a key tile; a window of 2^30 would be off by 0.047
+    assert ((lse[0].double() - want).abs() <= window / 128 / 64 * 2.0 ** -24 + 1e-4).all()
