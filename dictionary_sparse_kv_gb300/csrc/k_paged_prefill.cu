@@ -155,6 +155,22 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// mbar_wait for an item: the current one's share of the limit is read where
+// the time is looked at, as the items' warp works it out behind the item.
+__device__ __forceinline__ bool wait_item(uint32_t bar, uint32_t parity, unsigned long long* status, unsigned long long limit_ns,
+                                          const volatile unsigned long long* item_ns)
+{
+    if (mbar_try(bar, parity)) return true;
+    const unsigned long long t0 = globaltimer();
+    for (uint32_t i = 0;; ++i) {
+        if (mbar_try(bar, parity)) return true;
+        if ((i & 255u) == 255u && globaltimer() - t0 > limit_ns + *item_ns) {
+            atomicOr(status, (unsigned long long)FADKV_DEV_TIMEOUT);
+            return false;
+        }
+    }
+}
+
 // Shared-memory matrix descriptor of V [keys][d] as the B operand with d
 // along the rows of 128 bytes (N-major, 128-byte swizzle): 8-key groups 1024
 // bytes apart, 64-element halves of d one panel apart.
@@ -347,8 +363,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     // only after its last load for the item: the next one is then taken, late enough for an even share of a short
     // list and early enough to be hidden behind the tiles in flight.
     auto next_item = [&](int n, Item& it) {
-        const unsigned long long limit = a.wait_ns + *(volatile unsigned long long*)&s_item_ns;
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(ifull, (uint32_t)n & 1u, status, limit));
+        ok = ok && __all_sync(0xffffffffu, wait_item(ifull, (uint32_t)n & 1u, status, a.wait_ns, &s_item_ns));
         if (!ok) return false;
         it = s_item;
         __syncwarp();
@@ -672,7 +687,6 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                 it.head0 = it.hk * grp + h0;
                 it.hn = min(gch, grp - h0);
             }
-            const unsigned long long item_ns = it.live ? (unsigned long long)Tiles(it, a).count * a.tile_ns : 0ull;
             if (lane == 0) {
                 if (it.live && it.parts > 1 && it.piece == 0) {
                     head->item[it.index].row0 = it.row0;
@@ -681,11 +695,12 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                     head->item[it.index].hn = it.hn;
                 }
                 s_item = it;
-                s_item_ns = item_ns;
                 mbar_arrive(ifull);
             }
             __syncwarp();
             if (!it.live) break;
+            const unsigned long long item_ns = (unsigned long long)Tiles(it, a).count * a.tile_ns;
+            if (lane == 0) s_item_ns = item_ns;
             ok = __all_sync(0xffffffffu, mbar_wait(iempty, (uint32_t)n & 1u, status, a.wait_ns + item_ns));
         }
         // the last CTA to stop leaves the counters at zero for the next call
