@@ -1,0 +1,221 @@
+// Quantises a step's keys and values into the 8-bit pages.
+//
+// For a block of tokens and a head, with a the largest |x| of its new rows:
+//   t = 2^e, e least with a <= M 2^e;  s = t or max(old scale, t);
+//   code = rn(x / s);  codes of earlier tokens, if s grew: rn(code old / s).
+// Powers of two make every division exact, so a code is x with one rounding,
+// and keep what is rounded again within a step (a grown scale has doubled at
+// least).
+//
+// The new rows have to be read once and the codes written once: HBM for
+// prompts, latency for single tokens.  A warp takes one (block, head, keys or
+// values): its rows (up to 16 of 128 elements) stay in registers between the
+// maximum and the rounding, longer runs are read a second time, from L2.  The
+// runs of rows that share a block are found by the warps themselves, from the
+// slots: the warp whose rows a run begins in takes it.
+#include "paged8.cuh"
+
+namespace fadkv {
+namespace {
+
+using namespace paged8;
+
+constexpr int kThreads = 128;
+constexpr int kHeld = 8;         // steps of rows kept in registers
+
+// Eight consecutive elements as loaded; their largest |x| as the type's bits.
+template <typename T> struct Raw8 {
+    uint4 a;
+    static constexpr uint32_t kInfinite = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+    __device__ __forceinline__ void load(const T* p) { a = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void get(float* x) const
+    {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = Num<T>::unpack(w[i]);
+            x[2 * i] = f.x, x[2 * i + 1] = f.y;
+        }
+    }
+    __device__ __forceinline__ uint32_t most() const
+    {
+        const uint32_t m = 0x7fff7fffu;
+        const uint32_t v = __vmaxu2(__vmaxu2(a.x & m, a.y & m), __vmaxu2(a.z & m, a.w & m));
+        return max(v & 0xffffu, v >> 16);
+    }
+    static __device__ __forceinline__ uint32_t wide(uint32_t bits) { return __float_as_uint(Num<T>::unpack(bits).x); }
+};
+template <> struct Raw8<float> {
+    float4 a, b;
+    static constexpr uint32_t kInfinite = 0x7f800000u;
+    __device__ __forceinline__ void load(const float* p)
+    {
+        a = __ldg(reinterpret_cast<const float4*>(p));
+        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    }
+    __device__ __forceinline__ void get(float* x) const
+    {
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+    __device__ __forceinline__ uint32_t most() const
+    {
+        const float m = fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w))),
+                              fmaxf(fmaxf(fabsf(b.x), fabsf(b.y)), fmaxf(fabsf(b.z), fabsf(b.w))));
+        const float n = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));   // NaN, where one is
+        return n == n ? __float_as_uint(m) : 0x7fc00000u;
+    }
+    static __device__ __forceinline__ uint32_t wide(uint32_t bits) { return bits; }
+};
+
+// What a run of rows is written to.
+struct Place {
+    uint8_t* block;              // the block's first token, this head
+    float* scale;
+};
+
+template <typename T, int D, int FORMAT>
+__device__ __forceinline__ void quantise(const Append8Args& a, const T* x, long long stride, const Place& to, int row0, int n,
+                                         int first, int lane)
+{
+    constexpr int LPR = D / 8, RPW = 32 / LPR, ROWS = kHeld * RPW;   // lanes a row, rows a step, rows kept
+    const int sub = lane / LPR, l = lane % LPR, mask = (1 << a.bshift) - 1;
+    float old = first > 0 && lane == 0 ? *to.scale : 0.f;
+    Raw8<T> raw[kHeld];
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int u = 0; u < kHeld; ++u)
+            if (i0 + u * RPW < n) raw[u].load(x + min(row0 + i0 + u * RPW + sub, row0 + n - 1) * stride + l * 8);
+    };
+    uint32_t top = 0;
+    for (int i0 = 0; i0 < n; i0 += ROWS) {
+        load(i0);
+#pragma unroll
+        for (int u = 0; u < kHeld; ++u)
+            if (i0 + u * RPW < n) top = max(top, raw[u].most());
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (top >= Raw8<T>::kInfinite) {                   // the largest finite one
+        top = 0;
+        for (int i = sub; i < n; i += RPW) {
+            Raw8<T> r;
+            float f[8];
+            r.load(x + (row0 + i) * stride + l * 8);
+            r.get(f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t b = __float_as_uint(fabsf(f[j]));
+                top = max(top, b < 0x7f800000u ? b : 0u);
+            }
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+    } else {
+        top = Raw8<T>::wide(top);
+    }
+    const float t = __uint_as_float((uint32_t)max(Code<FORMAT>::exponent(top), 1) << 23);
+    old = __shfl_sync(0xffffffffu, old, 0);
+    const float s = first > 0 ? fmaxf(old, t) : t, inv = 1.f / s;
+    if (lane == 0) *to.scale = s;
+    if (first > 0 && s > old) {
+        const float ratio = old / s;
+#pragma unroll 4
+        for (int i = sub; i < first; i += RPW) {
+            uint2* at = reinterpret_cast<uint2*>(to.block + i * a.p.token_stride + l * 8);
+            const uint2 c = *at;
+            float y[8];
+            values<FORMAT>(c.x, y);
+            values<FORMAT>(c.y, y + 4);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] *= ratio;
+            *at = make_uint2(Code<FORMAT>::pack(y[0], y[1], y[2], y[3]), Code<FORMAT>::pack(y[4], y[5], y[6], y[7]));
+        }
+    }
+    for (int i0 = 0; i0 < n; i0 += ROWS) {
+        if (n > ROWS) load(i0);
+#pragma unroll
+        for (int u = 0; u < kHeld; ++u) {
+            const int i = i0 + u * RPW + sub;
+            if (i >= n) continue;
+            float y[8];
+            raw[u].get(y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] *= inv;
+            const int token = __ldg(a.slots + row0 + i) & mask;
+            *reinterpret_cast<uint2*>(to.block + token * a.p.token_stride + l * 8) =
+                make_uint2(Code<FORMAT>::pack(y[0], y[1], y[2], y[3]), Code<FORMAT>::pack(y[4], y[5], y[6], y[7]));
+        }
+    }
+}
+
+// A warp takes `each` rows (at most 16) of one head's keys or values: the runs
+// that begin there.
+template <int D, int FORMAT>
+__global__ void __launch_bounds__(kThreads)
+paged8_append_kernel(const __grid_constant__ Append8Args a, int each)
+{
+    pdl_begin();
+    const unsigned int w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), columns = 2u * (unsigned int)a.p.Hkv;
+    const int lane = threadIdx.x & 31, column = (int)(w % columns);
+    const long long r0 = (long long)(w / columns) * each;
+    if (r0 >= a.p.T) return;
+    const bool is_v = column >= a.p.Hkv;
+    const int head = is_v ? column - a.p.Hkv : column;
+
+    const int limit = a.p.num_pages << (a.shift - a.bshift);          // blocks of a pool
+    auto block_of = [&](long long row) {
+        const int slot = row >= 0 && row < a.p.T ? __ldg(a.slots + row) : -1;
+        return slot >= 0 && (slot >> a.bshift) < limit ? slot : -1;
+    };
+    // lane l: row r0 - 1 + l
+    const int slot = block_of(r0 - 1 + lane), blk = slot >> a.bshift;  // (-1 for rows that are skipped)
+    const int before = __shfl_up_sync(0xffffffffu, blk, 1);
+    uint32_t leads = __ballot_sync(0xffffffffu, lane >= 1 && lane <= each && blk >= 0 && blk != before);
+    for (; leads; leads &= leads - 1) {
+        const int at = __ffs(leads) - 1, row0 = (int)r0 - 1 + at, b = __shfl_sync(0xffffffffu, blk, at);
+        // the run's rows, and the first of their places in the block
+        uint32_t other = __ballot_sync(0xffffffffu, lane >= at && blk != b);
+        int n = (other ? __ffs(other) - 1 : 32) - at;
+        int first = lane >= at && lane < at + n ? slot : 0x7fffffff;
+        if (!other)
+            for (int i = row0 + n;; i += 32) {
+                const int s = block_of((long long)i + lane);
+                other = __ballot_sync(0xffffffffu, (s >> a.bshift) != b);
+                const int more = other ? __ffs(other) - 1 : 32;
+                if (lane < more) first = min(first, s);
+                n += more;
+                if (other) break;
+            }
+        first = __reduce_min_sync(0xffffffffu, first) & ((1 << a.bshift) - 1);
+        const int token = (b << a.bshift) & ((1 << a.shift) - 1), page = (b << a.bshift) >> a.shift;
+        Place to;
+        to.block = (is_v ? a.v_pages : a.k_pages) + page * a.p.page_stride + head * a.p.head_stride + token * a.p.token_stride;
+        to.scale = (is_v ? a.v_scales : a.k_scales) + scale_at(page, head, token, a.p.Hkv, a.shift, a.bshift);
+        const int type = is_v ? a.p.v_dtype : a.p.k_dtype;
+        const void* x = is_v ? a.v : a.k;
+        const long long stride = is_v ? a.p.v_stride : a.p.k_stride;
+        if (type == FADKV_F32) quantise<float, D, FORMAT>(a, (const float*)x + head * D, stride, to, row0, n, first, lane);
+        else if (type == FADKV_F16) quantise<__half, D, FORMAT>(a, (const __half*)x + head * D, stride, to, row0, n, first, lane);
+        else quantise<__nv_bfloat16, D, FORMAT>(a, (const __nv_bfloat16*)x + head * D, stride, to, row0, n, first, lane);
+    }
+}
+
+template <int D, int FORMAT>
+cudaError_t launch_t(const Append8Args& a, cudaStream_t st)
+{
+    const long long columns = 2ll * a.p.Hkv;
+    const int each = a.p.T * columns <= 152 * 64 ? 1 : 16;
+    const long long warps = (a.p.T + each - 1) / each * columns;
+    if (warps > 0x7fffffffll) return cudaErrorInvalidValue;
+    const unsigned grid = (unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32));
+    return launch_pdl(paged8_append_kernel<D, FORMAT>, dim3(grid), dim3(kThreads), 0, st, a, each);
+}
+
+}  // namespace
+
+cudaError_t launch_paged8_append(const Append8Args& a, cudaStream_t st)
+{
+    if (a.p.T <= 0 || a.p.num_pages <= 0) return cudaSuccess;
+    if (a.p.format == FADKV_E4M3) return a.p.d == 128 ? launch_t<128, FADKV_E4M3>(a, st) : launch_t<64, FADKV_E4M3>(a, st);
+    return a.p.d == 128 ? launch_t<128, FADKV_I8>(a, st) : launch_t<64, FADKV_I8>(a, st);
+}
+
+}  // namespace fadkv

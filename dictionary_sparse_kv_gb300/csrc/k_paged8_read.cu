@@ -1,0 +1,143 @@
+// Reads tokens of the 8-bit pages back as full vectors: code * scale in 32
+// bits, rounded once.
+//
+// Codes are read and vectors written once: HBM.  The work is one list of
+// 16-token tiles, request by request, tile by tile and head by head; every CTA
+// takes an even contiguous share, its warps every fourth tile of it, keys and
+// values together (all their loads in flight at once).
+#include "paged8.cuh"
+
+namespace fadkv {
+namespace {
+
+using namespace paged8;
+
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kTile = 16;
+constexpr int kCtas = 152 * 8;
+
+__device__ __forceinline__ void store8(float* p, const float* y)
+{
+    reinterpret_cast<float4*>(p)[0] = make_float4(y[0], y[1], y[2], y[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(y[4], y[5], y[6], y[7]);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float* y)
+{
+    *reinterpret_cast<uint4*>(p) = make_uint4(Num<T>::pack(y[0], y[1]), Num<T>::pack(y[2], y[3]), Num<T>::pack(y[4], y[5]),
+                                              Num<T>::pack(y[6], y[7]));
+}
+
+template <typename T, int D, int FORMAT>
+__global__ void __launch_bounds__(kThreads)
+paged8_read_kernel(const __grid_constant__ Read8Args a)
+{
+    constexpr int LPR = D / 8, RPW = 32 / LPR, STEPS = kTile / RPW;    // lanes a row, rows a step, steps a tile
+    __shared__ int s_b;
+    __shared__ long long s_base;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.p.B, heads = a.p.Hkv;
+    const int most = a.p.max_pages << a.shift;
+    pdl_begin();
+
+    // tokens lo .. hi-1 of request b, in tiles from t0 on
+    struct Range { int lo, hi, t0, tiles; };
+    auto range = [&](int b) {
+        Range r;
+        r.hi = min(max(__ldg(a.lengths + b), 0), most);
+        r.lo = a.first ? max(__ldg(a.first + b), 0) : 0;
+        r.t0 = r.lo / kTile;
+        r.tiles = r.hi > r.lo ? (r.hi + kTile - 1) / kTile - r.t0 : 0;
+        return r;
+    };
+    long long U, u, u1, base;
+    int cur;
+    {
+        const int each = (B + kThreads - 1) / kThreads, b0 = min(B, tid * each), b1 = min(B, b0 + each);
+        long long mine = 0;
+        for (int b = b0; b < b1; ++b) mine += (long long)range(b).tiles * heads;
+        long long at = paged::block_scan<kThreads>(mine, &U);
+        if (U == 0) return;
+        const long long C = min((long long)gridDim.x, U);
+        if ((long long)blockIdx.x >= C) return;
+        u = U * blockIdx.x / C;
+        u1 = U * (blockIdx.x + 1) / C;
+        if (u >= at && u < at + mine) {
+            int b = b0;
+            for (long long n; u >= at + (n = (long long)range(b).tiles * heads); ++b) at += n;
+            s_b = b;
+            s_base = at;
+        }
+        __syncthreads();
+        cur = s_b;
+        base = s_base;
+    }
+    const int sub = lane / LPR, l = lane % LPR;
+    for (u += warp; u < u1; u += kWarps) {
+        Range r = range(cur);
+        while (u >= base + (long long)r.tiles * heads) {
+            base += (long long)r.tiles * heads;
+            r = range(++cur);
+        }
+        const long long rel = u - base;
+        const int tile = (int)(rel / heads), head = (int)(rel - (long long)tile * heads);
+        const int token = (r.t0 + tile) * kTile, column = token >> a.shift, at = token & ((1 << a.shift) - 1);
+        const long long entry = (long long)cur * a.p.max_pages + column;
+        const int page = __ldg(a.table + entry);
+        const long long to = a.out_table ? __ldg(a.out_table + entry) : entry;
+        if (page < 0 || page >= a.p.num_pages || to < 0 || to >= a.p.out_pages) continue;
+        const size_t sc = scale_at(page, head, at, heads, a.shift, a.bshift);
+        const float ks = __ldg(a.k_scales + sc), vs = __ldg(a.v_scales + sc);
+        const long long from = page * a.p.page_stride + head * a.p.head_stride + at * a.p.token_stride + l * 8;
+        const long long dst = to * a.p.out_page_stride + head * a.p.out_head_stride + at * a.p.out_token_stride + l * 8;
+        uint2 c[2][STEPS];
+#pragma unroll
+        for (int j = 0; j < STEPS; ++j) {
+            const int i = j * RPW + sub;
+            const bool live = token + i >= r.lo && token + i < r.hi;
+            c[0][j] = live ? __ldg(reinterpret_cast<const uint2*>(a.k_pages + from + i * a.p.token_stride)) : make_uint2(0u, 0u);
+            c[1][j] = live ? __ldg(reinterpret_cast<const uint2*>(a.v_pages + from + i * a.p.token_stride)) : make_uint2(0u, 0u);
+        }
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+            for (int j = 0; j < STEPS; ++j) {
+                const int i = j * RPW + sub;
+                if (token + i < r.lo || token + i >= r.hi) continue;
+                float y[8];
+                values<FORMAT>(c[kv][j].x, y);
+                values<FORMAT>(c[kv][j].y, y + 4);
+#pragma unroll
+                for (int x = 0; x < 8; ++x) y[x] *= kv ? vs : ks;
+                store8((T*)(kv ? a.v_out : a.k_out) + dst + i * a.p.out_token_stride, y);
+            }
+    }
+}
+
+template <typename T, int D>
+cudaError_t launch_t(const Read8Args& a, cudaStream_t st)
+{
+    // an upper bound of the tiles: lengths are known on the device only
+    const long long tiles = (((long long)a.p.max_pages << a.shift) / kTile) * a.p.B * a.p.Hkv;
+    const unsigned grid = (unsigned)(tiles < kCtas ? tiles : kCtas);
+    return launch_pdl(a.p.format == FADKV_E4M3 ? paged8_read_kernel<T, D, FADKV_E4M3> : paged8_read_kernel<T, D, FADKV_I8>, dim3(grid),
+                      dim3(kThreads), 0, st, a);
+}
+
+template <typename T>
+cudaError_t launch_d(const Read8Args& a, cudaStream_t st)
+{
+    return a.p.d == 128 ? launch_t<T, 128>(a, st) : launch_t<T, 64>(a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_paged8_read(const Read8Args& a, cudaStream_t st)
+{
+    if (a.p.B <= 0 || a.p.num_pages <= 0 || a.p.out_pages <= 0) return cudaSuccess;
+    if (a.p.out_dtype == FADKV_F32) return launch_d<float>(a, st);
+    if (a.p.out_dtype == FADKV_F16) return launch_d<__half>(a, st);
+    return launch_d<__nv_bfloat16>(a, st);
+}
+
+}  // namespace fadkv

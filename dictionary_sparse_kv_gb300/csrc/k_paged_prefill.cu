@@ -269,7 +269,9 @@ template <int NST> struct Ring {
     }
 };
 
-template <typename T, int D>
+// ROWS: keys and values are rows of their own (packed prompts), row i of a
+// request its token i; no pages and no cached tokens.
+template <typename T, int D, bool ROWS>
 __global__ void __launch_bounds__(kPreThreads, 1)
 paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v, const __grid_constant__ PagedArgs a)
@@ -336,9 +338,14 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             start = __ldg(a.starts + b);
             const int stop = __ldg(a.starts + b + 1);
             if (start >= 0 && stop > start && start < a.p.T) {
-                all = stop - start;
                 cnt = min(stop, a.p.T) - start;
-                my_len = length_of(b, start, a);
+                if (ROWS) {
+                    all = cnt;
+                    my_len = a.positions && __ldg(a.positions + start) < 0 ? 0 : cnt;
+                } else {
+                    all = stop - start;
+                    my_len = length_of(b, start, a);
+                }
             }
         }
         tiles = (cnt + per_item - 1) / per_item;
@@ -387,6 +394,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             const int tiles = ts.count, nq = it.nt > tq ? 2 : 1;
             auto page_of = [&](int i) {
                 int page = a.p.num_pages;                      // outside the map: zeros
+                if (ROWS) return 0;                            // (the rows of a tile are there, or behind the last one: zeros)
                 if (i < tiles && lane < pages) {
                     const int key = ts.key0(i) + row;
                     // a page is asked for if any of its keys is seen: its first one (of the first tokens) or its last
@@ -399,7 +407,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
             int page = page_of(0);
             for (int i = 0; i < tiles && ok; ++i, ++gtile) {
                 const int k0 = ts.key0(i), next = page_of(i + 1);
-                const uint32_t good = __ballot_sync(0xffffffffu, page < a.p.num_pages || lane >= pages);
+                const uint32_t good = ROWS ? 0xffffffffu : __ballot_sync(0xffffffffu, page < a.p.num_pages || lane >= pages);
                 for (int kv = 0; kv < 2; ++kv) {
                     if (!wait(empty(ring.st), ring.ph ^ 1u)) break;
                     if (lane == 0) {
@@ -419,15 +427,22 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
                     }
                     __syncwarp();
                     const CUtensorMap* map = kv ? &map_v : &map_k;
-                    const int y = k0 & ((1 << a.shift) - 1) & ~(rows - 1);
-#pragma unroll 4
-                    for (int j = 0; j < pages; ++j) {
-                        const int w = __shfl_sync(0xffffffffu, page, j);
-                        const uint32_t dst = sR + ring.st * TILE + j * rows * 128;
+                    const uint32_t dst = sR + ring.st * TILE;
+                    if (ROWS) {
                         if (leader)
 #pragma unroll
                             for (int h = 0; h < HALVES; ++h)
-                                tma_load_4d(dst + h * (kKeys * 128), map, h * 64, y, it.hk, w, full(ring.st));
+                                tma_load_3d(dst + h * (kKeys * 128), map, h * 64, it.hk, it.row0 - it.first + k0, full(ring.st));
+                    } else {
+                        const int y = k0 & ((1 << a.shift) - 1) & ~(rows - 1);
+#pragma unroll 4
+                        for (int j = 0; j < pages; ++j) {
+                            const int w = __shfl_sync(0xffffffffu, page, j);
+                            if (leader)
+#pragma unroll
+                                for (int h = 0; h < HALVES; ++h)
+                                    tma_load_4d(dst + j * rows * 128 + h * (kKeys * 128), map, h * 64, y, it.hk, w, full(ring.st));
+                        }
                     }
                     ring.next();
                     ++issued;
@@ -999,19 +1014,20 @@ bool pool_map(CUtensorMap* map, const void* base, const PagedArgs& a)
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Queries as (element, head, row), boxes of 64 elements by the heads and
-// tokens of a tile: row by row as the tile has them.
-bool query_map(CUtensorMap* map, const PagedArgs& a, int heads, int tokens)
+// Rows as (element, head, row).  Queries: boxes of 64 elements by the heads
+// and tokens of a tile, row by row as the tile has them; keys and values of
+// prompts: of one head and a tile's rows.
+bool row_map(CUtensorMap* map, const PagedArgs& a, const void* base, int all, int64_t row, int heads, int tokens)
 {
     auto fn = tma_encode_fn();
     if (!fn) return false;
     const fadkv_paged_params& p = a.p;
-    cuuint64_t dims[3] = {(cuuint64_t)p.d, (cuuint64_t)p.Hq, (cuuint64_t)p.T};
-    cuuint64_t strides[2] = {(cuuint64_t)p.d * 2, (cuuint64_t)p.q_stride * 2};
+    cuuint64_t dims[3] = {(cuuint64_t)p.d, (cuuint64_t)all, (cuuint64_t)p.T};
+    cuuint64_t strides[2] = {(cuuint64_t)p.d * 2, (cuuint64_t)row * 2};
     cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)tokens};
     cuuint32_t estr[3] = {1, 1, 1};
     return fn(map, p.dtype == FADKV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-              const_cast<void*>(a.q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1039,10 +1055,10 @@ PreShape pre_shape(const fadkv_paged_params& p)
     return s;
 }
 
-template <typename T, int D>
-cudaError_t launch_t(const PagedArgs& args, cudaStream_t st)
+template <typename T, int D, bool ROWS>
+cudaError_t launch_rows(const PagedArgs& args, cudaStream_t st)
 {
-    auto k = paged_prefill_kernel<T, D>;
+    auto k = paged_prefill_kernel<T, D, ROWS>;
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, PreCfg<D>::alloc);
     if (e != cudaSuccess) return e;
     PagedArgs a = args;
@@ -1052,13 +1068,22 @@ cudaError_t launch_t(const PagedArgs& args, cudaStream_t st)
     a.tile_ns = a.wait_ns ? 0 : kTileNs;               // (a test's limit is the whole limit)
     a.wait_ns = a.wait_ns ? a.wait_ns : kWaitNs;
     CUtensorMap mq, mk, mv;
-    if (!query_map(&mq, a, s.gch, s.tq) || !pool_map(&mk, a.k, a) || !pool_map(&mv, a.v, a)) return cudaErrorInvalidValue;
+    if (!row_map(&mq, a, a.q, a.p.Hq, a.p.q_stride, s.gch, s.tq)) return cudaErrorInvalidValue;
+    if (ROWS ? !row_map(&mk, a, a.k, a.p.Hkv, a.k_row, 1, kKeys) || !row_map(&mv, a, a.v, a.p.Hkv, a.v_row, 1, kKeys)
+             : !pool_map(&mk, a.k, a) || !pool_map(&mv, a.v, a))
+        return cudaErrorInvalidValue;
     if (s.items > 0x7fffffffll) return cudaErrorInvalidValue;
     const int ctas = s.split || s.items > kPreCtas ? kPreCtas : (int)s.items;
     e = launch_pdl(k, dim3(ctas), dim3(kPreThreads), PreCfg<D>::alloc, st, mq, mk, mv, a);
     if (e != cudaSuccess || !s.split) return e;
     const int items = (int)(s.items < kPreCtas ? s.items : kPreCtas);
     return launch_pdl(paged_prefill_join_kernel<T, D>, dim3(items * s.split, D / 8), dim3(kRows), 0, st, a);
+}
+
+template <typename T, int D>
+cudaError_t launch_t(const PagedArgs& a, cudaStream_t st, bool rows)
+{
+    return rows ? launch_rows<T, D, true>(a, st) : launch_rows<T, D, false>(a, st);
 }
 
 }  // namespace
@@ -1068,11 +1093,11 @@ size_t paged_prefill_workspace(const fadkv_paged_params& p)
     return kHeadBytes + (size_t)kSplitSlots * pre_shape(p).split * slot_floats(p.d) * sizeof(float);
 }
 
-cudaError_t launch_paged_prefill(const PagedArgs& a, cudaStream_t st)
+cudaError_t launch_paged_prefill(const PagedArgs& a, cudaStream_t st, bool rows)
 {
     if (a.p.B <= 0 || a.p.T <= 0) return cudaSuccess;
-    if (a.p.dtype == FADKV_F16) return a.p.d == 128 ? launch_t<__half, 128>(a, st) : launch_t<__half, 64>(a, st);
-    return a.p.d == 128 ? launch_t<__nv_bfloat16, 128>(a, st) : launch_t<__nv_bfloat16, 64>(a, st);
+    if (a.p.dtype == FADKV_F16) return a.p.d == 128 ? launch_t<__half, 128>(a, st, rows) : launch_t<__half, 64>(a, st, rows);
+    return a.p.d == 128 ? launch_t<__nv_bfloat16, 128>(a, st, rows) : launch_t<__nv_bfloat16, 64>(a, st, rows);
 }
 
 }  // namespace fadkv

@@ -51,6 +51,7 @@ struct PagedArgs {
     float scale_log2;         // scale * log2(e): scores in units of powers of two
     const void* k;
     const void* v;
+    int64_t k_row, v_row;     // elements from one row to the next (prompts: keys and values as rows)
     const int32_t* table;
     const int32_t* lengths;
     const int32_t* starts;
@@ -62,8 +63,10 @@ struct PagedArgs {
 };
 size_t paged_attend_workspace(const fadkv_paged_params& p);
 cudaError_t launch_paged_attend(const PagedArgs& a, cudaStream_t st);
+// With `rows` set, keys and values are rows like the queries: a.k and a.v
+// rows, their pages the multiples of a.p.page_size (128) of a request's own.
 size_t paged_prefill_workspace(const fadkv_paged_params& p);
-cudaError_t launch_paged_prefill(const PagedArgs& a, cudaStream_t st);
+cudaError_t launch_paged_prefill(const PagedArgs& a, cudaStream_t st, bool rows = false);
 
 namespace paged {
 

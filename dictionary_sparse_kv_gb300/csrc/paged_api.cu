@@ -7,7 +7,7 @@
 
 #include <atomic>
 
-#include "paged.cuh"
+#include "paged8.cuh"
 
 using namespace fadkv;
 
@@ -87,6 +87,7 @@ PagedArgs paged_args(const fadkv_paged_params& p, const void* k, const void* v, 
     a.scale_log2 = p.scale * 1.44269504088896f;
     a.k = k;
     a.v = v;
+    a.k_row = a.v_row = 0;
     a.table = table;
     a.lengths = lengths;
     a.starts = starts;
@@ -99,6 +100,75 @@ PagedArgs paged_args(const fadkv_paged_params& p, const void* k, const void* v, 
 }
 
 bool dtype_ok(int t) { return t == FADKV_F16 || t == FADKV_F32 || t == FADKV_BF16; }
+
+bool stride8_ok(int64_t s, int64_t least) { return s >= least && s % 16 == 0 && s < ((int64_t)1 << 38); }
+
+// Pools of the 8-bit cache: format, sizes and strides (in bytes).
+fadkv_status check_pool8(int format, int page_size, int num_pages, int block, int Hkv, int d, int64_t page_stride,
+                         int64_t head_stride, int64_t token_stride)
+{
+    if (num_pages < 0 || Hkv < 1 || (format != FADKV_E4M3 && format != FADKV_I8)) return FADKV_ERR_INVALID_ARG;
+    if (!page_size_ok(page_size) || page_size < 16 || block < 16 || block > page_size || (block & (block - 1)) != 0 ||
+        (int64_t)num_pages * page_size > 0x7fffffffll || (d != 64 && d != 128) || Hkv > 4096)
+        return FADKV_ERR_UNSUPPORTED;
+    if (num_pages > 0 && (!stride8_ok(page_stride, d) || !stride8_ok(head_stride, d) || !stride8_ok(token_stride, d)))
+        return FADKV_ERR_INVALID_ARG;
+    return FADKV_OK;
+}
+
+fadkv_status check_paged8(const fadkv_paged8_params* p)
+{
+    if (!p) return FADKV_ERR_INVALID_ARG;
+    if (p->B < 0 || p->Hq < 1 || p->Hkv < 1 || p->Hq % p->Hkv != 0 || p->max_pages < 1 || p->num_pages < 1 ||
+        p->window < 0 || p->sinks < 0 || !isfinite(p->scale) || !dtype_ok(p->dtype))
+        return FADKV_ERR_INVALID_ARG;
+    if (p->dtype == FADKV_F32 || p->B > FADKV_MAX_REQUESTS || p->Hq > 4096) return FADKV_ERR_UNSUPPORTED;
+    const fadkv_status st = check_pool8(p->format, p->page_size, p->num_pages, p->block, p->Hkv, p->d, p->page_stride,
+                                        p->head_stride, p->token_stride);
+    if (st != FADKV_OK) return st;
+    if ((int64_t)p->max_pages * p->page_size > 0x7fffffffll - 4096) return FADKV_ERR_UNSUPPORTED;
+    if (!stride_ok(p->q_stride, (int64_t)p->Hq * p->d) || !stride_ok(p->out_stride, (int64_t)p->Hq * p->d))
+        return FADKV_ERR_INVALID_ARG;
+    return FADKV_OK;
+}
+
+// Prompts as the paged prefill takes them: rows in place of pages.
+constexpr int kPromptShift = 7;
+
+fadkv_status check_prompt(const fadkv_prompt_params* p)
+{
+    if (!p) return FADKV_ERR_INVALID_ARG;
+    if (p->B < 0 || p->T < 0 || p->Hq < 1 || p->Hkv < 1 || p->Hq % p->Hkv != 0 || p->window < 0 || p->sinks < 0 ||
+        !isfinite(p->scale) || !dtype_ok(p->dtype))
+        return FADKV_ERR_INVALID_ARG;
+    if (p->dtype == FADKV_F32 || (p->d != 64 && p->d != 128) || p->B > FADKV_MAX_REQUESTS || p->Hq > 4096 ||
+        p->T > 0x7fffffff - 4096)
+        return FADKV_ERR_UNSUPPORTED;
+    if (!stride_ok(p->q_stride, (int64_t)p->Hq * p->d) || !stride_ok(p->out_stride, (int64_t)p->Hq * p->d) ||
+        !stride_ok(p->k_stride, (int64_t)p->Hkv * p->d) || !stride_ok(p->v_stride, (int64_t)p->Hkv * p->d))
+        return FADKV_ERR_INVALID_ARG;
+    return FADKV_OK;
+}
+
+fadkv_paged_params prompt_shape(const fadkv_prompt_params& p)
+{
+    fadkv_paged_params s;
+    s.B = p.B;
+    s.T = p.T;
+    s.Hq = p.Hq;
+    s.Hkv = p.Hkv;
+    s.d = p.d;
+    s.dtype = p.dtype;
+    s.page_size = 1 << kPromptShift;
+    s.num_pages = s.max_pages = p.T > 0 ? ((p.T - 1) >> kPromptShift) + 1 : 1;
+    s.window = p.window;
+    s.sinks = p.sinks;
+    s.scale = p.scale;
+    s.q_stride = p.q_stride;
+    s.out_stride = p.out_stride;
+    s.page_stride = s.head_stride = s.token_stride = 0;
+    return s;
+}
 
 }  // namespace
 
@@ -325,6 +395,162 @@ fadkv_status fadkv_paged_prefill_planned(const fadkv_paged_params* p, const void
 {
     return paged_call("fadkv_paged_prefill_planned", true, p, k_pages, v_pages, block_table, lengths, starts,
                       positions, q, out, lse, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"
+
+extern "C" {
+
+fadkv_status fadkv_paged8_append(const fadkv_append8_params* p, const void* k, const void* v, const int32_t* slots,
+                                 void* k_pages, void* v_pages, float* k_scales, float* v_scales, void* stream)
+{
+    if (!p || p->T < 0 || !dtype_ok(p->k_dtype) || !dtype_ok(p->v_dtype)) return FADKV_ERR_INVALID_ARG;
+    const fadkv_status st = check_pool8(p->format, p->page_size, p->num_pages, p->block, p->Hkv, p->d, p->page_stride,
+                                        p->head_stride, p->token_stride);
+    if (st != FADKV_OK) return st;
+    if (!stride_ok(p->k_stride, (int64_t)p->Hkv * p->d) || !stride_ok(p->v_stride, (int64_t)p->Hkv * p->d))
+        return FADKV_ERR_INVALID_ARG;
+    if (p->T > 0 && p->num_pages > 0) {
+        if (!k || !v || !slots || !k_pages || !v_pages || !k_scales || !v_scales) return FADKV_ERR_INVALID_ARG;
+        if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(slots, 4) ||
+            !aligned(k_scales, 4) || !aligned(v_scales, 4))
+            return FADKV_ERR_INVALID_ARG;
+    }
+    if (fault_injected()) return cuda_error("fadkv_paged8_append", cudaErrorLaunchFailure);
+    Append8Args a;
+    a.p = *p;
+    a.shift = log2_exact(p->page_size);
+    a.bshift = log2_exact(p->block);
+    a.k = k;
+    a.v = v;
+    a.slots = slots;
+    a.k_pages = (uint8_t*)k_pages;
+    a.v_pages = (uint8_t*)v_pages;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    const cudaError_t e = launch_paged8_append(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? FADKV_OK : cuda_error("fadkv_paged8_append", e);
+}
+
+fadkv_status fadkv_paged8_read(const fadkv_read8_params* p, const void* k_pages, const void* v_pages,
+                               const float* k_scales, const float* v_scales, const int32_t* block_table,
+                               const int32_t* lengths, const int32_t* first, const int32_t* out_table, void* k_out,
+                               void* v_out, void* stream)
+{
+    if (!p || p->B < 0 || p->max_pages < 1 || p->out_pages < 0 || !dtype_ok(p->out_dtype)) return FADKV_ERR_INVALID_ARG;
+    if (p->B > FADKV_MAX_REQUESTS) return FADKV_ERR_UNSUPPORTED;
+    const fadkv_status st = check_pool8(p->format, p->page_size, p->num_pages, p->block, p->Hkv, p->d, p->page_stride,
+                                        p->head_stride, p->token_stride);
+    if (st != FADKV_OK) return st;
+    if ((int64_t)p->max_pages * p->page_size > 0x7fffffffll - 4096) return FADKV_ERR_UNSUPPORTED;
+    if (p->out_pages > 0 && (!stride_ok(p->out_page_stride, p->d) || !stride_ok(p->out_head_stride, p->d) ||
+                             !stride_ok(p->out_token_stride, p->d)))
+        return FADKV_ERR_INVALID_ARG;
+    if (p->B > 0 && p->num_pages > 0 && p->out_pages > 0) {
+        if (!k_pages || !v_pages || !k_scales || !v_scales || !block_table || !lengths || !k_out || !v_out)
+            return FADKV_ERR_INVALID_ARG;
+        if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(k_out, 16) || !aligned(v_out, 16) ||
+            !aligned(k_scales, 4) || !aligned(v_scales, 4) || !aligned(block_table, 4) || !aligned(lengths, 4) ||
+            !aligned(first, 4) || !aligned(out_table, 4))
+            return FADKV_ERR_INVALID_ARG;
+    }
+    if (fault_injected()) return cuda_error("fadkv_paged8_read", cudaErrorLaunchFailure);
+    Read8Args a;
+    a.p = *p;
+    a.shift = log2_exact(p->page_size);
+    a.bshift = log2_exact(p->block);
+    a.k_pages = (const uint8_t*)k_pages;
+    a.v_pages = (const uint8_t*)v_pages;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.table = block_table;
+    a.lengths = lengths;
+    a.first = first;
+    a.out_table = out_table;
+    a.k_out = k_out;
+    a.v_out = v_out;
+    const cudaError_t e = launch_paged8_read(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? FADKV_OK : cuda_error("fadkv_paged8_read", e);
+}
+
+fadkv_status fadkv_paged8_attend_workspace_bytes(const fadkv_paged8_params* p, size_t* bytes)
+{
+    const fadkv_status st = check_paged8(p);
+    if (st != FADKV_OK) return st;
+    if (!bytes) return FADKV_ERR_INVALID_ARG;
+    *bytes = paged8_attend_workspace(*p);
+    return FADKV_OK;
+}
+
+fadkv_status fadkv_paged8_attend(const fadkv_paged8_params* p, const void* k_pages, const void* v_pages,
+                                 const float* k_scales, const float* v_scales, const int32_t* block_table,
+                                 const int32_t* lengths, const int32_t* positions, const void* q, void* out, float* lse,
+                                 void* workspace, size_t workspace_bytes, void* stream)
+{
+    const fadkv_status st = check_paged8(p);
+    if (st != FADKV_OK) return st;
+    if (workspace_bytes < paged8_attend_workspace(*p) || !workspace) return FADKV_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return FADKV_ERR_INVALID_ARG;
+    if (p->B > 0) {
+        if (!k_pages || !v_pages || !k_scales || !v_scales || !block_table || !lengths || !q || !out)
+            return FADKV_ERR_INVALID_ARG;
+        if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(k_scales, 4) || !aligned(v_scales, 4) ||
+            !aligned(block_table, 4) || !aligned(lengths, 4) || !aligned(positions, 4) || !aligned(q, 16) ||
+            !aligned(out, 16) || !aligned(lse, 4))
+            return FADKV_ERR_INVALID_ARG;
+    }
+    if (fault_injected()) return cuda_error("fadkv_paged8_attend", cudaErrorLaunchFailure);
+    Paged8Args a;
+    a.p = *p;
+    a.shift = log2_exact(p->page_size);
+    a.bshift = log2_exact(p->block);
+    a.grp = p->Hq / p->Hkv;
+    a.scale_log2 = p->scale * 1.44269504088896f;
+    a.k = (const uint8_t*)k_pages;
+    a.v = (const uint8_t*)v_pages;
+    a.k_scales = k_scales;
+    a.v_scales = v_scales;
+    a.table = block_table;
+    a.lengths = lengths;
+    a.positions = positions;
+    a.q = q;
+    a.out = out;
+    a.lse = lse;
+    a.ws = workspace;
+    const cudaError_t e = launch_paged8_attend(a, (cudaStream_t)stream);
+    return e == cudaSuccess ? FADKV_OK : cuda_error("fadkv_paged8_attend", e);
+}
+
+fadkv_status fadkv_prompt_attend_workspace_bytes(const fadkv_prompt_params* p, size_t* bytes)
+{
+    const fadkv_status st = check_prompt(p);
+    if (st != FADKV_OK) return st;
+    if (!bytes) return FADKV_ERR_INVALID_ARG;
+    *bytes = paged_prefill_workspace(prompt_shape(*p));
+    return FADKV_OK;
+}
+
+fadkv_status fadkv_prompt_attend(const fadkv_prompt_params* p, const void* q, const void* k, const void* v,
+                                 const int32_t* starts, const int32_t* positions, void* out, float* lse,
+                                 void* workspace, size_t workspace_bytes, void* stream)
+{
+    const fadkv_status st = check_prompt(p);
+    if (st != FADKV_OK) return st;
+    const fadkv_paged_params shape = prompt_shape(*p);
+    if (workspace_bytes < paged_prefill_workspace(shape) || !workspace) return FADKV_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return FADKV_ERR_INVALID_ARG;
+    if (p->B > 0 && p->T > 0) {
+        if (!q || !k || !v || !starts || !out) return FADKV_ERR_INVALID_ARG;
+        if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(starts, 4) ||
+            !aligned(positions, 4) || !aligned(lse, 4))
+            return FADKV_ERR_INVALID_ARG;
+    }
+    if (fault_injected()) return cuda_error("fadkv_prompt_attend", cudaErrorLaunchFailure);
+    PagedArgs a = paged_args(shape, k, v, nullptr, nullptr, starts, positions, q, out, lse, workspace);
+    a.k_row = p->k_stride;
+    a.v_row = p->v_stride;
+    const cudaError_t e = launch_paged_prefill(a, (cudaStream_t)stream, true);
+    return e == cudaSuccess ? FADKV_OK : cuda_error("fadkv_prompt_attend", e);
 }
 
 }  // extern "C"

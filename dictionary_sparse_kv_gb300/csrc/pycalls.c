@@ -14,17 +14,17 @@
 #include "fadkv.h"
 
 static PyObject* s_data_ptr;
-enum { PAGE, QK, ROPE, PAGED, TYPES };
+enum { PAGE, QK, ROPE, PAGED, APPEND8, READ8, PAGED8, PROMPT, TYPES };
 static PyTypeObject* s_types[TYPES];
 
-/* types(PageParams, QkParams, Rope, PagedParams): the structs' classes. */
+/* types(PageParams, QkParams, Rope, PagedParams, Append8Params, Read8Params, Paged8Params, PromptParams): the structs' classes. */
 static PyObject* types(PyObject* self, PyObject* const* args, Py_ssize_t n)
 {
     (void)self;
     for (Py_ssize_t i = 0; i < n; ++i)
         if (n != TYPES || !PyType_Check(args[i])) n = -1;
     if (n != TYPES) {
-        PyErr_SetString(PyExc_TypeError, "four classes wanted");
+        PyErr_SetString(PyExc_TypeError, "eight classes wanted");
         return NULL;
     }
     for (int i = 0; i < TYPES; ++i) {
@@ -159,12 +159,88 @@ static PyObject* paged_prefill(PyObject* self, PyObject* const* args, Py_ssize_t
     return PyLong_FromLong(rc);
 }
 
+/* (function, params, 7 arrays, stream) */
+static PyObject* paged8_append(PyObject* self, PyObject* const* args, Py_ssize_t n)
+{
+    void *f, *p[8];
+    const void* params;
+    (void)self;
+    if (arity(n, 10) || address(args[0], &f) || structure(args[1], APPEND8, sizeof(fadkv_append8_params), &params) ||
+        pointers(args + 2, 8, p))
+        return NULL;
+    __typeof__(&fadkv_paged8_append) call = (__typeof__(&fadkv_paged8_append))f;
+    fadkv_status rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = call(params, p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7]);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+/* (function, params, 10 arrays, stream) */
+static PyObject* paged8_read(PyObject* self, PyObject* const* args, Py_ssize_t n)
+{
+    void *f, *p[11];
+    const void* params;
+    (void)self;
+    if (arity(n, 13) || address(args[0], &f) || structure(args[1], READ8, sizeof(fadkv_read8_params), &params) ||
+        pointers(args + 2, 11, p))
+        return NULL;
+    __typeof__(&fadkv_paged8_read) call = (__typeof__(&fadkv_paged8_read))f;
+    fadkv_status rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = call(params, p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8], p[9], p[10]);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+/* (function, params, 10 arrays, workspace, bytes, stream) */
+static PyObject* paged8_attend(PyObject* self, PyObject* const* args, Py_ssize_t n)
+{
+    void *f, *p[11], *st;
+    const void* params;
+    (void)self;
+    if (arity(n, 15) || address(args[0], &f) || structure(args[1], PAGED8, sizeof(fadkv_paged8_params), &params) ||
+        pointers(args + 2, 11, p) || address(args[14], &st))
+        return NULL;
+    const size_t bytes = PyLong_AsSize_t(args[13]);
+    if (PyErr_Occurred()) return NULL;
+    __typeof__(&fadkv_paged8_attend) call = (__typeof__(&fadkv_paged8_attend))f;
+    fadkv_status rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = call(params, p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8], p[9], p[10], bytes, st);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
+/* (function, params, 7 arrays, workspace, bytes, stream) */
+static PyObject* prompt_attend(PyObject* self, PyObject* const* args, Py_ssize_t n)
+{
+    void *f, *p[8], *st;
+    const void* params;
+    (void)self;
+    if (arity(n, 12) || address(args[0], &f) || structure(args[1], PROMPT, sizeof(fadkv_prompt_params), &params) ||
+        pointers(args + 2, 8, p) || address(args[11], &st))
+        return NULL;
+    const size_t bytes = PyLong_AsSize_t(args[10]);
+    if (PyErr_Occurred()) return NULL;
+    __typeof__(&fadkv_prompt_attend) call = (__typeof__(&fadkv_prompt_attend))f;
+    fadkv_status rc;
+    Py_BEGIN_ALLOW_THREADS
+    rc = call(params, p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], bytes, st);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(rc);
+}
+
 static PyMethodDef methods[] = {
     {"types", (PyCFunction)(void (*)(void))types, METH_FASTCALL, NULL},
     {"page_plan", (PyCFunction)(void (*)(void))page_plan, METH_FASTCALL, NULL},
     {"qk_norm_rope", (PyCFunction)(void (*)(void))qk_norm_rope, METH_FASTCALL, NULL},
     {"paged_attend", (PyCFunction)(void (*)(void))paged_attend, METH_FASTCALL, NULL},
     {"paged_prefill", (PyCFunction)(void (*)(void))paged_prefill, METH_FASTCALL, NULL},
+    {"paged8_append", (PyCFunction)(void (*)(void))paged8_append, METH_FASTCALL, NULL},
+    {"paged8_read", (PyCFunction)(void (*)(void))paged8_read, METH_FASTCALL, NULL},
+    {"paged8_attend", (PyCFunction)(void (*)(void))paged8_attend, METH_FASTCALL, NULL},
+    {"prompt_attend", (PyCFunction)(void (*)(void))prompt_attend, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL},
 };
 

@@ -24,6 +24,7 @@ CALLS_PATH = os.path.join(_PKG, "_build", "_fadkv_calls.so")
 F16 = 0
 F32 = 1
 BF16 = 2                                  # the paged-cache calls only
+E4M3, I8 = 3, 4                           # formats of the 8-bit paged cache
 STATS_FIELDS = 8
 STATS_NAMES = ("encoded", "replaced", "flagged", "overflow", "nonfinite", "topn_slow_path", "status", "reserved")
 DEV_NONFINITE_INPUT = 0x1
@@ -103,6 +104,29 @@ class PagedParams(C.Structure):
         (n, C.c_int64) for n in ("q_stride", "out_stride", "page_stride", "head_stride", "token_stride")]
 
 
+class Append8Params(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("T", "Hkv", "d", "k_dtype", "v_dtype", "format", "page_size", "num_pages", "block")] + [
+        (n, C.c_int64) for n in ("k_stride", "v_stride", "page_stride", "head_stride", "token_stride")]
+
+
+class Read8Params(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("B", "Hkv", "d", "format", "page_size", "num_pages", "max_pages", "block", "out_dtype",
+                                         "out_pages")] + [
+        (n, C.c_int64) for n in ("page_stride", "head_stride", "token_stride", "out_page_stride", "out_head_stride",
+                                 "out_token_stride")]
+
+
+class Paged8Params(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("B", "Hq", "Hkv", "d", "dtype", "format", "page_size", "num_pages", "max_pages", "block",
+                                         "window", "sinks")] + [("scale", C.c_float)] + [
+        (n, C.c_int64) for n in ("q_stride", "out_stride", "page_stride", "head_stride", "token_stride")]
+
+
+class PromptParams(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("B", "T", "Hq", "Hkv", "d", "dtype", "window", "sinks")] + [("scale", C.c_float)] + [
+        (n, C.c_int64) for n in ("q_stride", "k_stride", "v_stride", "out_stride")]
+
+
 def params(num_dicts, N, d, n, s, dtype=F16, max_batch=1, lambda_abs=1e-4, lambda_rel=0.20) -> Params:
     """Handle parameters; the ridge defaults are Table 5's 1e-4 + 0.20 diag(G)."""
     return Params(num_dicts, N, d, n, s, lambda_abs, lambda_rel, dtype, max_batch)
@@ -154,6 +178,12 @@ _SIGS = {
     "fadkv_paged_prefill_workspace_bytes": ([C.POINTER(PagedParams), C.POINTER(C.c_size_t)], C.c_int),
     "fadkv_paged_status": ([C.c_void_p, C.POINTER(C.c_uint64), C.c_int32, C.c_void_p], C.c_int),
     "fadkv_debug_paged_wait_limit": ([C.c_uint64], C.c_int),
+    "fadkv_paged8_append": ([C.POINTER(Append8Params)] + [C.c_void_p] * 8, C.c_int),
+    "fadkv_paged8_read": ([C.POINTER(Read8Params)] + [C.c_void_p] * 11, C.c_int),
+    "fadkv_paged8_attend": ([C.POINTER(Paged8Params)] + [C.c_void_p] * 11 + [C.c_size_t, C.c_void_p], C.c_int),
+    "fadkv_paged8_attend_workspace_bytes": ([C.POINTER(Paged8Params), C.POINTER(C.c_size_t)], C.c_int),
+    "fadkv_prompt_attend": ([C.POINTER(PromptParams)] + [C.c_void_p] * 8 + [C.c_size_t, C.c_void_p], C.c_int),
+    "fadkv_prompt_attend_workspace_bytes": ([C.POINTER(PromptParams), C.POINTER(C.c_size_t)], C.c_int),
     "fadkv_profile_enable": ([C.c_void_p, C.c_int32], C.c_int),
     "fadkv_profile_select": ([C.c_void_p, C.c_uint32], C.c_int),
     "fadkv_profile_read": ([C.c_void_p, C.POINTER(C.c_int64), C.POINTER(C.c_double), C.c_int32], C.c_int),
@@ -198,9 +228,11 @@ def _load_calls():
             loader = importlib.machinery.ExtensionFileLoader("_fadkv_calls", CALLS_PATH)
             m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fadkv_calls", loader))
             loader.exec_module(m)
-            m.types(PageParams, QkParams, Rope, PagedParams)
+            m.types(PageParams, QkParams, Rope, PagedParams, Append8Params, Read8Params, Paged8Params, PromptParams)
             for name, function in (("page_plan", "page_plan"), ("qk_norm_rope", "qk_norm_rope"),
-                                   ("paged_attend", "paged_attend_planned"), ("paged_prefill", "paged_prefill_planned")):
+                                   ("paged_attend", "paged_attend_planned"), ("paged_prefill", "paged_prefill_planned"),
+                                   ("paged8_append", "paged8_append"), ("paged8_read", "paged8_read"),
+                                   ("paged8_attend", "paged8_attend"), ("prompt_attend", "prompt_attend")):
                 _direct[name] = C.cast(getattr(L, "fadkv_" + function), C.c_void_p).value
             _calls = m
     return _calls
@@ -533,6 +565,152 @@ def paged_status(workspace, clear: bool = True, stream=None) -> int:
 def debug_paged_wait_limit(limit_ns: int) -> None:
     """Test hook: limit of the pipeline's waits of paged_prefill calls from now on (0 = default)."""
     _check("fadkv_debug_paged_wait_limit", lib().fadkv_debug_paged_wait_limit(int(limit_ns)))
+
+
+# --- the paged cache in 8 bits, and attention of prompts over their own rows ---
+
+def _pool8(pages, layout, scales, v_pages, v_scales):
+    """(format, block, Hkv, page size, page stride, head stride, token stride) of an 8-bit pool (float8_e4m3fn or int8) and
+    its scales [pages][Hkv][page size / block]."""
+    import torch
+    formats = {torch.float8_e4m3fn: E4M3, torch.int8: I8}
+    if pages.dtype not in formats:
+        raise ValueError("an 8-bit pool is of float8_e4m3fn or int8")
+    hkv, ps, *strides = _pool(pages, layout)
+    _check_pools(pages, v_pages)
+    if scales.dim() != 3 or scales.shape[2] < 1 or ps % scales.shape[2]:
+        raise ValueError("scales are [pages][Hkv][page size / block]")
+    shape = (pages.shape[0], hkv, scales.shape[2])
+    _check_dense("scales", scales, shape, torch.float32)
+    _check_dense("scales", v_scales, shape, torch.float32)
+    return (formats[pages.dtype], ps // scales.shape[2], hkv, ps, *strides)
+
+
+def _check_rows(*rows):
+    for x in rows:
+        if x.dim() != 3 or x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2]):
+            raise ValueError("rows are [rows][heads][d] with the heads back to back")
+
+
+def _check_table(table, shape=None):
+    import torch
+    if table.dim() != 2 or table.dtype != torch.int32 or not table.is_contiguous() or (shape and tuple(table.shape) != tuple(shape)):
+        raise ValueError("block tables are contiguous [B][max_pages] int32")
+
+
+def append8_params(k, v, k_pages, layout: str = "head", k_scales=None, v_pages=None, v_scales=None) -> Append8Params:
+    """Parameters of paged8_append from tensors k, v [T][Hkv][d] (heads contiguous, rows at any stride), an 8-bit pool and its
+    scales.  The call itself sees addresses alone: v_pages and v_scales, where given, are checked here."""
+    _check_rows(k, v)
+    fmt, block, hkv, ps, *strides = _pool8(k_pages, layout, k_scales, v_pages, v_scales)
+    T, _, d = k.shape
+    if k.shape != v.shape or k.shape[1] != hkv or k_pages.shape[3] != d:
+        raise ValueError("k and v are [T][Hkv][d], Hkv and d as in the pool")
+    return Append8Params(T, hkv, d, _dtype(k), _dtype(v), fmt, ps, k_pages.shape[0], block, _stride(k, 0, hkv * d),
+                         _stride(v, 0, hkv * d), *strides)
+
+
+def paged8_append(p: Append8Params, k, v, slots, k_pages, v_pages, k_scales, v_scales, stream=None) -> None:
+    """Keys and values quantised into the 8-bit pools (see fadkv_paged8_append)."""
+    rc = (_calls or _load_calls()).paged8_append(_direct["paged8_append"], p, k, v, slots, k_pages, v_pages, k_scales, v_scales,
+                                                 _stream(stream, k, k_pages))
+    if rc:
+        _check("fadkv_paged8_append", rc)
+
+
+def read8_params(k_pages, k_scales, k_out, block_table, layout: str = "head", out_layout=None, v_pages=None, v_scales=None,
+                 v_out=None, out_table=None) -> Read8Params:
+    """Parameters of paged8_read from an 8-bit pool, its scales, an output pool of full vectors with pages of the same size (in
+    out_layout, by default the pool's) and the block tables.  The call itself sees addresses alone: the other tensors, where
+    given, are checked here."""
+    fmt, block, hkv, ps, *strides = _pool8(k_pages, layout, k_scales, v_pages, v_scales)
+    out_hkv, out_ps, *out_strides = _pool(k_out, out_layout or layout)
+    _check_pools(k_out, v_out)
+    if (out_hkv, out_ps, k_out.shape[3]) != (hkv, ps, k_pages.shape[3]):
+        raise ValueError("the output pools have the 8-bit pools' heads, page size and dimension")
+    _check_table(block_table)
+    if out_table is not None:
+        _check_table(out_table, block_table.shape)
+    return Read8Params(block_table.shape[0], hkv, k_pages.shape[3], fmt, ps, k_pages.shape[0], block_table.shape[1], block,
+                       _dtype(k_out), k_out.shape[0], *strides, *out_strides)
+
+
+def paged8_read(p: Read8Params, k_pages, v_pages, k_scales, v_scales, block_table, lengths, first, out_table, k_out, v_out,
+                stream=None) -> None:
+    """Tokens of the 8-bit pools as full vectors (see fadkv_paged8_read)."""
+    rc = (_calls or _load_calls()).paged8_read(_direct["paged8_read"], p, k_pages, v_pages, k_scales, v_scales, block_table,
+                                               lengths, first, out_table, k_out, v_out, _stream(stream, k_pages, k_out))
+    if rc:
+        _check("fadkv_paged8_read", rc)
+
+
+def paged8_params(q, out, k_pages, k_scales, layout: str = "head", block_table=None, window: int = 0, sinks: int = 0, scale=None,
+                  v_pages=None, v_scales=None, lse=None) -> Paged8Params:
+    """Parameters of paged8_attend from tensors q, out [B][Hq][d] (heads contiguous), an 8-bit pool, its scales and the block
+    tables [B][max_pages].  The call itself sees addresses alone: the other tensors, where given, are checked here."""
+    _check_rows(q, out)
+    fmt, block, hkv, ps, *strides = _pool8(k_pages, layout, k_scales, v_pages, v_scales)
+    if q.shape != out.shape or q.dtype != out.dtype or k_pages.shape[3] != q.shape[2]:
+        raise ValueError("q and out have one shape and type, and the pool's dimension")
+    B, Hq, d = q.shape
+    _check_table(block_table)
+    if block_table.shape[0] != B:
+        raise ValueError("q has one row a request")
+    if lse is not None:
+        import torch
+        _check_dense("lse", lse, (B, Hq), torch.float32)
+    return Paged8Params(B, Hq, hkv, d, _dtype(q), fmt, ps, k_pages.shape[0], block_table.shape[1], block, window, sinks,
+                        d ** -0.5 if scale is None else scale, _stride(q, 0, Hq * d), _stride(out, 0, Hq * d), *strides)
+
+
+def paged8_attend_workspace_bytes(p: Paged8Params) -> int:
+    out = C.c_size_t(0)
+    _check("fadkv_paged8_attend_workspace_bytes", lib().fadkv_paged8_attend_workspace_bytes(C.byref(p), C.byref(out)))
+    return out.value
+
+
+def paged8_attend(p: Paged8Params, k_pages, v_pages, k_scales, v_scales, block_table, lengths, q, out, lse, workspace, stream=None,
+                  positions=None) -> None:
+    """Attention of one new token per request over the 8-bit pages (see fadkv_paged8_attend).  The workspace is zero-filled
+    before its first use.  With a plan's positions, requests that it refused see nothing."""
+    rc = (_calls or _load_calls()).paged8_attend(_direct["paged8_attend"], p, k_pages, v_pages, k_scales, v_scales, block_table,
+                                                 lengths, positions, q, out, lse, workspace,
+                                                 _nbytes(workspace, paged8_attend_workspace_bytes, p), _stream(stream, q, out))
+    if rc:
+        _check("fadkv_paged8_attend", rc)
+
+
+def prompt_params(q, k, v, out, B: int, window: int = 0, sinks: int = 0, scale=None, lse=None) -> PromptParams:
+    """Parameters of prompt_attend from tensors q, out [T][Hq][d] and k, v [T][Hkv][d] (heads contiguous, rows at any stride)
+    of B prompts.  The call itself sees addresses alone: lse, where given, is checked here."""
+    _check_rows(q, k, v, out)
+    if not q.dtype == k.dtype == v.dtype == out.dtype:
+        raise ValueError("q, k, v and out have one type")
+    T, Hq, d = q.shape
+    if out.shape != q.shape or k.shape != v.shape or k.shape[0] != T or k.shape[2] != d:
+        raise ValueError("q and out are [T][Hq][d], k and v [T][Hkv][d]")
+    if lse is not None:
+        import torch
+        _check_dense("lse", lse, (T, Hq), torch.float32)
+    hkv = k.shape[1]
+    return PromptParams(B, T, Hq, hkv, d, _dtype(q), window, sinks, d ** -0.5 if scale is None else scale, _stride(q, 0, Hq * d),
+                        _stride(k, 0, hkv * d), _stride(v, 0, hkv * d), _stride(out, 0, Hq * d))
+
+
+def prompt_attend_workspace_bytes(p: PromptParams) -> int:
+    out = C.c_size_t(0)
+    _check("fadkv_prompt_attend_workspace_bytes", lib().fadkv_prompt_attend_workspace_bytes(C.byref(p), C.byref(out)))
+    return out.value
+
+
+def prompt_attend(p: PromptParams, q, k, v, starts, out, lse=None, workspace=None, stream=None, positions=None) -> None:
+    """Causal attention of packed prompts over their own keys and values (see fadkv_prompt_attend).  The workspace is
+    zero-filled before its first use; paged_status reads its status word.  With a plan's positions, prompts that it refused
+    see nothing."""
+    rc = (_calls or _load_calls()).prompt_attend(_direct["prompt_attend"], p, q, k, v, starts, positions, out, lse, workspace,
+                                                 _nbytes(workspace, prompt_attend_workspace_bytes, p), _stream(stream, q, out))
+    if rc:
+        _check("fadkv_prompt_attend", rc)
 
 
 def reconstruct(h: int, V: int, idx, coef, repl_id, repl_coef, xhat, stream=None) -> None:

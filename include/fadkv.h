@@ -82,8 +82,9 @@ typedef enum {
 } fadkv_status;
 
 /* FADKV_BF16 is taken by the paged-cache calls only; dictionaries and codes
-   are binary16 or binary32. */
-typedef enum { FADKV_F16 = 0, FADKV_F32 = 1, FADKV_BF16 = 2 } fadkv_dtype;
+   are binary16 or binary32.  FADKV_E4M3 and FADKV_I8 are formats of the 8-bit
+   paged cache. */
+typedef enum { FADKV_F16 = 0, FADKV_F32 = 1, FADKV_BF16 = 2, FADKV_E4M3 = 3, FADKV_I8 = 4 } fadkv_dtype;
 
 /* Device status word bits (per dictionary, see fadkv_dict_stats). */
 #define FADKV_DEV_NONFINITE_INPUT 0x1   /* an input held a NaN or infinity */
@@ -633,6 +634,165 @@ fadkv_status fadkv_paged_status(void* workspace, uint64_t* host_out, int32_t cle
 fadkv_status fadkv_debug_paged_wait_limit(uint64_t limit_ns);
 
 fadkv_status fadkv_paged_prefill_workspace_bytes(const fadkv_paged_params* params, size_t* bytes);
+
+/* ---------------------------------------------------------------------------
+   The paged cache in 8 bits: the same pages at half the bytes, with a scale
+   for each block of tokens and head.  Handle-free and asynchronous as above;
+   block tables, lengths, positions and slots are fadkv_page_plan's.
+
+   Pools are laid out as above with elements of one byte: page_size a power of
+   two, 16 .. 1024, strides multiples of 16, pools 16-byte aligned.  A block is
+   `block` consecutive tokens of a page (a power of two, 16 .. page_size), and
+   a token's value is its code times the scale of its block:
+     k_scales, v_scales  [num_pages][Hkv][page_size / block] float32
+   Scales are positive and finite; fadkv_paged8_append writes powers of two,
+   the other calls take any.
+     FADKV_E4M3  sign, 4 bits of exponent, 3 of fraction, largest 448; the
+                 codes 0x7f and 0xff are NaN
+     FADKV_I8    whole numbers; -127 .. 127 are written
+   --------------------------------------------------------------------------- */
+
+typedef struct {
+    int32_t T;            /* rows (new tokens of the step) */
+    int32_t Hkv;
+    int32_t d;            /* head dimension: 64 or 128 */
+    int32_t k_dtype, v_dtype;   /* of the rows: FADKV_F16, FADKV_BF16 or FADKV_F32 */
+    int32_t format;       /* FADKV_E4M3 or FADKV_I8 */
+    int32_t page_size, num_pages, block;
+    int64_t k_stride, v_stride;   /* elements from one token to the next, multiples of 8 */
+    int64_t page_stride, head_stride, token_stride;   /* of the pools, bytes */
+} fadkv_append8_params;
+
+/* Quantises one step's keys and values into the pages.  For each block and
+   head that gets tokens, with a the largest |x| of the finite elements that
+   this call writes there, M = 448 (E4M3) or 127 (I8) and t the least power of
+   two with a <= M t (2^-126 at least):
+     s = t, if the block's first token is among them;
+     s = max(its scale, t), if not.  Where that is more, the codes of the
+         block's tokens before the new ones are rounded again: code * (scale / s).
+   The new codes are x / s, rounded to nearest, ties to even (a scale that is no
+   power of two: x * (1 / s) and code * (scale / s) in 32 bits, rounded).  A
+   scale of powers of two that grows at least doubles: an I8 code that is
+   rounded again and again ends less than one step of the last scale from its
+   value; an E4M3 code changes only where it leaves the type's normal range.  A
+   NaN becomes NaN in E4M3 and 0 in I8, an infinity NaN in E4M3 and the largest
+   code of its sign in I8.
+     k, v        rows of Hkv heads of d elements, heads back to back, rows
+                 k_stride (v_stride) apart; 16-byte aligned.  k is the k_out of
+                 fadkv_qk_norm_rope, say, and v a part of a projection's output
+     slots       [T] int32: where row t goes; slots outside
+                 [0, num_pages * page_size) are skipped.  Rows of one block are
+                 consecutive rows (as a plan gives them; in any order), and a
+                 slot appears once at most.  A block's tokens are filled in
+                 their order: tokens behind those of this call are not the
+                 block's any more if its scale changes.
+   Pools and scales do not overlap the inputs.  The call can be repeated on the
+   same inputs with the same result.
+   Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+fadkv_status fadkv_paged8_append(const fadkv_append8_params* params, const void* k, const void* v,
+                                 const int32_t* slots, void* k_pages, void* v_pages, float* k_scales,
+                                 float* v_scales, void* stream);
+
+typedef struct {
+    int32_t B;            /* requests, 0 .. FADKV_MAX_REQUESTS */
+    int32_t Hkv;
+    int32_t d;            /* head dimension: 64 or 128 */
+    int32_t format;       /* FADKV_E4M3 or FADKV_I8 */
+    int32_t page_size, num_pages, max_pages, block;
+    int32_t out_dtype;    /* FADKV_F16, FADKV_BF16 or FADKV_F32 */
+    int32_t out_pages;    /* pages of the output pools */
+    int64_t page_stride, head_stride, token_stride;               /* of the 8-bit pools, bytes */
+    int64_t out_page_stride, out_head_stride, out_token_stride;   /* of the output pools, elements, multiples of 8 */
+} fadkv_read8_params;
+
+/* Reads tokens back as full vectors, code * scale in 32 bits rounded once, into
+   pools of pages of the same size: for fadkv_paged_prefill (a chunk on top of
+   cached tokens) or an encode.
+     block_table [B][max_pages] int32, lengths [B] int32 (clamped to
+                 [0, max_pages * page_size])
+     first       [B] int32 or null (0): tokens first[b] .. lengths[b] - 1 of
+                 request b are read
+     out_table   [B][max_pages] int32 or null: the output page that takes page
+                 i of request b; null: page b * max_pages + i
+     k_out, v_out  output pools, 16-byte aligned
+   Tokens on pages outside [0, num_pages), or for output pages outside
+   [0, out_pages), are skipped; what is not read back is left as it is.
+   Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+fadkv_status fadkv_paged8_read(const fadkv_read8_params* params, const void* k_pages, const void* v_pages,
+                               const float* k_scales, const float* v_scales, const int32_t* block_table,
+                               const int32_t* lengths, const int32_t* first, const int32_t* out_table,
+                               void* k_out, void* v_out, void* stream);
+
+typedef struct {
+    int32_t B;            /* requests and query rows, 0 .. FADKV_MAX_REQUESTS */
+    int32_t Hq;           /* query heads (a multiple of Hkv); head h reads KV head h / (Hq / Hkv) */
+    int32_t Hkv;
+    int32_t d;            /* head dimension: 64 or 128 */
+    int32_t dtype;        /* of q and out: FADKV_F16 or FADKV_BF16 */
+    int32_t format;       /* FADKV_E4M3 or FADKV_I8 */
+    int32_t page_size, num_pages, max_pages, block;
+    int32_t window;       /* a query sees its last `window` tokens, itself among them; 0: all */
+    int32_t sinks;        /* first tokens that stay visible beside the window */
+    float scale;          /* score scale, 1/sqrt(d) for standard attention */
+    int64_t q_stride, out_stride;   /* elements from one row of q (out) to the next; heads back to back */
+    int64_t page_stride, head_stride, token_stride;   /* of the pools, bytes */
+} fadkv_paged8_params;
+
+/* fadkv_paged_attend over 8-bit pages: one new token per request, row b is
+   request b's.  Which tokens are seen, empty rows, lse, positions (as in
+   fadkv_paged_attend_planned, or null) and the workspace's rules are the same,
+   and one workspace (of the largest size) may serve these calls in turn.
+   Scores, softmax and sums in 32 bits; bfloat16 queries enter the product with
+   the codes as binary16 values, scaled by a power of two for each head (exact
+   but for elements below 2^-28 of the head's largest); the probabilities,
+   times the scales of the values, enter the product with the codes as two
+   binary16 terms (22 bits; one below 2^-36 of the largest is lost).  A seen
+   code that is NaN, or a scale that is not finite, makes what it enters NaN;
+   what is not seen is never used.
+   Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+fadkv_status fadkv_paged8_attend(const fadkv_paged8_params* params, const void* k_pages, const void* v_pages,
+                                 const float* k_scales, const float* v_scales, const int32_t* block_table,
+                                 const int32_t* lengths, const int32_t* positions, const void* q, void* out,
+                                 float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Device workspace fadkv_paged8_attend needs (host-only; writes *bytes).
+   Errors: INVALID_ARG, UNSUPPORTED. */
+fadkv_status fadkv_paged8_attend_workspace_bytes(const fadkv_paged8_params* params, size_t* bytes);
+
+typedef struct {
+    int32_t B;            /* prompts, 0 .. FADKV_MAX_REQUESTS */
+    int32_t T;            /* rows of all prompts */
+    int32_t Hq;           /* query heads (a multiple of Hkv); head h reads KV head h / (Hq / Hkv) */
+    int32_t Hkv;
+    int32_t d;            /* head dimension: 64 or 128 */
+    int32_t dtype;        /* of q, k, v and out: FADKV_F16 or FADKV_BF16 */
+    int32_t window, sinks;   /* as in fadkv_paged_params */
+    float scale;
+    int64_t q_stride, k_stride, v_stride, out_stride;   /* elements from one row to the next, multiples of 8; heads back to back */
+} fadkv_prompt_params;
+
+/* Causal attention of packed prompts over their own keys and values, with no
+   pages: for prompts that begin at their first token, from the full vectors,
+   whatever the cache then keeps of them (8 bits, codes).  Rows starts[b] ..
+   starts[b+1]-1 of q, k and v are the tokens of prompt b, row i of it at
+   position i.
+     starts      [B+1] int32 as fadkv_page_plan writes them: 0, ascending; rows
+                 at and past T are left out.  Rows past starts[B] are not read
+                 and their out and lse not written.
+     positions   [T] int32 as fadkv_page_plan writes them, or null: a prompt
+                 whose first row has a negative position was refused and sees
+                 nothing (out = 0, lse = -inf)
+     q, k, v, out  16-byte aligned; lse [T][Hq] float32, or null
+   Numerics, the workspace and its status word (fadkv_paged_status) are those
+   of fadkv_paged_prefill; out and lse do not overlap the inputs.
+   Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+fadkv_status fadkv_prompt_attend(const fadkv_prompt_params* params, const void* q, const void* k, const void* v,
+                                 const int32_t* starts, const int32_t* positions, void* out, float* lse,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* Device workspace fadkv_prompt_attend needs (host-only; writes *bytes).
+   Errors: INVALID_ARG, UNSUPPORTED. */
+fadkv_status fadkv_prompt_attend_workspace_bytes(const fadkv_prompt_params* params, size_t* bytes);
 
 /* Kernel classes reported by fadkv_profile_read. */
 #define FADKV_PROFILE_KERNELS 8
