@@ -21,7 +21,8 @@ namespace {
 using namespace paged8;
 
 constexpr int kThreads = 128;
-constexpr int kHeld = 8;         // steps of rows kept in registers
+// Steps of rows kept in registers: 32 registers a lane, whatever the type.
+template <typename T> constexpr int kHeld = 16 / (int)sizeof(T);
 
 // Eight consecutive elements as loaded; their largest |x| as the type's bits.
 template <typename T> struct Raw8 {
@@ -77,20 +78,20 @@ template <typename T, int D, int FORMAT>
 __device__ __forceinline__ void quantise(const Append8Args& a, const T* x, long long stride, const Place& to, int row0, int n,
                                          int first, int lane)
 {
-    constexpr int LPR = D / 8, RPW = 32 / LPR, ROWS = kHeld * RPW;   // lanes a row, rows a step, rows kept
+    constexpr int LPR = D / 8, RPW = 32 / LPR, HELD = kHeld<T>, ROWS = HELD * RPW;   // lanes a row, rows a step, rows kept
     const int sub = lane / LPR, l = lane % LPR, mask = (1 << a.bshift) - 1;
     float old = first > 0 && lane == 0 ? *to.scale : 0.f;
-    Raw8<T> raw[kHeld];
+    Raw8<T> raw[HELD];
     auto load = [&](int i0) {
 #pragma unroll
-        for (int u = 0; u < kHeld; ++u)
+        for (int u = 0; u < HELD; ++u)
             if (i0 + u * RPW < n) raw[u].load(x + min(row0 + i0 + u * RPW + sub, row0 + n - 1) * stride + l * 8);
     };
     uint32_t top = 0;
     for (int i0 = 0; i0 < n; i0 += ROWS) {
         load(i0);
 #pragma unroll
-        for (int u = 0; u < kHeld; ++u)
+        for (int u = 0; u < HELD; ++u)
             if (i0 + u * RPW < n) top = max(top, raw[u].most());
     }
     top = __reduce_max_sync(0xffffffffu, top);
@@ -113,10 +114,13 @@ __device__ __forceinline__ void quantise(const Append8Args& a, const T* x, long 
     }
     const float t = __uint_as_float((uint32_t)max(Code<FORMAT>::exponent(top), 1) << 23);
     old = __shfl_sync(0xffffffffu, old, 0);
-    const float s = first > 0 ? fmaxf(old, t) : t, inv = 1.f / s;
+    const float s = first > 0 ? fmaxf(old, t) : t;
+    // 1 / s of a power of two by its exponent (a division there would keep its registers through the loads)
+    const uint32_t bits = __float_as_uint(s);
+    const float inv = (bits & 0x7fffffu) == 0u && bits < (254u << 23) ? __uint_as_float((254u << 23) - bits) : 1.f / s;
     if (lane == 0) *to.scale = s;
     if (first > 0 && s > old) {
-        const float ratio = old / s;
+        const float ratio = old * inv;                 // s is t here
 #pragma unroll 4
         for (int i = sub; i < first; i += RPW) {
             uint2* at = reinterpret_cast<uint2*>(to.block + i * a.p.token_stride + l * 8);
@@ -132,7 +136,7 @@ __device__ __forceinline__ void quantise(const Append8Args& a, const T* x, long 
     for (int i0 = 0; i0 < n; i0 += ROWS) {
         if (n > ROWS) load(i0);
 #pragma unroll
-        for (int u = 0; u < kHeld; ++u) {
+        for (int u = 0; u < HELD; ++u) {
             const int i = i0 + u * RPW + sub;
             if (i >= n) continue;
             float y[8];
@@ -149,7 +153,7 @@ __device__ __forceinline__ void quantise(const Append8Args& a, const T* x, long 
 // A warp takes `each` rows (at most 16) of one head's keys or values: the runs
 // that begin there.
 template <int D, int FORMAT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 6)
 paged8_append_kernel(const __grid_constant__ Append8Args a, int each)
 {
     pdl_begin();

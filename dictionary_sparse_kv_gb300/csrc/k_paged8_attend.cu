@@ -40,27 +40,36 @@ constexpr int kTile = 16;                          // tokens per warp step
 constexpr int kBlock = kTile * kWarps;             // tokens per unit of work
 constexpr int kMaxHeads = 16;                      // query heads per piece; larger groups are several pieces
 constexpr float kGrow = 4.f;                       // growth (log2) that moves m and M
-constexpr float kUp = 2048.f;                      // 2^(15 - kGrow): what w is multiplied by for the product
+constexpr float kUp = 11.f;                        // 15 - kGrow: w is multiplied by 2^kUp for the product
+constexpr int kExtra = 3;                          // units that a piece costs beside its blocks
 constexpr int kSms = 152;
 
-template <int D> struct Cfg {
+// ONE: every CTA takes one piece, and joins where its tiles were.
+template <int D, bool ONE> struct Cfg {
     static constexpr int PER_SM = D == 128 ? 3 : 4;
-    static constexpr int STAGES = D == 128 ? 3 : 4;
+    static constexpr int STAGES = D == 128 ? (ONE ? 4 : 3) : (ONE ? 6 : 4);
     static constexpr int CTAS = PER_SM * kSms;
     static constexpr int TILE_BYTES = kTile * D;
     static constexpr int WARP_BYTES = STAGES * 2 * TILE_BYTES;
-    static constexpr int JOIN_BYTES = kWarps * 3 * (D / 16 / kWarps) * 32 * 16;
-    static constexpr int SMEM = kWarps * WARP_BYTES + JOIN_BYTES;
+    static constexpr int ROW = D + 8;                                  // floats of a result: d values, m, l; padding
+    static constexpr int JOIN_BYTES = D == 128 ? 24576 : 16384;        // results that are joined
+    static constexpr int SMEM = kWarps * WARP_BYTES + (ONE ? 0 : JOIN_BYTES);
+    static_assert(kWarps * WARP_BYTES >= JOIN_BYTES, "join");
 };
+template <int D> constexpr int kCtas = Cfg<D, true>::CTAS;
+static_assert(kCtas<64> == Cfg<64, false>::CTAS && kCtas<128> == Cfg<128, false>::CTAS, "grid");
 
 // Pieces that one CTA joins: more are joined in groups, as in the 16-bit kernel.
 constexpr int kAtOnce = 32, kGroup = 16;
 constexpr int kCounters = 1024;
-static_assert(Cfg<64>::CTAS <= kCounters && Cfg<128>::CTAS <= kCounters, "counters");
+static_assert(kCtas<64> <= kCounters && kCtas<128> <= kCounters, "counters");
 static_assert(3 * kCounters * sizeof(int) <= kHeadBytes - kDecodeHead, "workspace head");
 
-// A piece in the workspace: kMaxHeads rows of d results, then their m and l.
-__host__ __device__ constexpr size_t piece_floats(int d) { return (size_t)kMaxHeads * (d + 2); }
+template <int D> constexpr bool kJoins = Cfg<D, true>::JOIN_BYTES >= (kAtOnce > 8 * kWarps ? kAtOnce : 8 * kWarps) * Cfg<D, true>::ROW * 4;
+static_assert(kJoins<64> && kJoins<128>, "join");
+
+// A piece in the workspace: a row for each of its heads.
+__host__ __device__ constexpr size_t piece_floats(int d) { return (size_t)kMaxHeads * (d + 8); }
 
 // Byte offset of 16-byte chunk c of row r: eight rows at one chunk lie in
 // eight different bank groups.
@@ -70,10 +79,7 @@ __device__ __forceinline__ uint32_t swz8(int r, int c)
     return D == 128 ? (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
+__device__ __forceinline__ void prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 __device__ __forceinline__ int add_acq_rel(int* p, int v)
 {
@@ -103,26 +109,28 @@ struct Work {
     Blocks seen;
 };
 
-template <typename T, int D, int NT, int FORMAT>
-__global__ void __launch_bounds__(kThreads, Cfg<D>::PER_SM)
+template <typename T, int D, int NT, int FORMAT, bool ONE>
+__global__ void __launch_bounds__(kThreads, Cfg<D, ONE>::PER_SM)
 paged8_attend_kernel(const __grid_constant__ Paged8Args a)
 {
-    using C_ = Cfg<D>;
+    using C_ = Cfg<D, ONE>;
     constexpr int STAGES = C_::STAGES, CPR = D / 16;                   // 16-byte chunks per row
-    constexpr int KS = D / 16, KQ = KS / kWarps;                       // 16-element steps; those a warp writes out
+    constexpr int KS = D / 16, ROW = C_::ROW;                          // 16-element steps; floats of a result
     extern __shared__ __align__(1024) unsigned char smem[];
-    __shared__ int s_b, s_last, s_longest;
-    __shared__ long long s_base;
-    __shared__ float s_m[kWarps][8 * NT], s_l[kWarps][8 * NT];
-    __shared__ uint32_t s_ok[kWarps][STAGES];
-    __shared__ float s_scale[kWarps][STAGES][2];
+    __shared__ int s_b, s_last, s_sum[2][kWarps];
+    __shared__ long long s_unit;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int grp = a.grp, B = a.p.B;
+    const int grp = a.grp, B = a.p.B, grid = (int)gridDim.x;
     const int chunks = (grp + 8 * NT - 1) / (8 * NT);                 // pieces per KV head
-    const int segs = a.p.Hkv * chunks;
-    const uint32_t wbase = saddr(smem + warp * C_::WARP_BYTES);
-    float4* joinbuf = reinterpret_cast<float4*>(smem + kWarps * C_::WARP_BYTES);
+    const int segs = a.p.Hkv * chunks, sets = B * segs;
+    unsigned char* wsmem = smem + warp * C_::WARP_BYTES;
+    const uint32_t wbase = saddr(wsmem);
+    float* rows = reinterpret_cast<float*>(smem + (ONE ? 0 : kWarps * C_::WARP_BYTES));
+    // Lengths and tables on their way to L2 while the kernel before this one ends (a hint: they are read after it).
+    if (tid * 32 < B && blockIdx.x == 0) prefetch(a.lengths + tid * 32);
+    if (const unsigned line = blockIdx.x * kThreads + tid; line * 32ull < (unsigned long long)B * a.p.max_pages)
+        prefetch(a.table + (size_t)line * 32);
     pdl_begin();
 
     auto blocks_of = [&](int b) {
@@ -138,98 +146,158 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
     };
     // at least one, so that a request which sees nothing is written too
     auto units_of = [&](int b) { return max(1, blocks_of(b).count); };
-    long long u, u1, U, base;                                          // this CTA's units; all; the first of request cur_b
-    int C, cur_b = 0, longest, parts = 0;                              // parts > 0: (request, heads) in so many equal parts
-    auto share = [&] {
-        const int pieces = B * segs, grid = (int)gridDim.x;
-        C = (int)min((long long)grid, U);
-        if (pieces <= grid && 8 * U >= 7ll * pieces * longest) {
-            parts = min(longest, grid / pieces);
-            if (5 * pieces * parts >= 3 * C) C = pieces * parts;
-            else parts = 0;
+
+    // How the work is cut.  Where the (request, heads) are no more than the CTAs, every CTA takes one piece: as many for
+    // each as keep its pieces at `most` blocks or fewer, the least that the grid has room for.  Where they are more, the
+    // list is cut into even shares, each (request, heads) kExtra units longer than its blocks, which is what a piece costs.
+    int cur_b, parts = 1, part = 0, seg = 0;                           // one: this CTA's piece
+    long long u = 0, u1 = 1, U = 0, base = 0;                          // shares: this CTA's units; all; the first of request cur_b
+    // Each thread has the requests b0 .. b1-1: a lane each, the same in every warp, for up to 32; else over the block.
+    const bool few = B <= 32;
+    const int each = few ? 1 : (B + kThreads - 1) / kThreads, b0 = min(B, (few ? lane : tid) * each), b1 = min(B, b0 + each);
+    auto total = [&](int v, int slot) {                                // over the requests; the slots in turn
+        v = __reduce_add_sync(0xffffffffu, v);
+        if (!few) {
+            if (lane == 0) s_sum[slot][warp] = v;
+            __syncthreads();
+            v = 0;
+#pragma unroll
+            for (int x = 0; x < kWarps; ++x) v += s_sum[slot][x];
         }
-        if (U < (1 << 21)) {                                          // C <= 1024: the products fit 32 bits
-            u = (int)U * (int)blockIdx.x / C;
-            u1 = (int)U * (int)(blockIdx.x + 1) / C;
-        } else {
-            u = U * blockIdx.x / C;
-            u1 = U * (blockIdx.x + 1) / C;
-        }
+        return v;
     };
-    if (B <= 32) {                                                    // a lane a request, each warp for itself
-        const int nb = lane < B ? units_of(lane) : 0;
-        const long long mine = (long long)nb * segs;
-        long long upto = mine;
-        longest = __reduce_max_sync(0xffffffffu, nb);
+    if (ONE) {
+        constexpr int kEach = (kCtas<D> + kThreads - 1) / kThreads;   // there are no more requests than CTAs
+        int nb[kEach], sum = 0, longest = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            nb[i] = b0 + i < b1 ? units_of(b0 + i) : 0;
+            sum += nb[i];
+            longest = max(longest, nb[i]);
+        }
+        const unsigned all = (unsigned)total(sum, 0) * (unsigned)segs;
+        auto pieces = [&](int x) {                                     // of at most x blocks
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i)
+                if (i < each) n += (int)((unsigned)(nb[i] + x - 1) / (unsigned)x);
+            return n;
+        };
+        // (all / x + sets of them are too many: this x is large enough)
+        int lo = (int)((all + grid - 1) / grid), hi = 0x7fffffff;
+        if (sets < grid) {
+            hi = (int)(all / (unsigned)(grid - sets)) + 1;
+        } else {
+            hi = few ? __reduce_max_sync(0xffffffffu, longest) : (int)all;
+        }
+        int slot = 1;
+        while (lo < hi) {
+            const int mid = lo + (hi - lo) / 2;
+            if (total(pieces(mid), slot) * segs <= grid) hi = mid;
+            else lo = mid + 1;
+            slot ^= 1;
+        }
+        const int mine = pieces(hi) * segs;
+        int upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+            const int y = __shfl_up_sync(0xffffffffu, upto, o);
             if (lane >= o) upto += y;
         }
-        U = __shfl_sync(0xffffffffu, upto, 31);
-        share();
-        if ((int)blockIdx.x >= C) return;
-        if (parts == 0) {
-            cur_b = __ffs(__ballot_sync(0xffffffffu, upto > u)) - 1;
-            base = __shfl_sync(0xffffffffu, upto - mine, cur_b);
+        int end = __shfl_sync(0xffffffffu, upto, 31);
+        if (!few) {
+            if (lane == 31) s_sum[slot][warp] = upto;
+            __syncthreads();
+            end = 0;
+#pragma unroll
+            for (int x = 0; x < kWarps; ++x) {
+                if (x < warp) upto += s_sum[slot][x];
+                end += s_sum[slot][x];
+            }
         }
-    } else {
-        const int each = (B + kThreads - 1) / kThreads, b0 = min(B, tid * each), b1 = min(B, b0 + each);
-        long long mine = 0;
-        int most = 0;
-        if (tid == 0) s_longest = 0;
-        for (int b = b0; b < b1; ++b) {
-            const int nb = units_of(b);
-            mine += (long long)nb * segs;
-            most = max(most, nb);
-        }
-        long long at = block_scan<kThreads>(mine, &U);
-        most = __reduce_max_sync(0xffffffffu, most);
-        if (lane == 0) atomicMax(&s_longest, most);
-        __syncthreads();
-        longest = s_longest;
-        share();
-        if ((int)blockIdx.x >= C) return;
-        if (parts == 0 && u >= at && u < at + mine) {
-            int b = b0;
-            for (long long n; u >= at + (n = (long long)units_of(b) * segs); ++b) at += n;
-            s_b = b;
-            s_base = at;
-        }
-        __syncthreads();
-        if (parts == 0) {
+        if ((int)blockIdx.x >= end) return;
+        int from = upto - mine;
+        if (few) {
+            cur_b = __ffs(__ballot_sync(0xffffffffu, upto > (int)blockIdx.x)) - 1;
+            from = __shfl_sync(0xffffffffu, from, cur_b);
+        } else {
+            if ((int)blockIdx.x >= from && (int)blockIdx.x < upto) {
+                int b = b0;
+                for (int n; (int)blockIdx.x >= from + (n = (units_of(b) + hi - 1) / hi * segs); ++b) from += n;
+                s_b = b;
+                s_unit = from;
+            }
+            __syncthreads();
             cur_b = s_b;
-            base = s_base;
+            from = (int)s_unit;
+        }
+        parts = (units_of(cur_b) + hi - 1) / hi;
+        const int rel = (int)blockIdx.x - from;
+        seg = rel / parts;
+        part = rel - seg * parts;
+    } else {
+        auto units = [&](int b) { return (long long)(units_of(b) + kExtra) * segs; };
+        long long mine = 0;
+        for (int b = b0; b < b1; ++b) mine += units(b);
+        long long from;
+        if (few) {
+            long long upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += y;
+            }
+            U = __shfl_sync(0xffffffffu, upto, 31);
+            from = upto - mine;
+        } else {
+            from = block_scan<kThreads>(mine, &U);
+        }
+        u = U * blockIdx.x / grid;
+        u1 = U * (blockIdx.x + 1) / grid;
+        if (few) {
+            cur_b = __ffs(__ballot_sync(0xffffffffu, from + mine > u)) - 1;
+            base = __shfl_sync(0xffffffffu, from, cur_b);
+        } else {
+            if (u >= from && u < from + mine) {
+                int b = b0;
+                for (long long n; u >= from + (n = units(b)); ++b) from += n;
+                s_b = b;
+                s_unit = from;
+            }
+            __syncthreads();
+            cur_b = s_b;
+            base = s_unit;
         }
     }
-    if (parts > 0) cur_b = (int)blockIdx.x / parts / segs;
 
-    // the piece that begins at unit u (u < u1); u, cur_b and base move past it
+    // the next piece from unit u on (none: blk0 == blk1); u, cur_b and base move past it
     auto next_work = [&] {
         Work w;
-        w.b = cur_b;
-        w.seen = blocks_of(cur_b);
-        w.nb = max(1, w.seen.count);
-        w.unit0 = 0;
-        int seg;
-        if (parts > 0) {
-            seg = (int)blockIdx.x / parts % segs;
-            const int n = min(parts, w.nb), part = (int)blockIdx.x % parts;   // a short request has fewer parts
-            const int each = w.nb / n, rest = w.nb % n;                      // the first `rest` parts take one block more
-            w.blk0 = part * each + min(part, rest);
-            w.blk1 = part < n ? w.blk0 + each + (part < rest) : w.blk0;
-            u = u1;
-        } else {
+        for (;;) {
+            w.b = cur_b;
+            w.seen = blocks_of(cur_b);
+            w.nb = max(1, w.seen.count);
+            w.unit0 = 0;
+            if (ONE) {
+                const int each = w.nb / parts, rest = w.nb % parts;          // the first `rest` parts take one block more
+                w.blk0 = part * each + min(part, rest);
+                w.blk1 = w.blk0 + each + (part < rest);
+                u = u1;
+                break;
+            }
+            const int len = w.nb + kExtra;
             const long long rel = u - base;
-            seg = rel < 0x7fffffffll ? (int)rel / w.nb : (int)(rel / w.nb);
-            w.unit0 = base + (long long)seg * w.nb;
-            w.blk0 = (int)(u - w.unit0);
-            w.blk1 = (int)min((long long)w.nb, w.blk0 + (u1 - u));
-            u += w.blk1 - w.blk0;
-            if (w.blk1 == w.nb && seg == segs - 1) {
-                base += (long long)w.nb * segs;
+            seg = rel < 0x7fffffffll ? (int)rel / len : (int)(rel / len);
+            w.unit0 = base + (long long)seg * len;
+            const int lo = (int)(u - w.unit0), hi = (int)min((long long)len, lo + (u1 - u));
+            w.blk0 = min(lo, w.nb);
+            w.blk1 = min(hi, w.nb);
+            u += hi - lo;
+            if (hi == len && seg == segs - 1) {
+                base += (long long)len * segs;
                 ++cur_b;
             }
+            if (w.blk0 < w.blk1 || u >= u1) break;                           // (what is left of a share may be past the blocks)
         }
         w.hk = chunks == 1 ? seg : seg / chunks;
         const int h0 = chunks == 1 ? 0 : (seg % chunks) * 8 * NT;
@@ -238,45 +306,56 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
         return w;
     };
 
-    // this warp's 16 tokens of the piece's tile t (block blk0 + t): their page one step ahead of their load
-    int tok = 0, page = -1;
-    auto look_up = [&](const Work& w, int t) {
-        page = -1;
-        if (w.blk0 + t >= w.blk1) return;
-        tok = w.seen.token(w.blk0 + t) + warp * kTile;
-        if (w.seen.seen(tok)) page = __ldg(a.table + (size_t)w.b * a.p.max_pages + (tok >> a.shift));
+    // The piece's tiles of this warp (16 tokens of each block), 32 at a time, a lane each: page, tokens that are seen (none on
+    // a page that is none), scale of the keys, log2 of the values'.
+    struct Info { int page; uint32_t seen; float ks, ls; };
+    Info cur, nxt;
+    auto token_of = [&](const Work& w, int t) { return w.seen.token(w.blk0 + t) + warp * kTile; };
+    auto pages = [&](const Work& w, int t, Info& f) {
+        f.page = -1;
+        f.seen = 0u;
+        if (w.blk0 + t + lane < w.blk1) {
+            const int tok = token_of(w, t + lane);
+            f.seen = w.seen.seen(tok);
+            if (f.seen) f.page = __ldg(a.table + (size_t)w.b * a.p.max_pages + (tok >> a.shift));
+        }
+    };
+    auto scales = [&](const Work& w, int t, Info& f) {
+        f.ks = f.ls = 0.f;
+        if (f.page >= 0 && f.page < a.p.num_pages) {
+            const size_t at = scale_at(f.page, w.hk, token_of(w, t + lane) & ((1 << a.shift) - 1), a.p.Hkv, a.shift, a.bshift);
+            f.ks = __ldg(a.k_scales + at);
+            f.ls = __log2f(__ldg(a.v_scales + at));
+        } else {
+            f.seen = 0u;
+        }
     };
     const int row0 = lane / CPR, chunk = lane % CPR;                   // this lane's pieces of a tile: rows row0 + j 32 / CPR
     const long long lane_off = row0 * a.p.token_stride + chunk * 16, step_off = (32 / CPR) * a.p.token_stride;
-    auto load = [&](const Work& w, int t) {
-        const int s = t % STAGES;
-        const bool ok = page >= 0 && page < a.p.num_pages;
-        const uint32_t bits = ok ? w.seen.seen(tok) : 0u;
-        const int at = tok & ((1 << a.shift) - 1);
-        const long long off = ok ? page * a.p.page_stride + w.hk * a.p.head_stride + at * a.p.token_stride + lane_off : 0;
-        const uint32_t dst = wbase + s * 2 * C_::TILE_BYTES;
+    // tile t, whose Info is in f
+    auto load = [&](const Work& w, int t, const Info& f) {
+        const int page = __shfl_sync(0xffffffffu, f.page, t & 31);
+        const uint32_t seen = __shfl_sync(0xffffffffu, f.seen, t & 31);
+        if (page < 0 || page >= a.p.num_pages) return;
+        const int at = token_of(w, t) & ((1 << a.shift) - 1);
+        const long long off = page * a.p.page_stride + w.hk * a.p.head_stride + at * a.p.token_stride + lane_off;
+        const uint32_t dst = wbase + (t % STAGES) * 2 * C_::TILE_BYTES;
 #pragma unroll
         for (int j = 0; j < kTile * CPR / 32; ++j) {
             const int r = row0 + j * (32 / CPR);
-            const bool v = (bits >> r) & 1u;
+            const bool v = (seen >> r) & 1u;
             cp16(dst + swz8<D>(r, chunk), a.k + off + j * step_off, v);
             cp16(dst + C_::TILE_BYTES + swz8<D>(r, chunk), a.v + off + j * step_off, v);
         }
-        if (lane < 2) {
-            if (lane == 0) s_ok[warp][s] = bits;
-            if (ok) cp4(saddr(&s_scale[warp][s][lane]), (lane ? a.v_scales : a.k_scales) + scale_at(page, w.hk, at, a.p.Hkv, a.shift, a.bshift));
-            else s_scale[warp][s][lane] = 1.f;
-        }
     };
     auto begin = [&](const Work& w) {                                   // the first tiles, STAGES - 1 copy groups
-        look_up(w, 0);
+        pages(w, 0, cur);
         for (int t = 0; t < STAGES - 1; ++t) {
-            if (w.blk0 + t < w.blk1) {
-                load(w, t);
-                look_up(w, t + 1);
-            }
+            if (w.blk0 + t < w.blk1) load(w, t, cur);
             cp_commit();
         }
+        scales(w, 0, cur);
+        pages(w, 32, nxt);
     };
     // Queries as the B operand: lane holds head lane / 4; of step k its elements 16 k + 4 (lane % 4) + {0, 1, 2, 3}, the
     // order in which the lanes have a row's bytes.  qs: what the scores of heads 2 (lane % 4) + {0, 1} are multiplied by.
@@ -319,52 +398,54 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
     };
 
     Work w = next_work();
-    if (w.blk0 == w.blk1) return;                                       // a part that a short request does not have
+    if (w.blk0 == w.blk1) return;                                       // a share without a block
     begin(w);
     load_q(w);
     for (;;) {
-        float o[NT][KS][4], m[NT][2], M[NT][2], l[NT][2];
+        // references mr and Mr of the exponents (0 before the first token) and what has to be passed to move them
+        float o[NT][KS][4], mr[NT][2], Mr[NT][2], mg[NT][2], Mg[NT][2], l[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            m[n][0] = m[n][1] = M[n][0] = M[n][1] = -INFINITY;
+            mr[n][0] = mr[n][1] = Mr[n][0] = Mr[n][1] = 0.f;
+            mg[n][0] = mg[n][1] = Mg[n][0] = Mg[n][1] = -INFINITY;
             l[n][0] = l[n][1] = 0.f;
 #pragma unroll
             for (int k = 0; k < KS; ++k) o[n][k][0] = o[n][k][1] = o[n][k][2] = o[n][k][3] = 0.f;
         }
         const int tiles = w.blk1 - w.blk0;
         for (int t = 0; t < tiles; ++t) {
+            if ((t & 31) == 0 && t > 0) {
+                cur = nxt;
+                pages(w, t + 32, nxt);
+            }
+            if ((t & 31) == 16) scales(w, (t & ~31) + 32, nxt);
             cp_wait<STAGES - 2>();
             __syncwarp();
-            if (t + STAGES - 1 < tiles) {
-                load(w, t + STAGES - 1);
-                look_up(w, t + STAGES);
-            }
+            const int ahead = t + STAGES - 1;
+            if (ahead < tiles) load(w, ahead, (ahead ^ t) < 32 ? cur : nxt);
             cp_commit();
-            const int s = t % STAGES;
-            const uint32_t kt = wbase + s * 2 * C_::TILE_BYTES, vt = kt + C_::TILE_BYTES;
-            const uint32_t oks = s_ok[warp][s];
+            const uint32_t oks = __shfl_sync(0xffffffffu, cur.seen, t & 31);
             if (oks == 0u) continue;
-            const float ks = s_scale[warp][s][0], ls = __log2f(s_scale[warp][s][1]);
+            const float ks = __shfl_sync(0xffffffffu, cur.ks, t & 31), ls = __shfl_sync(0xffffffffu, cur.ls, t & 31);
+            const uint32_t kt = wbase + (t % STAGES) * 2 * C_::TILE_BYTES, vt = kt + C_::TILE_BYTES;
 
             float sc[NT][4], sc2[NT][4];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sc[n][i] = sc2[n][i] = 0.f;
-            {
-                const int r = (lane & 7) + ((lane >> 3) & 1) * 8, c = lane >> 4;
+            const int r = (lane & 7) + ((lane >> 3) & 1) * 8, c = lane >> 4;
 #pragma unroll
-                for (int k = 0; k < KS; k += 2) {
-                    uint32_t b[4];
-                    ldsm_x4(b, kt + swz8<D>(r, k + c));
+            for (int k = 0; k < KS; k += 2) {
+                uint32_t b[4];
+                ldsm_x4(b, kt + swz8<D>(r, k + c));
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t f[4];
-                        Code<FORMAT>::halves(b[2 * i], f[0], f[2]);
-                        Code<FORMAT>::halves(b[2 * i + 1], f[1], f[3]);
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t f[4];
+                    Code<FORMAT>::halves(b[2 * i], f[0], f[2]);
+                    Code<FORMAT>::halves(b[2 * i + 1], f[1], f[3]);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) Num<__half>::mma(i ? sc2[n] : sc[n], f, qf[n][k + i][0], qf[n][k + i][1]);
-                    }
+                    for (int n = 0; n < NT; ++n) Num<__half>::mma(i ? sc2[n] : sc[n], f, qf[n][k + i][0], qf[n][k + i][1]);
                 }
             }
             bool grew = false;
@@ -381,7 +462,7 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const float v = fmaxf(sc[n][i], sc[n][i + 2]);
-                    grew |= v > m[n][i] + kGrow || v + ls > M[n][i] + kGrow;
+                    grew |= v > fminf(mg[n][i], Mg[n][i] - ls);
                 }
             }
             if (__any_sync(0xffffffffu, grew)) {
@@ -394,14 +475,19 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                        if (v > m[n][i]) {
-                            l[n][i] *= exp2_fast(m[n][i] - v);
-                            m[n][i] = v;
+                        // (the first time there is nothing to rescale)
+                        const bool first = mg[n][i] == -INFINITY, First = Mg[n][i] == -INFINITY;
+                        if (first ? v > mg[n][i] : v > mr[n][i]) {
+                            l[n][i] *= first ? 0.f : exp2_fast(mr[n][i] - v);
+                            mr[n][i] = v;
+                            mg[n][i] = v + kGrow;
                         }
                         f[i] = 1.f;
-                        if (v + ls > M[n][i]) {
-                            f[i] = exp2_fast(M[n][i] - (v + ls));
-                            M[n][i] = v + ls;
+                        v += ls;
+                        if (First ? v > Mg[n][i] : v > Mr[n][i]) {
+                            f[i] = First ? 0.f : exp2_fast(Mr[n][i] - v);
+                            Mr[n][i] = v;
+                            Mg[n][i] = v + kGrow;
                         }
                     }
 #pragma unroll
@@ -416,13 +502,12 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
             uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
+                const float up[2] = {ls - Mr[n][0] + kUp, ls - Mr[n][1] + kUp};
                 float e[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    // a head that has seen nothing yet: every score is -inf and every p is 0
-                    const float mi = m[n][i & 1] == -INFINITY ? 0.f : m[n][i & 1], Mi = M[n][i & 1] == -INFINITY ? 0.f : M[n][i & 1];
-                    l[n][i & 1] += exp2_fast(sc[n][i] - mi);
-                    e[i] = exp2_fast(sc[n][i] + ls - Mi) * kUp;
+                    l[n][i & 1] += exp2_fast(sc[n][i] - mr[n][i & 1]);
+                    e[i] = exp2_fast(sc[n][i] + up[i & 1]);
                 }
                 const uint32_t a0 = Num<__half>::pack(e[0], e[1]), a1 = Num<__half>::pack(e[2], e[3]);
                 const float2 r0 = Num<__half>::unpack(a0), r1 = Num<__half>::unpack(a1);
@@ -431,149 +516,110 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
                 pl[n][0] = transpose8(Num<__half>::pack(e[0] - r0.x, e[1] - r0.y));
                 pl[n][1] = transpose8(Num<__half>::pack(e[2] - r1.x, e[3] - r1.y));
             }
-            {
-                const int r = (lane & 7) + ((lane >> 3) & 1) * 8, c = lane >> 4;
 #pragma unroll
-                for (int k = 0; k < KS; k += 2) {
-                    uint32_t b[4];
-                    ldsm_x4_trans(b, vt + swz8<D>(r, k + c));
+            for (int k = 0; k < KS; k += 2) {
+                uint32_t b[4];
+                ldsm_x4_trans(b, vt + swz8<D>(r, k + c));
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        uint32_t f[4];
-                        Code<FORMAT>::crossed(b[2 * i], f[0], f[1]);
-                        Code<FORMAT>::crossed(b[2 * i + 1], f[2], f[3]);
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t f[4];
+                    Code<FORMAT>::crossed(b[2 * i], f[0], f[1]);
+                    Code<FORMAT>::crossed(b[2 * i + 1], f[2], f[3]);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            Num<__half>::mma(o[n][k + i], f, ph[n][0], ph[n][1]);
-                            Num<__half>::mma(o[n][k + i], f, pl[n][0], pl[n][1]);
-                        }
+                    for (int n = 0; n < NT; ++n) {
+                        Num<__half>::mma(o[n][k + i], f, ph[n][0], ph[n][1]);
+                        Num<__half>::mma(o[n][k + i], f, pl[n][0], pl[n][1]);
                     }
                 }
             }
         }
         __syncwarp();
+        if (ONE) {                                                      // the joins' rows lie over every warp's tiles
+            cp_wait<0>();
+            __syncthreads();
+        }
         const Work done = w;
-        const bool more = u < u1;
+        bool more = !ONE && u < u1;
         if (more) {                                                     // every buffer of this warp is free
             w = next_work();
-            begin(w);
-            load_q(w);
+            more = w.blk0 < w.blk1;
+            if (more) {
+                begin(w);
+                load_q(w);
+            }
         }
 
-        // this piece's results: each warp's divided by its l, and joined quarter by quarter of d, each by one warp.
-        // o[n][k] holds heads n 8 + 2 (lane % 4) + {0, 1} of elements k 16 + 2 (lane / 4) (first two) and the one after it.
+        // Results are rows of d values, m and l, the values divided by l.  Joins n rows of each of the heads h0 .. h0 + heads - 1
+        // of the piece, row (j, h) at rows + (j each + h) ROW, four columns a thread: as the result, or into a piece.
+        auto combine = [&](int n, int each, int heads, int h0, bool result, float* piece) {
+            constexpr int TPR = D / 4;                  // threads per row
+            const int c = tid % TPR * 4, step = each * ROW;
+#pragma unroll 1
+            for (int h = tid / TPR; h < heads; h += kThreads / TPR) {
+                const float* r = rows + h * ROW;
+                float top = -INFINITY, lh = 0.f;
+                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                for (int j = 0; j < n; ++j) top = fmaxf(top, r[j * step + D]);
+                const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll 4
+                for (int j = 0; j < n; ++j) {
+                    const float f = exp2_fast(r[j * step + D] - ref) * r[j * step + D + 1];
+                    const float4 v = *reinterpret_cast<const float4*>(r + j * step + c);
+                    lh += f;
+                    y.x = fmaf(f, v.x, y.x);
+                    y.y = fmaf(f, v.y, y.y);
+                    y.z = fmaf(f, v.z, y.z);
+                    y.w = fmaf(f, v.w, y.w);
+                }
+                const float inv = lh == 0.f ? 0.f : __fdividef(1.f, lh);
+                y.x *= inv, y.y *= inv, y.z *= inv, y.w *= inv;
+                if (result) {
+                    const size_t row = (size_t)done.b * a.p.Hq + done.head0 + h0 + h;
+                    T* out = (T*)a.out + (size_t)done.b * a.p.out_stride + (size_t)(done.head0 + h0 + h) * D + c;
+                    *reinterpret_cast<uint2*>(out) = make_uint2(Num<T>::pack(y.x, y.y), Num<T>::pack(y.z, y.w));
+                    if (c == 0 && a.lse) a.lse[row] = lh == 0.f ? -INFINITY : (top + __log2f(lh)) * kLn2;
+                } else {
+                    float* q = piece + (size_t)(h0 + h) * ROW;
+                    *reinterpret_cast<float4*>(q + c) = y;
+                    if (c == 0) *reinterpret_cast<float2*>(q + D) = make_float2(top, lh);
+                }
+            }
+        };
+        const bool whole = done.blk0 == 0 && done.blk1 == done.nb;
+        float* pieces = reinterpret_cast<float*>((unsigned char*)a.ws + kHeadBytes);
+        constexpr size_t PF = piece_floats(D);
+        float* mine = pieces + (2 * (size_t)blockIdx.x + (done.blk0 == 0 ? 1 : 0)) * PF;
+        // the warps' results, eight heads at a time.  o[n][k] holds heads n 8 + 2 (lane % 4) + {0, 1} of elements
+        // k 16 + 2 (lane / 4) (first two) and the one after it.
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float f[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 float v = l[n][i];
                 v += __shfl_xor_sync(0xffffffffu, v, 4);
                 v += __shfl_xor_sync(0xffffffffu, v, 8);
                 v += __shfl_xor_sync(0xffffffffu, v, 16);
-                if (lane < 4) {
-                    s_m[warp][n * 8 + 2 * lane + i] = m[n][i];
-                    s_l[warp][n * 8 + 2 * lane + i] = v;
-                }
-                // (v is 0 where nothing was seen, and M - m not a number)
-                f[i] = v == 0.f ? 0.f : (M[n][i] == -INFINITY ? 0.f : exp2_fast(M[n][i] - m[n][i])) / (v * kUp);
-            }
+                const float f = v == 0.f ? 0.f : __fdividef(exp2_fast(Mg[n][i] == -INFINITY ? 0.f : Mr[n][i] - mr[n][i] - kUp), v);
+                float* r = rows + (warp * 8 + 2 * (lane & 3) + i) * ROW;       // (f is 0 where nothing was seen)
 #pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                o[n][k][0] *= f[0];
-                o[n][k][1] *= f[1];
-                o[n][k][2] *= f[0];
-                o[n][k][3] *= f[1];
-            }
-        }
-        const bool whole = done.blk0 == 0 && done.blk1 == done.nb;
-        float* pieces = reinterpret_cast<float*>((unsigned char*)a.ws + kHeadBytes);
-        constexpr size_t PF = piece_floats(D);
-        float* mine = pieces + (2 * (size_t)blockIdx.x + (done.blk0 == 0 ? 1 : 0)) * PF;
-        auto lse_of = [&](float mh, float lh) { return lh == 0.f ? -INFINITY : (mh + log2f(lh)) * kLn2; };
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            // slot of warp x's quarter y (y != x): [x][y or y - 1][step][lane]
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-                const int y = k / KQ;
-                if (y != warp)
-                    joinbuf[((warp * 3 + (y < warp ? y : y - 1)) * KQ + k % KQ) * 32 + lane] =
-                        make_float4(o[n][k][0], o[n][k][1], o[n][k][2], o[n][k][3]);
+                for (int k = 0; k < KS; ++k)
+                    *reinterpret_cast<float2*>(r + k * 16 + (lane >> 2) * 2) = make_float2(o[n][k][i] * f, o[n][k][i + 2] * f);
+                if (lane < 4) *reinterpret_cast<float2*>(r + D) = make_float2(mg[n][i] == -INFINITY ? -INFINITY : mr[n][i], v);
             }
             __syncthreads();
-            float f[kWarps][2], mh[2], lh[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int h = n * 8 + 2 * (lane & 3) + i;
-                mh[i] = -INFINITY;
-                lh[i] = 0.f;
-#pragma unroll
-                for (int x = 0; x < kWarps; ++x) mh[i] = fmaxf(mh[i], s_m[x][h]);
-                const float top = mh[i] == -INFINITY ? 0.f : mh[i];
-#pragma unroll
-                for (int x = 0; x < kWarps; ++x) {
-                    f[x][i] = exp2_fast(s_m[x][h] - top) * s_l[x][h];
-                    lh[i] += f[x][i];
-                }
-                const float inv = lh[i] == 0.f ? 0.f : 1.f / lh[i];
-#pragma unroll
-                for (int x = 0; x < kWarps; ++x) f[x][i] *= inv;
-            }
-#pragma unroll
-            for (int k = 0; k < KQ; ++k) {
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                for (int x = 0; x < kWarps; ++x) {
-                    float4 v;
-                    if (x == warp) {
-                        // o[n][warp KQ + k], with constant indexes
-                        v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                        for (int y = 0; y < kWarps; ++y)
-                            if (y == warp) v = make_float4(o[n][y * KQ + k][0], o[n][y * KQ + k][1], o[n][y * KQ + k][2], o[n][y * KQ + k][3]);
-                    } else {
-                        v = joinbuf[((x * 3 + (warp < x ? warp : warp - 1)) * KQ + k) * 32 + lane];
-                    }
-                    acc.x = fmaf(f[x][0], v.x, acc.x);
-                    acc.y = fmaf(f[x][1], v.y, acc.y);
-                    acc.z = fmaf(f[x][0], v.z, acc.z);
-                    acc.w = fmaf(f[x][1], v.w, acc.w);
-                }
-                const int c = (warp * KQ + k) * 16 + (lane >> 2) * 2;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int h = n * 8 + 2 * (lane & 3) + i;
-                    const float y0 = i ? acc.y : acc.x, y1 = i ? acc.w : acc.z;
-                    if (h >= done.hn) continue;
-                    if (whole) {
-                        T* out = (T*)a.out + (size_t)done.b * a.p.out_stride + (size_t)(done.head0 + h) * D + c;
-                        *reinterpret_cast<uint32_t*>(out) = Num<T>::pack(y0, y1);
-                        if (k == 0 && warp == 0 && lane < 4 && a.lse)
-                            a.lse[(size_t)done.b * a.p.Hq + done.head0 + h] = lse_of(mh[i], lh[i]);
-                    } else {
-                        *reinterpret_cast<float2*>(mine + h * D + c) = make_float2(y0, y1);
-                        if (k == 0 && warp == 0 && lane < 4) {
-                            mine[kMaxHeads * D + h] = mh[i];
-                            mine[kMaxHeads * (D + 1) + h] = lh[i];
-                        }
-                    }
-                }
-            }
-            __syncthreads();                            // the buffer, and s_m and s_l, are written again
+            combine(kWarps, 8, min(8, done.hn - n * 8), n * 8, whole, mine);
+            __syncthreads();                            // the rows are written again
         }
         if (!whole) {
-            // the CTAs that have its parts; of shares, unit x is in share ((x + 1) C - 1) / U
+            // the CTAs that have its pieces; of shares, unit x is in share ((x + 1) grid - 1) / U
             int c0, c1;
-            if (parts > 0) {
-                c0 = (int)blockIdx.x / parts * parts;
-                c1 = c0 + min(parts, done.nb) - 1;
-            } else if (U < (1 << 21)) {
-                c0 = (int)(((unsigned int)done.unit0 + 1) * (unsigned int)C - 1) / (int)U;
-                c1 = (int)(((unsigned int)done.unit0 + done.nb) * (unsigned int)C - 1) / (int)U;
+            if (ONE) {
+                c0 = (int)blockIdx.x - part;
+                c1 = c0 + parts - 1;
             } else {
-                c0 = (int)(((done.unit0 + 1) * C - 1) / U);
-                c1 = (int)(((done.unit0 + done.nb) * C - 1) / U);
+                c0 = (int)(((done.unit0 + 1) * grid - 1) / U);
+                c1 = (int)(((done.unit0 + done.nb) * grid - 1) / U);
             }
             // whether this CTA is the last of n at a counter; the counter is back at zero then
             auto last_at = [&](int index, int n) {
@@ -587,59 +633,24 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
                 return s_last != 0;
             };
             auto piece = [&](int x) { return pieces + (2 * (size_t)x + (x == c0 ? 1 : 0)) * PF; };
-            // joins pieces x0, x0 + step, ... (n of them) in their order, so that it does not matter who does it: four columns
-            // a thread, all rows at once; into the first one, or as the result
+            // pieces x0, x0 + step, ... (n of them) in their order, so that it does not matter who joins them; as many heads at a
+            // time as there is room for; into the first one, or as the result
             auto join = [&](int x0, int n, int step, bool result) {
-                constexpr int TPR = D / 4;              // threads per row, all of one warp
-                for (int h = tid / TPR; h < done.hn; h += kThreads / TPR) {
-                    const int c = tid % TPR * 4;
-                    float mh = -INFINITY, lh = 0.f;
-                    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-                    // eight pieces at a time, all their loads in flight; past the last one the last one again, with weight 0
+                constexpr int CPW = ROW / 4;            // 16-byte chunks per row
+                const int group = min(done.hn, C_::JOIN_BYTES / (n * ROW * 4));
 #pragma unroll 1
-                    for (int i0 = 0; i0 < n; i0 += 8) {
-                        float pm[8], ll[8];
-                        float4 v[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float* q = piece(x0 + min(i0 + j, n - 1) * step);
-                            pm[j] = __ldcg(q + kMaxHeads * D + h);
-                            ll[j] = __ldcg(q + kMaxHeads * (D + 1) + h);
-                            v[j] = __ldcg(reinterpret_cast<const float4*>(q + h * D + c));
-                        }
-                        float top = mh;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) top = fmaxf(top, pm[j]);
-                        const float ref = top == -INFINITY ? 0.f : top, g = exp2_fast(mh - ref);
-                        mh = top;
-                        lh *= g;
-                        y.x *= g, y.y *= g, y.z *= g, y.w *= g;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            if (i0 + j >= n) break;
-                            const float f = exp2_fast(pm[j] - ref) * ll[j];
-                            lh += f;
-                            y.x = fmaf(f, v[j].x, y.x);
-                            y.y = fmaf(f, v[j].y, y.y);
-                            y.z = fmaf(f, v[j].z, y.z);
-                            y.w = fmaf(f, v[j].w, y.w);
-                        }
+                for (int h0 = 0; h0 < done.hn; h0 += group) {
+                    const int heads = min(group, done.hn - h0);
+#pragma unroll 1
+                    for (int x = tid; x < n * heads * CPW; x += kThreads) {
+                        const int row = x / CPW, j = row / heads;
+                        cp16(saddr(rows) + x * 16, piece(x0 + j * step) + (h0 + row - j * heads) * ROW + (x - row * CPW) * 4, true);
                     }
-                    const float inv = lh == 0.f ? 0.f : 1.f / lh;
-                    y.x *= inv, y.y *= inv, y.z *= inv, y.w *= inv;
-                    if (result) {
-                        T* out = (T*)a.out + (size_t)done.b * a.p.out_stride + (size_t)(done.head0 + h) * D + c;
-                        *reinterpret_cast<uint2*>(out) = make_uint2(Num<T>::pack(y.x, y.y), Num<T>::pack(y.z, y.w));
-                        if (c == 0 && a.lse) a.lse[(size_t)done.b * a.p.Hq + done.head0 + h] = lse_of(mh, lh);
-                    } else {
-                        float* q = piece(x0);
-                        __syncwarp(__activemask());     // every thread of the row has read its m and l
-                        *reinterpret_cast<float4*>(q + h * D + c) = y;
-                        if (c == 0) {
-                            q[kMaxHeads * D + h] = mh;
-                            q[kMaxHeads * (D + 1) + h] = lh;
-                        }
-                    }
+                    cp_commit();
+                    cp_wait<0>();
+                    __syncthreads();
+                    combine(n, heads, heads, h0, result, piece(x0));
+                    __syncthreads();
                 }
             };
             // (a CTA that begins one (request, heads) may also be within another: their counters lie apart)
@@ -658,25 +669,32 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
                 count = groups;
                 step = size;
             }
-            __syncthreads();                            // s_last is written again
         }
         if (!more) break;
     }
 }
 
+template <typename T, int D, int NT, int FORMAT, bool ONE>
+cudaError_t launch_one(const Paged8Args& a, int grid, cudaStream_t st)
+{
+    auto k = paged8_attend_kernel<T, D, NT, FORMAT, ONE>;
+    const int smem = Cfg<D, ONE>::SMEM;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(k, dim3((unsigned)grid), dim3(kThreads), smem, st, a);
+}
+
 template <typename T, int D, int NT, int FORMAT>
 cudaError_t launch_nt(const Paged8Args& a, cudaStream_t st)
 {
-    auto k = paged8_attend_kernel<T, D, NT, FORMAT>;
-    const int smem = Cfg<D>::SMEM, ctas = Cfg<D>::CTAS;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
     // an upper bound of the units: lengths are known on the device only
     long long most = (long long)a.p.max_pages << a.shift;
     if (a.p.window > 0) most = most < (long long)a.p.window + a.p.sinks ? most : (long long)a.p.window + a.p.sinks;
-    const long long chunks = (a.grp + 8 * NT - 1) / (8 * NT);
-    const long long units = ((most + kBlock - 1) / kBlock + 2) * a.p.B * a.p.Hkv * chunks;
-    return launch_pdl(k, dim3((unsigned)(units < ctas ? units : ctas)), dim3(kThreads), smem, st, a);
+    const long long sets = (long long)a.p.B * a.p.Hkv * ((a.grp + 8 * NT - 1) / (8 * NT)), units = ((most + kBlock - 1) / kBlock + 2) * sets;
+    const int grid = (int)(units < kCtas<D> ? units : kCtas<D>);
+    // (one piece a CTA: sums of units in 32 bits)
+    if (sets <= grid && units < 0x7fffffffll) return launch_one<T, D, NT, FORMAT, true>(a, grid, st);
+    return launch_one<T, D, NT, FORMAT, false>(a, grid, st);
 }
 
 template <typename T, int D>
@@ -690,7 +708,7 @@ cudaError_t launch_t(const Paged8Args& a, cudaStream_t st)
 
 size_t paged8_attend_workspace(const fadkv_paged8_params& p)
 {
-    return kHeadBytes + (size_t)2 * (p.d == 128 ? Cfg<128>::CTAS : Cfg<64>::CTAS) * piece_floats(p.d) * sizeof(float);
+    return kHeadBytes + (size_t)2 * (p.d == 128 ? kCtas<128> : kCtas<64>) * piece_floats(p.d) * sizeof(float);
 }
 
 cudaError_t launch_paged8_attend(const Paged8Args& a, cudaStream_t st)

@@ -15,7 +15,8 @@ using namespace paged8;
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTile = 16;
-constexpr int kCtas = 152 * 8;
+constexpr int kPerSm = 6;
+constexpr int kCtas = 152 * kPerSm;
 
 __device__ __forceinline__ void store8(float* p, const float* y)
 {
@@ -30,7 +31,7 @@ __device__ __forceinline__ void store8(T* p, const float* y)
 }
 
 template <typename T, int D, int FORMAT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kPerSm)
 paged8_read_kernel(const __grid_constant__ Read8Args a)
 {
     constexpr int LPR = D / 8, RPW = 32 / LPR, STEPS = kTile / RPW;    // lanes a row, rows a step, steps a tile
@@ -72,45 +73,68 @@ paged8_read_kernel(const __grid_constant__ Read8Args a)
         cur = s_b;
         base = s_base;
     }
-    const int sub = lane / LPR, l = lane % LPR;
-    for (u += warp; u < u1; u += kWarps) {
+    // where a unit's tile lies: page (-1: nothing to do) and output page, scales, tokens lo .. hi-1 of it
+    struct Tile { int page, head, at, lo, hi; long long to; float ks, vs; };
+    auto locate = [&](long long u) {
+        Tile t;
+        t.page = -1;
+        if (u >= u1) return t;
         Range r = range(cur);
         while (u >= base + (long long)r.tiles * heads) {
             base += (long long)r.tiles * heads;
             r = range(++cur);
         }
         const long long rel = u - base;
-        const int tile = (int)(rel / heads), head = (int)(rel - (long long)tile * heads);
-        const int token = (r.t0 + tile) * kTile, column = token >> a.shift, at = token & ((1 << a.shift) - 1);
+        const int tile = rel < 0x7fffffffll ? (int)rel / heads : (int)(rel / heads);
+        const int token = (r.t0 + tile) * kTile, column = token >> a.shift;
         const long long entry = (long long)cur * a.p.max_pages + column;
-        const int page = __ldg(a.table + entry);
-        const long long to = a.out_table ? __ldg(a.out_table + entry) : entry;
-        if (page < 0 || page >= a.p.num_pages || to < 0 || to >= a.p.out_pages) continue;
-        const size_t sc = scale_at(page, head, at, heads, a.shift, a.bshift);
-        const float ks = __ldg(a.k_scales + sc), vs = __ldg(a.v_scales + sc);
-        const long long from = page * a.p.page_stride + head * a.p.head_stride + at * a.p.token_stride + l * 8;
-        const long long dst = to * a.p.out_page_stride + head * a.p.out_head_stride + at * a.p.out_token_stride + l * 8;
-        uint2 c[2][STEPS];
-#pragma unroll
-        for (int j = 0; j < STEPS; ++j) {
-            const int i = j * RPW + sub;
-            const bool live = token + i >= r.lo && token + i < r.hi;
-            c[0][j] = live ? __ldg(reinterpret_cast<const uint2*>(a.k_pages + from + i * a.p.token_stride)) : make_uint2(0u, 0u);
-            c[1][j] = live ? __ldg(reinterpret_cast<const uint2*>(a.v_pages + from + i * a.p.token_stride)) : make_uint2(0u, 0u);
+        t.head = (int)(rel - (long long)tile * heads);
+        t.at = token & ((1 << a.shift) - 1);
+        t.lo = r.lo - token;
+        t.hi = r.hi - token;
+        t.page = __ldg(a.table + entry);
+        t.to = a.out_table ? __ldg(a.out_table + entry) : entry;
+        if (t.page >= a.p.num_pages || t.to < 0 || t.to >= a.p.out_pages) t.page = -1;
+        if (t.page >= 0) {
+            const size_t sc = scale_at(t.page, t.head, t.at, heads, a.shift, a.bshift);
+            t.ks = __ldg(a.k_scales + sc);
+            t.vs = __ldg(a.v_scales + sc);
         }
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv)
+        return t;
+    };
+    const int sub = lane / LPR, l = lane % LPR;
+    u += warp;
+    Tile t = locate(u);
+    for (; u < u1; u += kWarps) {
+        uint2 c[2][STEPS];
+        if (t.page >= 0) {
+            const long long from = t.page * a.p.page_stride + t.head * a.p.head_stride + t.at * a.p.token_stride + l * 8;
 #pragma unroll
             for (int j = 0; j < STEPS; ++j) {
                 const int i = j * RPW + sub;
-                if (token + i < r.lo || token + i >= r.hi) continue;
-                float y[8];
-                values<FORMAT>(c[kv][j].x, y);
-                values<FORMAT>(c[kv][j].y, y + 4);
-#pragma unroll
-                for (int x = 0; x < 8; ++x) y[x] *= kv ? vs : ks;
-                store8((T*)(kv ? a.v_out : a.k_out) + dst + i * a.p.out_token_stride, y);
+                const bool live = i >= t.lo && i < t.hi;
+                c[0][j] = live ? __ldg(reinterpret_cast<const uint2*>(a.k_pages + from + i * a.p.token_stride)) : make_uint2(0u, 0u);
+                c[1][j] = live ? __ldg(reinterpret_cast<const uint2*>(a.v_pages + from + i * a.p.token_stride)) : make_uint2(0u, 0u);
             }
+        }
+        const Tile next = locate(u + kWarps);          // on its way while these are
+        if (t.page >= 0) {
+            const long long dst = t.to * a.p.out_page_stride + t.head * a.p.out_head_stride + t.at * a.p.out_token_stride + l * 8;
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+                for (int j = 0; j < STEPS; ++j) {
+                    const int i = j * RPW + sub;
+                    if (i < t.lo || i >= t.hi) continue;
+                    float y[8];
+                    values<FORMAT>(c[kv][j].x, y);
+                    values<FORMAT>(c[kv][j].y, y + 4);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) y[x] *= kv ? t.vs : t.ks;
+                    store8((T*)(kv ? a.v_out : a.k_out) + dst + i * a.p.out_token_stride, y);
+                }
+        }
+        t = next;
     }
 }
 
