@@ -81,16 +81,20 @@ template <> struct Code<FADKV_E4M3> {
     {
         halves(__byte_perm(x, 0u, 0x3120), a, b);
     }
-    // the nearest codes of four values that lie in the type's range; what is not finite becomes NaN (y + 0 y)
-    static __device__ __forceinline__ uint32_t pack(float y0, float y1, float y2, float y3)
+    // the nearest codes of four y inv that are finite and in the type's range; in pack_any what is not finite becomes NaN
+    static __device__ __forceinline__ uint32_t pack(const float* y, float inv)
     {
         uint32_t r;
-        y0 = fmaf(y0, 0.f, y0), y1 = fmaf(y1, 0.f, y1), y2 = fmaf(y2, 0.f, y2), y3 = fmaf(y3, 0.f, y3);
         asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f32 l, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %4, %3;\n\t"
             "mov.b32 %0, {l, h};\n\t}"
             : "=r"(r)
-            : "f"(y0), "f"(y1), "f"(y2), "f"(y3));
+            : "f"(y[0] * inv), "f"(y[1] * inv), "f"(y[2] * inv), "f"(y[3] * inv));
         return r;
+    }
+    static __device__ __forceinline__ uint32_t pack_any(const float* y, float inv)
+    {
+        const float z[4] = {fmaf(y[0], 0.f, y[0]), fmaf(y[1], 0.f, y[1]), fmaf(y[2], 0.f, y[2]), fmaf(y[3], 0.f, y[3])};
+        return pack(z, inv);
     }
     // biased exponent of the least power of two t with a <= 448 t (448 = 1.75 2^8), a by its bits
     static __device__ __forceinline__ int exponent(uint32_t a) { return (int)(a >> 23) - 8 + ((a & 0x7fffffu) > 0x600000u); }
@@ -115,14 +119,21 @@ template <> struct Code<FADKV_I8> {
         a = centred(__byte_perm(x, 0x64646464u, 0x4240));
         b = centred(__byte_perm(x, 0x64646464u, 0x4341));
     }
-    // the nearest whole numbers; NaN becomes 0, what is past the range the largest
-    static __device__ __forceinline__ uint32_t one(float y)
+    // the nearest whole numbers of four y inv, by the low byte of 1.5 2^23 + y inv; in pack_any NaN becomes 0 and an infinity
+    // the largest
+    static __device__ __forceinline__ uint32_t pack(const float* y, float inv)
     {
-        return (uint32_t)__float2int_rn(fminf(fmaxf(y == y ? y : 0.f, -127.f), 127.f)) & 0xffu;
+        uint32_t z[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = __float_as_uint(__fadd_rn(__fmul_rn(y[i], inv), 12582912.f));
+        return __byte_perm(__byte_perm(z[0], z[1], 0x0040), __byte_perm(z[2], z[3], 0x0040), 0x5410);
     }
-    static __device__ __forceinline__ uint32_t pack(float y0, float y1, float y2, float y3)
+    static __device__ __forceinline__ uint32_t pack_any(const float* y, float inv)
     {
-        return one(y0) | one(y1) << 8 | one(y2) << 16 | one(y3) << 24;
+        float z[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = y[i] == y[i] ? fminf(fmaxf(y[i] * inv, -127.f), 127.f) : 0.f;
+        return pack(z, 1.f);
     }
     // 127 = 1.984375 2^6
     static __device__ __forceinline__ int exponent(uint32_t a) { return (int)(a >> 23) - 6 + ((a & 0x7fffffu) > 0x7e0000u); }
