@@ -79,8 +79,6 @@ __device__ __forceinline__ uint32_t swz8(int r, int c)
     return D == 128 ? (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-__device__ __forceinline__ void prefetch(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-
 __device__ __forceinline__ int add_acq_rel(int* p, int v)
 {
     int old;
@@ -127,10 +125,7 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
     unsigned char* wsmem = smem + warp * C_::WARP_BYTES;
     const uint32_t wbase = saddr(wsmem);
     float* rows = reinterpret_cast<float*>(smem + (ONE ? 0 : kWarps * C_::WARP_BYTES));
-    // Lengths and tables on their way to L2 while the kernel before this one ends (a hint: they are read after it).
-    if (tid * 32 < B && blockIdx.x == 0) prefetch(a.lengths + tid * 32);
-    if (const unsigned line = blockIdx.x * kThreads + tid; line * 32ull < (unsigned long long)B * a.p.max_pages)
-        prefetch(a.table + (size_t)line * 32);
+    prefetch_tables(a.lengths, a.table, B, a.p.max_pages);
     pdl_begin();
 
     auto blocks_of = [&](int b) {

@@ -15,8 +15,8 @@ using namespace paged8;
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTile = 16;
-constexpr int kPerSm = 6;
-constexpr int kCtas = 152 * kPerSm;
+// CTAs a multiprocessor: what the registers of two tiles in flight allow.
+template <int D> constexpr int kPerSm = D == 128 ? 4 : 6;
 
 __device__ __forceinline__ void store8(float* p, const float* y)
 {
@@ -31,7 +31,7 @@ __device__ __forceinline__ void store8(T* p, const float* y)
 }
 
 template <typename T, int D, int FORMAT>
-__global__ void __launch_bounds__(kThreads, kPerSm)
+__global__ void __launch_bounds__(kThreads, kPerSm<D>)
 paged8_read_kernel(const __grid_constant__ Read8Args a)
 {
     constexpr int LPR = D / 8, RPW = 32 / LPR, STEPS = kTile / RPW;    // lanes a row, rows a step, steps a tile
@@ -39,6 +39,7 @@ paged8_read_kernel(const __grid_constant__ Read8Args a)
     __shared__ long long s_base;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.p.B, heads = a.p.Hkv;
     const int most = a.p.max_pages << a.shift;
+    prefetch_tables(a.lengths, a.table, B, a.p.max_pages);
     pdl_begin();
 
     // tokens lo .. hi-1 of request b, in tiles from t0 on
@@ -78,6 +79,7 @@ paged8_read_kernel(const __grid_constant__ Read8Args a)
     auto locate = [&](long long u) {
         Tile t;
         t.page = -1;
+        t.head = t.at = t.lo = t.hi = 0;
         if (u >= u1) return t;
         Range r = range(cur);
         while (u >= base + (long long)r.tiles * heads) {
@@ -103,21 +105,26 @@ paged8_read_kernel(const __grid_constant__ Read8Args a)
         return t;
     };
     const int sub = lane / LPR, l = lane % LPR;
+    struct Codes { uint2 c[2][STEPS]; };
+    auto load = [&](const Tile& t, Codes& x) {
+        const long long from = t.page * a.p.page_stride + t.head * a.p.head_stride + t.at * a.p.token_stride + l * 8;
+#pragma unroll
+        for (int j = 0; j < STEPS; ++j) {
+            const int i = j * RPW + sub;
+            const bool live = t.page >= 0 && i >= t.lo && i < t.hi;
+            x.c[0][j] = live ? __ldg(reinterpret_cast<const uint2*>(a.k_pages + from + i * a.p.token_stride)) : make_uint2(0u, 0u);
+            x.c[1][j] = live ? __ldg(reinterpret_cast<const uint2*>(a.v_pages + from + i * a.p.token_stride)) : make_uint2(0u, 0u);
+        }
+    };
+    // a tile's codes are on their way while the one before it is stored, and the place of the one behind it is looked up
+    Codes now, ahead;
     u += warp;
     Tile t = locate(u);
+    load(t, now);
+    Tile next = locate(u + kWarps);
     for (; u < u1; u += kWarps) {
-        uint2 c[2][STEPS];
-        if (t.page >= 0) {
-            const long long from = t.page * a.p.page_stride + t.head * a.p.head_stride + t.at * a.p.token_stride + l * 8;
-#pragma unroll
-            for (int j = 0; j < STEPS; ++j) {
-                const int i = j * RPW + sub;
-                const bool live = i >= t.lo && i < t.hi;
-                c[0][j] = live ? __ldg(reinterpret_cast<const uint2*>(a.k_pages + from + i * a.p.token_stride)) : make_uint2(0u, 0u);
-                c[1][j] = live ? __ldg(reinterpret_cast<const uint2*>(a.v_pages + from + i * a.p.token_stride)) : make_uint2(0u, 0u);
-            }
-        }
-        const Tile next = locate(u + kWarps);          // on its way while these are
+        load(next, ahead);
+        const Tile after = locate(u + 2 * kWarps);
         if (t.page >= 0) {
             const long long dst = t.to * a.p.out_page_stride + t.head * a.p.out_head_stride + t.at * a.p.out_token_stride + l * 8;
 #pragma unroll
@@ -127,14 +134,16 @@ paged8_read_kernel(const __grid_constant__ Read8Args a)
                     const int i = j * RPW + sub;
                     if (i < t.lo || i >= t.hi) continue;
                     float y[8];
-                    values<FORMAT>(c[kv][j].x, y);
-                    values<FORMAT>(c[kv][j].y, y + 4);
+                    values<FORMAT>(now.c[kv][j].x, y);
+                    values<FORMAT>(now.c[kv][j].y, y + 4);
 #pragma unroll
                     for (int x = 0; x < 8; ++x) y[x] *= kv ? t.vs : t.ks;
                     store8((T*)(kv ? a.v_out : a.k_out) + dst + i * a.p.out_token_stride, y);
                 }
         }
+        now = ahead;
         t = next;
+        next = after;
     }
 }
 
@@ -143,7 +152,8 @@ cudaError_t launch_t(const Read8Args& a, cudaStream_t st)
 {
     // an upper bound of the tiles: lengths are known on the device only
     const long long tiles = (((long long)a.p.max_pages << a.shift) / kTile) * a.p.B * a.p.Hkv;
-    const unsigned grid = (unsigned)(tiles < kCtas ? tiles : kCtas);
+    const long long ctas = 152 * kPerSm<D>;
+    const unsigned grid = (unsigned)(tiles < ctas ? tiles : ctas);
     return launch_pdl(a.p.format == FADKV_E4M3 ? paged8_read_kernel<T, D, FADKV_E4M3> : paged8_read_kernel<T, D, FADKV_I8>, dim3(grid),
                       dim3(kThreads), 0, st, a);
 }

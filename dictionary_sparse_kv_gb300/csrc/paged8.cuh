@@ -64,6 +64,16 @@ __device__ __forceinline__ size_t scale_at(int page, int head, int token, int he
     return (((size_t)page * heads + head) << (shift - bshift)) + (token >> bshift);
 }
 
+// Lengths and block tables on their way to L2 while the kernel before this one
+// ends: a hint that returns nothing, so that it may come before the wait for
+// that kernel.
+__device__ __forceinline__ void prefetch_tables(const int32_t* lengths, const int32_t* table, int B, int max_pages)
+{
+    const unsigned line = blockIdx.x * blockDim.x + threadIdx.x;
+    if (line * 32u < (unsigned)B) asm volatile("prefetch.global.L2 [%0];" ::"l"(lengths + line * 32u));
+    if (line * 32ull < (unsigned long long)B * max_pages) asm volatile("prefetch.global.L2 [%0];" ::"l"(table + (size_t)line * 32));
+}
+
 // Codes as binary16 values (both formats' are exact there) and in 32 bits.
 template <int FORMAT> struct Code;
 
