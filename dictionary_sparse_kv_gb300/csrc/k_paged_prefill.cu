@@ -55,6 +55,8 @@
 // FADKV_DEV_TIMEOUT in the workspace's first word, and the CTA drains and
 // returns: the copies, the products and the stores to TMEM that its warps
 // issued are waited for before TMEM is given back.
+#include <algorithm>
+
 #include "paged.cuh"
 #include "tc_common.cuh"
 
@@ -328,6 +330,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_con
     // (waits only: blocks of the join that are let in early slow the last pieces down: 84 tokens on 32768 43.1 against 40.6 us,
     // on 8192 23.4 against 21.5)
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (ROWS && a.split == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // no join follows
     // the items' warp reads its first requests meanwhile: a lane each, its first row, its rows, its rows before T is cut
     // off, its tokens, its pairs of tiles
     int start = 0, cnt = 0, all = 0, my_len = 0, tiles = 0;
@@ -1037,7 +1040,7 @@ struct PreShape {
     int split;                 // 0: items are not cut; else the tiles of an item that can hold rows
 };
 
-PreShape pre_shape(const fadkv_paged_params& p)
+PreShape pre_shape(const fadkv_paged_params& p, bool rows)
 {
     PreShape s;
     const int grp = p.Hq / p.Hkv;
@@ -1050,7 +1053,15 @@ PreShape pre_shape(const fadkv_paged_params& p)
     // requests, and if there can be keys for two pieces.  How many pieces there are is decided on the device.
     long long most = (long long)p.max_pages * p.page_size;
     if (p.window > 0) most = most < (long long)p.window + p.sinks + 2 * kKeys ? most : (long long)p.window + p.sinks + 2 * kKeys;
-    const bool cut = p.B <= 256 && (tiles + 1) * heads <= kPreCtas && most >= 2 * kLeastTiles * kKeys;
+    bool cut = p.B <= 256 && (tiles + 1) * heads <= kPreCtas && most >= 2 * kLeastTiles * kKeys;
+    if (rows && cut) {
+        // Prompts: T bounds the keys, mostly from far above, so the longest prompt is taken for twice the mean.  Cutting saves
+        // its key tiles' time (1.2 us each) but for items / 152 of it, and the pieces and their join cost some 10 us (8 heads over
+        // 1 of 128, 1500 tokens in 47 items: 21.2 us cut and 21.7 whole; 8 over 2, 1100 in 36: 23.5 and 20.2; 24 over 8, 1100
+        // in 112: 33 and 19; one head, 4000 in 16: 18 and 50).
+        const long long keys = std::min(std::min(most, (long long)p.T), 2ll * p.T / std::max(p.B, 1)), items = (tiles + 1) * heads;
+        cut = 3 * items <= kPreCtas && keys / kKeys * (kPreCtas - items) >= 1300;
+    }
     s.split = !cut ? 0 : (p.T <= s.tq ? 1 : 2);
     return s;
 }
@@ -1062,7 +1073,7 @@ cudaError_t launch_rows(const PagedArgs& args, cudaStream_t st)
     cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, PreCfg<D>::alloc);
     if (e != cudaSuccess) return e;
     PagedArgs a = args;
-    const PreShape s = pre_shape(a.p);
+    const PreShape s = pre_shape(a.p, ROWS);
     a.split = s.split;
     if (a.p.window >= a.p.max_pages << a.shift) a.p.window = 0;   // hides nothing
     a.tile_ns = a.wait_ns ? 0 : kTileNs;               // (a test's limit is the whole limit)
@@ -1088,9 +1099,9 @@ cudaError_t launch_t(const PagedArgs& a, cudaStream_t st, bool rows)
 
 }  // namespace
 
-size_t paged_prefill_workspace(const fadkv_paged_params& p)
+size_t paged_prefill_workspace(const fadkv_paged_params& p, bool rows)
 {
-    return kHeadBytes + (size_t)kSplitSlots * pre_shape(p).split * slot_floats(p.d) * sizeof(float);
+    return kHeadBytes + (size_t)kSplitSlots * pre_shape(p, rows).split * slot_floats(p.d) * sizeof(float);
 }
 
 cudaError_t launch_paged_prefill(const PagedArgs& a, cudaStream_t st, bool rows)

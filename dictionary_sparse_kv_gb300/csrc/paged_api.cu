@@ -526,7 +526,7 @@ fadkv_status fadkv_prompt_attend_workspace_bytes(const fadkv_prompt_params* p, s
     const fadkv_status st = check_prompt(p);
     if (st != FADKV_OK) return st;
     if (!bytes) return FADKV_ERR_INVALID_ARG;
-    *bytes = paged_prefill_workspace(prompt_shape(*p));
+    *bytes = paged_prefill_workspace(prompt_shape(*p), true);
     return FADKV_OK;
 }
 
@@ -537,7 +537,7 @@ fadkv_status fadkv_prompt_attend(const fadkv_prompt_params* p, const void* q, co
     const fadkv_status st = check_prompt(p);
     if (st != FADKV_OK) return st;
     const fadkv_paged_params shape = prompt_shape(*p);
-    if (workspace_bytes < paged_prefill_workspace(shape) || !workspace) return FADKV_ERR_WORKSPACE;
+    if (workspace_bytes < paged_prefill_workspace(shape, true) || !workspace) return FADKV_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return FADKV_ERR_INVALID_ARG;
     if (p->B > 0 && p->T > 0) {
         if (!q || !k || !v || !starts || !out) return FADKV_ERR_INVALID_ARG;
