@@ -79,6 +79,11 @@ __device__ __forceinline__ uint32_t swz8(int r, int c)
     return D == 128 ? (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)) : (uint32_t)(r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
+__device__ __forceinline__ void cp16_all(uint32_t dst, const void* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 __device__ __forceinline__ int add_acq_rel(int* p, int v)
 {
     int old;
@@ -107,10 +112,14 @@ struct Work {
     Blocks seen;
 };
 
-template <typename T, int D, int NT, int FORMAT, bool ONE>
+// TILES of eight heads; 0: four heads, twice, for the two terms of their
+// weights, which one product then takes together.
+template <typename T, int D, int TILES, int FORMAT, bool ONE>
 __global__ void __launch_bounds__(kThreads, Cfg<D, ONE>::PER_SM)
 paged8_attend_kernel(const __grid_constant__ Paged8Args a)
 {
+    constexpr bool TWO = TILES == 0;
+    constexpr int NT = TWO ? 1 : TILES;
     using C_ = Cfg<D, ONE>;
     constexpr int STAGES = C_::STAGES, CPR = D / 16;                   // 16-byte chunks per row
     constexpr int KS = D / 16, ROW = C_::ROW;                          // 16-element steps; floats of a result
@@ -302,8 +311,8 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
     };
 
     // The piece's tiles of this warp (16 tokens of each block), 32 at a time, a lane each: page, tokens that are seen (none on
-    // a page that is none), scale of the keys, log2 of the values'.
-    struct Info { int page; uint32_t seen; float ks, ls; };
+    // a page that is none), where they lie in the pools, scale of the keys, log2 of the values'.
+    struct Info { int page; uint32_t seen; long long off; float ks, ls; };
     Info cur, nxt;
     auto token_of = [&](const Work& w, int t) { return w.seen.token(w.blk0 + t) + warp * kTile; };
     auto pages = [&](const Work& w, int t, Info& f) {
@@ -315,36 +324,47 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
             if (f.seen) f.page = __ldg(a.table + (size_t)w.b * a.p.max_pages + (tok >> a.shift));
         }
     };
+    auto places = [&](const Work& w, int t, Info& f) {
+        if (f.page < 0 || f.page >= a.p.num_pages) f.seen = 0u;
+        f.off = f.seen ? f.page * a.p.page_stride + (token_of(w, t + lane) & ((1 << a.shift) - 1)) * a.p.token_stride : 0;
+    };
     auto scales = [&](const Work& w, int t, Info& f) {
         f.ks = f.ls = 0.f;
-        if (f.page >= 0 && f.page < a.p.num_pages) {
+        if (f.seen) {
             const size_t at = scale_at(f.page, w.hk, token_of(w, t + lane) & ((1 << a.shift) - 1), a.p.Hkv, a.shift, a.bshift);
             f.ks = __ldg(a.k_scales + at);
             f.ls = __log2f(__ldg(a.v_scales + at));
-        } else {
-            f.seen = 0u;
         }
     };
-    const int row0 = lane / CPR, chunk = lane % CPR;                   // this lane's pieces of a tile: rows row0 + j 32 / CPR
+    const int row0 = lane / CPR, chunk = lane % CPR;                   // this lane's chunks of a tile: rows row0 + j 32 / CPR
     const long long lane_off = row0 * a.p.token_stride + chunk * 16, step_off = (32 / CPR) * a.p.token_stride;
+    int st_in = 0, st_out = 0;                                         // the ring's next tile to load and to use
     // tile t, whose Info is in f
     auto load = [&](const Work& w, int t, const Info& f) {
-        const int page = __shfl_sync(0xffffffffu, f.page, t & 31);
         const uint32_t seen = __shfl_sync(0xffffffffu, f.seen, t & 31);
-        if (page < 0 || page >= a.p.num_pages) return;
-        const int at = token_of(w, t) & ((1 << a.shift) - 1);
-        const long long off = page * a.p.page_stride + w.hk * a.p.head_stride + at * a.p.token_stride + lane_off;
-        const uint32_t dst = wbase + (t % STAGES) * 2 * C_::TILE_BYTES;
+        const uint32_t dst = wbase + st_in * 2 * C_::TILE_BYTES;
+        st_in = st_in + 1 == STAGES ? 0 : st_in + 1;
+        const long long off = __shfl_sync(0xffffffffu, f.off, t & 31) + w.hk * a.p.head_stride + lane_off;
+        const uint8_t *k = a.k + off, *v = a.v + off;
+        if (seen == 0xffffu) {
 #pragma unroll
-        for (int j = 0; j < kTile * CPR / 32; ++j) {
-            const int r = row0 + j * (32 / CPR);
-            const bool v = (seen >> r) & 1u;
-            cp16(dst + swz8<D>(r, chunk), a.k + off + j * step_off, v);
-            cp16(dst + C_::TILE_BYTES + swz8<D>(r, chunk), a.v + off + j * step_off, v);
+            for (int j = 0; j < kTile * CPR / 32; ++j) {
+                cp16_all(dst + swz8<D>(row0 + j * (32 / CPR), chunk), k + j * step_off);
+                cp16_all(dst + C_::TILE_BYTES + swz8<D>(row0 + j * (32 / CPR), chunk), v + j * step_off);
+            }
+        } else if (seen) {
+#pragma unroll
+            for (int j = 0; j < kTile * CPR / 32; ++j) {
+                const int r = row0 + j * (32 / CPR);
+                cp16(dst + swz8<D>(r, chunk), k + j * step_off, (seen >> r) & 1u);
+                cp16(dst + C_::TILE_BYTES + swz8<D>(r, chunk), v + j * step_off, (seen >> r) & 1u);
+            }
         }
     };
     auto begin = [&](const Work& w) {                                   // the first tiles, STAGES - 1 copy groups
+        st_in = st_out = 0;
         pages(w, 0, cur);
+        places(w, 0, cur);
         for (int t = 0; t < STAGES - 1; ++t) {
             if (w.blk0 + t < w.blk1) load(w, t, cur);
             cp_commit();
@@ -355,11 +375,11 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
     // Queries as the B operand: lane holds head lane / 4; of step k its elements 16 k + 4 (lane % 4) + {0, 1, 2, 3}, the
     // order in which the lanes have a row's bytes.  qs: what the scores of heads 2 (lane % 4) + {0, 1} are multiplied by.
     uint32_t qf[NT][KS][2];
-    float qs[NT][2];
+    float qs[NT][2], qo[NT][2];                                        // (qo: kOffset times the sum of their elements)
     auto load_q = [&](const Work& w) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int h = n * 8 + (lane >> 2);
+            const int h = n * 8 + (TWO ? lane >> 2 & 3 : lane >> 2);
             const uint2* q = reinterpret_cast<const uint2*>((const T*)a.q + (size_t)w.b * a.p.q_stride + (size_t)(w.head0 + (h < w.hn ? h : 0)) * D) + (lane & 3);
             float mine = a.scale_log2;
 #pragma unroll
@@ -389,6 +409,19 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
             }
             qs[n][0] = __shfl_sync(0xffffffffu, mine, (lane & 3) * 8);
             qs[n][1] = __shfl_sync(0xffffffffu, mine, (lane & 3) * 8 + 4);
+            if (Code<FORMAT>::kOffset != 0.f) {
+                float sum = 0.f;
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    const float2 y = Num<__half>::unpack(qf[n][k][0]), z = Num<__half>::unpack(qf[n][k][1]);
+                    sum += (y.x + y.y) + (z.x + z.y);
+                }
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                sum *= Code<FORMAT>::kOffset;
+                qo[n][0] = __shfl_sync(0xffffffffu, sum, (lane & 3) * 8);
+                qo[n][1] = __shfl_sync(0xffffffffu, sum, (lane & 3) * 8 + 4);
+            }
         }
     };
 
@@ -413,17 +446,20 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
                 cur = nxt;
                 pages(w, t + 32, nxt);
             }
-            if ((t & 31) == 16) scales(w, (t & ~31) + 32, nxt);
+            if ((t & 31) == 16) {
+                places(w, (t & ~31) + 32, nxt);
+                scales(w, (t & ~31) + 32, nxt);
+            }
             cp_wait<STAGES - 2>();
             __syncwarp();
             const int ahead = t + STAGES - 1;
             if (ahead < tiles) load(w, ahead, (ahead ^ t) < 32 ? cur : nxt);
             cp_commit();
+            const uint32_t kt = wbase + st_out * 2 * C_::TILE_BYTES, vt = kt + C_::TILE_BYTES;
+            st_out = st_out + 1 == STAGES ? 0 : st_out + 1;
             const uint32_t oks = __shfl_sync(0xffffffffu, cur.seen, t & 31);
             if (oks == 0u) continue;
             const float ks = __shfl_sync(0xffffffffu, cur.ks, t & 31), ls = __shfl_sync(0xffffffffu, cur.ls, t & 31);
-            const uint32_t kt = wbase + (t % STAGES) * 2 * C_::TILE_BYTES, vt = kt + C_::TILE_BYTES;
-
             float sc[NT][4], sc2[NT][4];
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -437,8 +473,8 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     uint32_t f[4];
-                    Code<FORMAT>::halves(b[2 * i], f[0], f[2]);
-                    Code<FORMAT>::halves(b[2 * i + 1], f[1], f[3]);
+                    Code<FORMAT>::shifted(b[2 * i], f[0], f[2]);
+                    Code<FORMAT>::shifted(b[2 * i + 1], f[1], f[3]);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) Num<__half>::mma(i ? sc2[n] : sc[n], f, qf[n][k + i][0], qf[n][k + i][1]);
                 }
@@ -447,7 +483,11 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sc[n][i] = (sc[n][i] + sc2[n][i]) * (ks * qs[n][i & 1]);
+                for (int i = 0; i < 4; ++i) {
+                    sc[n][i] += sc2[n][i];
+                    if (Code<FORMAT>::kOffset != 0.f) sc[n][i] = fmaf(sc[n][i], Code<FORMAT>::kUnit, -qo[n][i & 1]);
+                    sc[n][i] *= ks * qs[n][i & 1];
+                }
                 if (oks != 0xffffu) {
                     const bool ok0 = (oks >> (lane >> 2)) & 1u, ok1 = (oks >> ((lane >> 2) + 8)) & 1u;
 #pragma unroll
@@ -506,10 +546,13 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
                 }
                 const uint32_t a0 = Num<__half>::pack(e[0], e[1]), a1 = Num<__half>::pack(e[2], e[3]);
                 const float2 r0 = Num<__half>::unpack(a0), r1 = Num<__half>::unpack(a1);
-                ph[n][0] = transpose8(a0);
-                ph[n][1] = transpose8(a1);
-                pl[n][0] = transpose8(Num<__half>::pack(e[0] - r0.x, e[1] - r0.y));
-                pl[n][1] = transpose8(Num<__half>::pack(e[2] - r1.x, e[3] - r1.y));
+                const uint32_t b0 = Num<__half>::pack(e[0] - r0.x, e[1] - r0.y), b1 = Num<__half>::pack(e[2] - r1.x, e[3] - r1.y);
+                ph[n][0] = transpose8(TWO && (lane & 2) ? b0 : a0);
+                ph[n][1] = transpose8(TWO && (lane & 2) ? b1 : a1);
+                if (!TWO) {
+                    pl[n][0] = transpose8(b0);
+                    pl[n][1] = transpose8(b1);
+                }
             }
 #pragma unroll
             for (int k = 0; k < KS; k += 2) {
@@ -523,7 +566,7 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         Num<__half>::mma(o[n][k + i], f, ph[n][0], ph[n][1]);
-                        Num<__half>::mma(o[n][k + i], f, pl[n][0], pl[n][1]);
+                        if (!TWO) Num<__half>::mma(o[n][k + i], f, pl[n][0], pl[n][1]);
                     }
                 }
             }
@@ -598,8 +641,14 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
                 const float f = v == 0.f ? 0.f : __fdividef(exp2_fast(Mg[n][i] == -INFINITY ? 0.f : Mr[n][i] - mr[n][i] - kUp), v);
                 float* r = rows + (warp * 8 + 2 * (lane & 3) + i) * ROW;       // (f is 0 where nothing was seen)
 #pragma unroll
-                for (int k = 0; k < KS; ++k)
-                    *reinterpret_cast<float2*>(r + k * 16 + (lane >> 2) * 2) = make_float2(o[n][k][i] * f, o[n][k][i + 2] * f);
+                for (int k = 0; k < KS; ++k) {
+                    float2 y = make_float2(o[n][k][i], o[n][k][i + 2]);
+                    if (TWO) {                          // both terms' sums
+                        y.x += __shfl_xor_sync(0xffffffffu, y.x, 2);
+                        y.y += __shfl_xor_sync(0xffffffffu, y.y, 2);
+                    }
+                    *reinterpret_cast<float2*>(r + k * 16 + (lane >> 2) * 2) = make_float2(y.x * f, y.y * f);
+                }
                 if (lane < 4) *reinterpret_cast<float2*>(r + D) = make_float2(mg[n][i] == -INFINITY ? -INFINITY : mr[n][i], v);
             }
             __syncthreads();
@@ -669,34 +718,42 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
     }
 }
 
-template <typename T, int D, int NT, int FORMAT, bool ONE>
+template <typename T, int D, int TILES, int FORMAT, bool ONE>
 cudaError_t launch_one(const Paged8Args& a, int grid, cudaStream_t st)
 {
-    auto k = paged8_attend_kernel<T, D, NT, FORMAT, ONE>;
+    auto k = paged8_attend_kernel<T, D, TILES, FORMAT, ONE>;
     const int smem = Cfg<D, ONE>::SMEM;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(k, dim3((unsigned)grid), dim3(kThreads), smem, st, a);
 }
 
-template <typename T, int D, int NT, int FORMAT>
+template <typename T, int D, int TILES, int FORMAT>
 cudaError_t launch_nt(const Paged8Args& a, cudaStream_t st)
 {
+    constexpr int NT = TILES == 0 ? 1 : TILES;
     // an upper bound of the units: lengths are known on the device only
     long long most = (long long)a.p.max_pages << a.shift;
     if (a.p.window > 0) most = most < (long long)a.p.window + a.p.sinks ? most : (long long)a.p.window + a.p.sinks;
-    const long long sets = (long long)a.p.B * a.p.Hkv * ((a.grp + 8 * NT - 1) / (8 * NT)), units = ((most + kBlock - 1) / kBlock + 2) * sets;
+    const long long sets = (long long)a.p.B * a.p.Hkv * ((a.grp + 8 * NT - 1) / (8 * NT));
+    const long long units = ((most + kBlock - 1) / kBlock + 2) * sets;
     const int grid = (int)(units < kCtas<D> ? units : kCtas<D>);
     // (one piece a CTA: sums of units in 32 bits)
-    if (sets <= grid && units < 0x7fffffffll) return launch_one<T, D, NT, FORMAT, true>(a, grid, st);
-    return launch_one<T, D, NT, FORMAT, false>(a, grid, st);
+    if (sets <= grid && units < 0x7fffffffll) return launch_one<T, D, TILES, FORMAT, true>(a, grid, st);
+    return launch_one<T, D, TILES, FORMAT, false>(a, grid, st);
+}
+
+template <typename T, int D, int FORMAT>
+cudaError_t launch_f(const Paged8Args& a, cudaStream_t st)
+{
+    if (a.grp <= 4) return launch_nt<T, D, 0, FORMAT>(a, st);
+    return a.grp <= 8 ? launch_nt<T, D, 1, FORMAT>(a, st) : launch_nt<T, D, 2, FORMAT>(a, st);
 }
 
 template <typename T, int D>
 cudaError_t launch_t(const Paged8Args& a, cudaStream_t st)
 {
-    if (a.p.format == FADKV_E4M3) return a.grp <= 8 ? launch_nt<T, D, 1, FADKV_E4M3>(a, st) : launch_nt<T, D, 2, FADKV_E4M3>(a, st);
-    return a.grp <= 8 ? launch_nt<T, D, 1, FADKV_I8>(a, st) : launch_nt<T, D, 2, FADKV_I8>(a, st);
+    return a.p.format == FADKV_E4M3 ? launch_f<T, D, FADKV_E4M3>(a, st) : launch_f<T, D, FADKV_I8>(a, st);
 }
 
 }  // namespace

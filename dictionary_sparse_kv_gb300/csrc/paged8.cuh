@@ -91,6 +91,9 @@ template <> struct Code<FADKV_E4M3> {
     {
         halves(__byte_perm(x, 0u, 0x3120), a, b);
     }
+    // as halves, but for a factor and an offset, which are put right in a sum of products q code: sum = kUnit sum' - kOffset sum(q)
+    static constexpr float kUnit = 1.f, kOffset = 0.f;
+    static __device__ __forceinline__ void shifted(uint32_t x, uint32_t& a, uint32_t& b) { halves(x, a, b); }
     // the nearest codes of four y inv that are finite and in the type's range; in pack_any what is not finite becomes NaN
     static __device__ __forceinline__ uint32_t pack(const float* y, float inv)
     {
@@ -128,6 +131,14 @@ template <> struct Code<FADKV_I8> {
         x ^= 0x80808080u;
         a = centred(__byte_perm(x, 0x64646464u, 0x4240));
         b = centred(__byte_perm(x, 0x64646464u, 0x4341));
+    }
+    // (code + 128) 2^-24: a byte is a number below binary16's normal range as it stands
+    static constexpr float kUnit = 16777216.f, kOffset = 128.f;
+    static __device__ __forceinline__ void shifted(uint32_t x, uint32_t& a, uint32_t& b)
+    {
+        x ^= 0x80808080u;
+        a = __byte_perm(x, 0u, 0x4140);
+        b = __byte_perm(x, 0u, 0x4342);
     }
     // the nearest whole numbers of four y inv, by the low byte of 1.5 2^23 + y inv; in pack_any NaN becomes 0 and an infinity
     // the largest
