@@ -184,7 +184,7 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
             int n = 0;
 #pragma unroll
             for (int i = 0; i < kEach; ++i)
-                if (i < each) n += (int)((unsigned)(nb[i] + x - 1) / (unsigned)x);
+                if (i < each) n += (int)(((unsigned)nb[i] + (unsigned)x - 1u) / (unsigned)x);
             return n;
         };
         // (all / x + sets of them are too many: this x is large enough)

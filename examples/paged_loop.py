@@ -1,11 +1,12 @@
-"""One attention layer of a serving loop: full vectors in pages, codes beside them.
+"""One attention layer of a serving loop: full vectors in pages, the same in 8 bits and codes beside them.
 
 Prompts of several requests are planned into pages, their queries and keys
-normalised, rotated and appended, and attended in one call; then decode steps
-follow, one token a request.  Every step's keys and values are also encoded
-into the layer's dictionaries and stored as packed codes, so the same query is
-answered three ways: over all full vectors, over a recent window and the first
-tokens of them, and over the codes.
+normalised, rotated and appended, and attended in one call, from the pages and
+from their own rows; then decode steps follow, one token a request.  Every
+step's keys and values are also quantised into 8-bit pages (the same slots)
+and encoded into the layer's dictionaries, stored as packed codes, so the same
+query is answered four ways: over all full vectors, over a recent window and
+the first tokens of them, over the 8-bit pages, and over the codes.
 
     python examples/paged_loop.py [--steps 16] [--prompt 48]
 """
@@ -33,6 +34,9 @@ class Layer:
         columns = -(-longest // PAGE)
         pages = R * columns
         self.k_pages, self.v_pages = (torch.zeros((pages, HKV, PAGE, D), dtype=torch.float16, device=dev) for _ in range(2))
+        # the 8-bit pages: a scale for each 16 tokens and head
+        self.pools8 = [torch.zeros((pages, HKV, PAGE, D), dtype=torch.int8, device=dev) for _ in range(2)] + [
+            torch.zeros((pages, HKV, PAGE // 16), device=dev) for _ in range(2)]
         self.table = torch.full((R, columns), -1, **i32)
         self.free, self.free_count = torch.arange(pages, **i32), torch.tensor([pages], **i32)
         self.lengths, self.starts, self.refused = torch.zeros(R, **i32), torch.zeros(R + 1, **i32), torch.zeros(1, **i32)
@@ -67,6 +71,8 @@ class Layer:
         q_out, k_out = torch.empty((T, HQ, D), dtype=torch.float16, device=self.dev), torch.empty((T, HKV, D), dtype=torch.float16, device=self.dev)
         F.qk_norm_rope(F.qk_params(q, k, v, q_out, self.k_pages, k_out=k_out, v_pages=self.v_pages, wq=self.wq, wk=self.wk), self.rope, q, k, v, self.wq, self.wk, self.positions, self.slots,
                        q_out, k_out, self.k_pages, self.v_pages)
+        k8, v8, ks, vs = self.pools8
+        F.paged8_append(F.append8_params(k_out, v, k8, "head", ks, v8, vs), k_out, v, self.slots, k8, v8, ks, vs)
         return q_out, k_out, v
 
     def code(self, k, v, pos):
@@ -82,6 +88,23 @@ class Layer:
         p = F.paged_params(q, out, self.k_pages, "head", self.table, window, sinks, v_pages=self.v_pages)
         ws = self.workspace("decode", F.paged_attend_workspace_bytes(p))
         F.paged_attend(p, self.k_pages, self.v_pages, self.table, self.lengths, q, out, None, ws, positions=positions)
+        return out
+
+    def attend8(self, q, positions=None):
+        """The same over the 8-bit pages."""
+        out = torch.empty_like(q)
+        k8, v8, ks, vs = self.pools8
+        p = F.paged8_params(q, out, k8, ks, "head", self.table, v_pages=v8, v_scales=vs)
+        ws = self.workspace("decode", F.paged8_attend_workspace_bytes(p))
+        F.paged8_attend(p, k8, v8, ks, vs, self.table, self.lengths, q, out, None, ws, positions=positions)
+        return out
+
+    def prompt(self, q, k, v):
+        """Prompts from their own rows (starts[b] .. starts[b + 1]), whatever the cache keeps of them."""
+        out = torch.empty_like(q)
+        p = F.prompt_params(q, k, v, out, self.R)
+        ws = self.workspace("prefill", F.prompt_attend_workspace_bytes(p))
+        F.prompt_attend(p, q, k, v, self.starts, out, None, ws, positions=self.positions)
         return out
 
     def prefill(self, q, window=0, sinks=0):
@@ -117,6 +140,7 @@ def main(argv=None):
     # the prompts: all of them in one call, a request's tokens together
     q, k, v = layer.append(torch.full((a.requests,), a.prompt, **i32))
     out = layer.prefill(q)
+    rows = (layer.prompt(q, k, v) - out).abs().max().item()
     by_token = lambda x: x.view(a.requests, a.prompt, -1, D).transpose(0, 1)
     for t in range(a.prompt):
         layer.code(by_token(k)[t], by_token(v)[t], torch.full((a.requests,), t, **i32))
@@ -130,11 +154,11 @@ def main(argv=None):
         layer.code(k, v, layer.lengths - 1)
         full = layer.attend(q, positions=layer.positions).float()
         recent = layer.attend(q, a.window, a.sinks, layer.positions).float()
-        for name, other in (("window", recent), ("codes", layer.attend_codes(q))):
+        for name, other in (("window", recent), ("8 bits", layer.attend8(q, layer.positions).float()), ("codes", layer.attend_codes(q))):
             diff.setdefault(name, []).append(((other - full).norm() / full.norm()).item())
     torch.cuda.synchronize()
     result = {"tokens": layer.lengths.tolist(), "refused": int(layer.refused), "pages left": int(layer.free_count),
-              "prefill and decode differ by": same, **{n + " against full": sum(d) / len(d) for n, d in diff.items()}}
+              "prefill and decode differ by": same, "prompts from pages and from rows differ by": rows, **{n + " against full": sum(d) / len(d) for n, d in diff.items()}}
     for n, x in result.items():
         print(f"{n}: {x}")
     return result
