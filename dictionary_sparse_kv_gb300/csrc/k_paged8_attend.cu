@@ -52,7 +52,7 @@ template <int D, bool ONE> struct Cfg {
     static constexpr int TILE_BYTES = kTile * D;
     static constexpr int WARP_BYTES = STAGES * 2 * TILE_BYTES;
     static constexpr int ROW = D + 8;                                  // floats of a result: d values, m, l; padding
-    static constexpr int JOIN_BYTES = D == 128 ? 24576 : 16384;        // results that are joined
+    static constexpr int JOIN_BYTES = ONE ? kWarps * WARP_BYTES : D == 128 ? 24576 : 16384;   // results that are joined
     static constexpr int SMEM = kWarps * WARP_BYTES + (ONE ? 0 : JOIN_BYTES);
     static_assert(kWarps * WARP_BYTES >= JOIN_BYTES, "join");
 };
@@ -65,7 +65,7 @@ constexpr int kCounters = 1024;
 static_assert(kCtas<64> <= kCounters && kCtas<128> <= kCounters, "counters");
 static_assert(3 * kCounters * sizeof(int) <= kHeadBytes - kDecodeHead, "workspace head");
 
-template <int D> constexpr bool kJoins = Cfg<D, true>::JOIN_BYTES >= (kAtOnce > 8 * kWarps ? kAtOnce : 8 * kWarps) * Cfg<D, true>::ROW * 4;
+template <int D> constexpr bool kJoins = Cfg<D, false>::JOIN_BYTES >= (kAtOnce > 8 * kWarps ? kAtOnce : 8 * kWarps) * Cfg<D, false>::ROW * 4;
 static_assert(kJoins<64> && kJoins<128>, "join");
 
 // A piece in the workspace: a row for each of its heads.
@@ -189,11 +189,14 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
         };
         // (all / x + sets of them are too many: this x is large enough)
         int lo = (int)((all + grid - 1) / grid), hi = 0x7fffffff;
-        if (sets < grid) {
-            hi = (int)(all / (unsigned)(grid - sets)) + 1;
-        } else {
-            hi = few ? __reduce_max_sync(0xffffffffu, longest) : (int)all;
-        }
+        if (few) longest = __reduce_max_sync(0xffffffffu, longest);
+        if (sets < grid) hi = (int)(all / (unsigned)(grid - sets)) + 1;
+        else hi = few ? longest : (int)all;
+        // Few requests: pieces that are worth their join, which grows with their number (one request of 24 heads over 8 of 128, us: 5
+        // blocks 6.1 whole and 6.6 in 5 pieces; 24 blocks 9.1 in 24, 7.9 in 12, 8.3 in 6; 47 blocks 10.6 in 47, 10.1 in 16, 11.1 in
+        // 6; 63 blocks of 8 heads over 1 13.2 in 63, 12.5 in 16 and in 8).
+        if (few) lo = max(lo, longest <= 6 ? longest : (int)ceilf(sqrtf((float)longest * (1.f / 6.f))));
+        hi = max(lo, hi);
         int slot = 1;
         while (lo < hi) {
             const int mid = lo + (hi - lo) / 2;
