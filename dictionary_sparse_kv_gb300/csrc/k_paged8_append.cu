@@ -23,13 +23,19 @@ namespace {
 using namespace paged8;
 
 constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kWindow = 31;      // rows whose runs a warp looks for at a time (their slots and the one before: a lane each)
 // Steps of rows kept in shared memory between the two passes, 8 KB a warp.
 constexpr int kHeldBytes = 8192;
 template <typename T> constexpr int kHeld = kHeldBytes / (256 * (int)sizeof(T));
 
-// Eight consecutive elements as loaded; their largest |x| as the type's bits.
-template <typename T> struct Raw8 {
+// Eight elements of a row as loaded, those from first(l) on for lane l: eight that
+// follow one another, or in 32 bits four and four half a row on, so that a row's
+// lanes read whole sectors together; their largest |x| as the type's bits.
+template <typename T, int D> struct Raw8 {
     uint4 a;
+    static constexpr int kGap = 4;
+    static __device__ __forceinline__ int first(int l) { return l * 8; }
     // a lane's 16 bytes of step u in its warp's buffer
     static __device__ __forceinline__ void copy(uint32_t buf, int u, const T* p) { paged::cp16(buf + u * 512, p, true); }
     __device__ __forceinline__ void held(const unsigned char* buf, int u) { a = *reinterpret_cast<const uint4*>(buf + u * 512); }
@@ -52,12 +58,14 @@ template <typename T> struct Raw8 {
     }
     static __device__ __forceinline__ uint32_t wide(uint32_t bits) { return __float_as_uint(Num<T>::unpack(bits).x); }
 };
-template <> struct Raw8<float> {
+template <int D> struct Raw8<float, D> {
     float4 a, b;
+    static constexpr int kGap = D / 2;
+    static __device__ __forceinline__ int first(int l) { return l * 4; }
     static __device__ __forceinline__ void copy(uint32_t buf, int u, const float* p)
     {
         paged::cp16(buf + u * 1024, p, true);
-        paged::cp16(buf + u * 1024 + 512, p + 4, true);
+        paged::cp16(buf + u * 1024 + 512, p + kGap, true);
     }
     __device__ __forceinline__ void held(const unsigned char* buf, int u)
     {
@@ -68,7 +76,7 @@ template <> struct Raw8<float> {
     __device__ __forceinline__ void load(const float* p)
     {
         a = __ldg(reinterpret_cast<const float4*>(p));
-        b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+        b = __ldg(reinterpret_cast<const float4*>(p + kGap));
     }
     __device__ __forceinline__ void get(float* x) const
     {
@@ -96,47 +104,62 @@ struct Place {
     float* scale;
 };
 
+// One run's keys (values) of a head, by a warp, or by warp `warp` of the block's
+// (team), which then take a part of the rows each and share their maxima.
 template <typename T, int D, int FORMAT>
-__device__ __forceinline__ void quantise(const Append8Args& a, const T* x, long long stride, const Place& to, const Run& run, int lane,
-                                         unsigned char* buf)
+__device__ __forceinline__ void quantise(const Append8Args& a, const T* x, long long stride, const Place& to, const Run& run, bool team,
+                                         int warp, unsigned char* buf, uint32_t* maxima)
 {
+    using Raw = Raw8<T, D>;
     constexpr int LPR = D / 8, RPW = 32 / LPR;                        // lanes a row, rows a step
-    const int sub = lane / LPR, l = lane % LPR, n = run.n, first = run.first;
-    const bool held = n <= kHeld<T> * RPW;
+    const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR, first = run.first;
+    const int i0 = team ? run.n * warp / kWarps : 0, i1 = team ? run.n * (warp + 1) / kWarps : run.n;
+    const bool held = i1 - i0 <= kHeld<T> * RPW;
     float old = first > 0 && lane == 0 ? *to.scale : 0.f;
-    x += (run.row0 + sub) * stride + l * 8;
+    x += ((long long)run.row0 + i0 + sub) * stride + Raw::first(l);
     const long long step = RPW * stride;
     uint32_t top = 0;
     // a lane reads back what it has copied itself, so nothing but its own copies is waited for
     if (held) {
         const T* p = x;
 #pragma unroll 4
-        for (int i = sub, u = 0; i < n; i += RPW, ++u, p += step) Raw8<T>::copy(paged::saddr(buf), u, p);
+        for (int i = i0 + sub, u = 0; i < i1; i += RPW, ++u, p += step) Raw::copy(paged::saddr(buf), u, p);
         paged::cp_commit();
         paged::cp_wait<0>();
 #pragma unroll 4
-        for (int i = sub, u = 0; i < n; i += RPW, ++u) {
-            Raw8<T> r;
+        for (int i = i0 + sub, u = 0; i < i1; i += RPW, ++u) {
+            Raw r;
             r.held(buf, u);
             top = max(top, r.most());
         }
     } else {
         const T* p = x;
 #pragma unroll 4
-        for (int i = sub; i < n; i += RPW, p += step) {
-            Raw8<T> r;
+        for (int i = i0 + sub; i < i1; i += RPW, p += step) {
+            Raw r;
             r.load(p);
             top = max(top, r.most());
         }
     }
-    top = __reduce_max_sync(0xffffffffu, top);
-    const bool finite = top < Raw8<T>::kInfinite;
+    int turn = 0;
+    auto largest = [&] {
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (team) {
+            if (lane == 0) maxima[turn * kWarps + warp] = top;
+            __syncthreads();
+#pragma unroll
+            for (int x = 0; x < kWarps; ++x) top = max(top, maxima[turn * kWarps + x]);
+            ++turn;
+        }
+    };
+    largest();
+    const bool finite = top < Raw::kInfinite;
     if (!finite) {                                     // the largest finite one
         top = 0;
         const T* p = x;
 #pragma unroll 1
-        for (int i = sub; i < n; i += RPW, p += step) {
-            Raw8<T> r;
+        for (int i = i0 + sub; i < i1; i += RPW, p += step) {
+            Raw r;
             float f[8];
             r.load(p);
             r.get(f);
@@ -146,9 +169,9 @@ __device__ __forceinline__ void quantise(const Append8Args& a, const T* x, long 
                 top = max(top, b < 0x7f800000u ? b : 0u);
             }
         }
-        top = __reduce_max_sync(0xffffffffu, top);
+        largest();
     } else {
-        top = Raw8<T>::wide(top);
+        top = Raw::wide(top);
     }
     const float t = __uint_as_float((uint32_t)max(Code<FORMAT>::exponent(top), 1) << 23);
     old = __shfl_sync(0xffffffffu, old, 0);
@@ -156,12 +179,13 @@ __device__ __forceinline__ void quantise(const Append8Args& a, const T* x, long 
     // 1 / s of a power of two by its exponent
     const uint32_t bits = __float_as_uint(s);
     const float inv = (bits & 0x7fffffu) == 0u && bits < (254u << 23) ? __uint_as_float((254u << 23) - bits) : 1.f / s;
-    if (lane == 0) *to.scale = s;
+    if (lane == 0 && (!team || warp == 0)) *to.scale = s;              // (every warp has read the old one)
     if (first > 0 && s > old) {
         const float ratio = old * inv;                 // s is t here
-        uint8_t* q = to.block + sub * a.p.token_stride + l * 8;
+        const int each = RPW * (team ? kWarps : 1), begin = sub + (team ? warp * RPW : 0);
+        uint8_t* q = to.block + begin * a.p.token_stride + l * 8;
 #pragma unroll 2
-        for (int i = sub; i < first; i += RPW, q += RPW * a.p.token_stride) {
+        for (int i = begin; i < first; i += each, q += each * a.p.token_stride) {
             const uint2 c = *reinterpret_cast<const uint2*>(q);
             float y[8];
             values<FORMAT>(c.x, y);
@@ -169,51 +193,56 @@ __device__ __forceinline__ void quantise(const Append8Args& a, const T* x, long 
             *reinterpret_cast<uint2*>(q) = make_uint2(Code<FORMAT>::pack(y, ratio), Code<FORMAT>::pack(y + 4, ratio));
         }
     }
-    auto put = [&](const Raw8<T>& r, int i) {
-        float y[8];
-        r.get(y);
-        const int token = run.even ? first + i : __ldg(a.slots + run.row0 + i) & ((1 << a.bshift) - 1);
-        *reinterpret_cast<uint2*>(to.block + token * a.p.token_stride + l * 8) =
-            finite ? make_uint2(Code<FORMAT>::pack(y, inv), Code<FORMAT>::pack(y + 4, inv))
-                   : make_uint2(Code<FORMAT>::pack_any(y, inv), Code<FORMAT>::pack_any(y + 4, inv));
+    auto put = [&](uint8_t* q, uint32_t c0, uint32_t c1) {
+        if (Raw::kGap == 4) {
+            *reinterpret_cast<uint2*>(q) = make_uint2(c0, c1);
+        } else {
+            *reinterpret_cast<uint32_t*>(q) = c0;
+            *reinterpret_cast<uint32_t*>(q + Raw::kGap) = c1;
+        }
     };
+    uint8_t* q = to.block + Raw::first(l);
     if (held && finite && run.even) {
-        uint8_t* q = to.block + (first + sub) * a.p.token_stride + l * 8;
+        q += (long long)(first + i0 + sub) * a.p.token_stride;
 #pragma unroll 2
-        for (int i = sub, u = 0; i < n; i += RPW, ++u, q += RPW * a.p.token_stride) {
-            Raw8<T> r;
+        for (int i = i0 + sub, u = 0; i < i1; i += RPW, ++u, q += RPW * a.p.token_stride) {
+            Raw r;
             float y[8];
             r.held(buf, u);
             r.get(y);
-            *reinterpret_cast<uint2*>(q) = make_uint2(Code<FORMAT>::pack(y, inv), Code<FORMAT>::pack(y + 4, inv));
+            put(q, Code<FORMAT>::pack(y, inv), Code<FORMAT>::pack(y + 4, inv));
         }
         return;
     }
     const T* p = x;
 #pragma unroll 2
-    for (int i = sub; i < n; i += RPW, p += step) {
-        Raw8<T> r;
+    for (int i = i0 + sub; i < i1; i += RPW, p += step) {
+        Raw r;
+        float y[8];
         r.load(p);
-        put(r, i);
+        r.get(y);
+        const int token = run.even ? first + i : __ldg(a.slots + run.row0 + i) & ((1 << a.bshift) - 1);
+        put(q + token * a.p.token_stride, finite ? Code<FORMAT>::pack(y, inv) : Code<FORMAT>::pack_any(y, inv),
+            finite ? Code<FORMAT>::pack(y + 4, inv) : Code<FORMAT>::pack_any(y + 4, inv));
     }
 }
 
-// A warp takes `each` rows (at most 31) of one head's keys or values: the runs
-// that begin there.
+// A warp (a block of threads, team) takes `each` rows of one head's keys or
+// values: the runs that begin there.
 template <int D, int FORMAT>
 __global__ void __launch_bounds__(kThreads, 6)
-paged8_append_kernel(const __grid_constant__ Append8Args a, int each)
+paged8_append_kernel(const __grid_constant__ Append8Args a, int each, int team)
 {
-    __shared__ __align__(16) unsigned char smem[kThreads / 32 * kHeldBytes];
+    __shared__ __align__(16) unsigned char smem[kWarps * kHeldBytes];
+    __shared__ uint32_t s_maxima[2][2 * kWarps];                      // of two runs in turn
     pdl_begin();
-    const unsigned int w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), columns = 2u * (unsigned int)a.p.Hkv;
-    const int lane = threadIdx.x & 31, column = (int)(w % columns);
-    const long long r0 = (long long)(w / columns) * each;
-    if (r0 >= a.p.T) return;
-    unsigned char* buf = smem + (threadIdx.x >> 5) * kHeldBytes + lane * 16;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned int w = team ? blockIdx.x : blockIdx.x * kWarps + warp, columns = 2u * (unsigned int)a.p.Hkv;
+    const int column = (int)(w % columns);
+    const long long begin = (long long)(w / columns) * each, end = min((long long)a.p.T, begin + each);
+    unsigned char* buf = smem + warp * kHeldBytes + lane * 16;
     const bool is_v = column >= a.p.Hkv;
     const int head = is_v ? column - a.p.Hkv : column;
-
     const int type = is_v ? a.p.v_dtype : a.p.k_dtype;
     const void* x = is_v ? a.v : a.k;
     const long long stride = is_v ? a.p.v_stride : a.p.k_stride;
@@ -222,36 +251,42 @@ paged8_append_kernel(const __grid_constant__ Append8Args a, int each)
         const int slot = row >= 0 && row < a.p.T ? __ldg(a.slots + row) : -1;
         return slot >= 0 && (slot >> a.bshift) < limit ? slot : -1;
     };
-    // lane l: row r0 - 1 + l, and the 32 after those
-    const int slot = slot_of(r0 - 1 + lane), later = slot_of(r0 + 31 + lane), blk = slot >> a.bshift;
-    const int before = __shfl_up_sync(0xffffffffu, blk, 1);
-    uint32_t leads = __ballot_sync(0xffffffffu, lane >= 1 && lane <= each && blk >= 0 && blk != before);
-    for (; leads; leads &= leads - 1) {
-        const int at = __ffs(leads) - 1, b = __shfl_sync(0xffffffffu, blk, at), s0 = __shfl_sync(0xffffffffu, slot, at);
-        Run run;
-        run.row0 = (int)r0 - 1 + at;
-        uint32_t other = __ballot_sync(0xffffffffu, lane >= at && blk != b);
-        run.n = (other ? __ffs(other) - 1 : 32) - at;
-        const bool mine = lane >= at && lane < at + run.n;
-        int first = mine ? slot : 0x7fffffff;
-        run.even = __all_sync(0xffffffffu, !mine || slot - s0 == lane - at);
-        if (!other)
-            for (int i = run.row0 + run.n, s = later;; i += 32, s = slot_of((long long)i + lane)) {
-                other = __ballot_sync(0xffffffffu, (s >> a.bshift) != b);
-                const int more = other ? __ffs(other) - 1 : 32;
-                if (lane < more) first = min(first, s);
-                run.even = run.even && __all_sync(0xffffffffu, lane >= more || s - s0 == run.n + lane);
-                run.n += more;
-                if (other) break;
+    int runs = 0;
+    for (long long r0 = begin; r0 < end; r0 += kWindow) {
+        // lane l: row r0 - 1 + l, and the 32 after those
+        const int slot = slot_of(r0 - 1 + lane), later = slot_of(r0 + 31 + lane), blk = slot >> a.bshift;
+        const int before = __shfl_up_sync(0xffffffffu, blk, 1);
+        uint32_t leads = __ballot_sync(0xffffffffu, lane >= 1 && r0 - 1 + lane < end && blk >= 0 && blk != before);
+        for (; leads; leads &= leads - 1) {
+            const int at = __ffs(leads) - 1, b = __shfl_sync(0xffffffffu, blk, at), s0 = __shfl_sync(0xffffffffu, slot, at);
+            Run run;
+            run.row0 = (int)r0 - 1 + at;
+            uint32_t other = __ballot_sync(0xffffffffu, lane >= at && blk != b);
+            run.n = (other ? __ffs(other) - 1 : 32) - at;
+            const bool mine = lane >= at && lane < at + run.n;
+            int first = mine ? slot : 0x7fffffff;
+            run.even = __all_sync(0xffffffffu, !mine || slot - s0 == lane - at);
+            if (!other) {
+                int s = later;
+                for (long long i = r0 + 31;; i += 32, s = slot_of(i + lane)) {
+                    other = __ballot_sync(0xffffffffu, (s >> a.bshift) != b);
+                    const int more = other ? __ffs(other) - 1 : 32;
+                    if (lane < more) first = min(first, s);
+                    run.even = run.even && __all_sync(0xffffffffu, lane >= more || s - s0 == run.n + lane);
+                    run.n += more;
+                    if (other) break;
+                }
             }
-        run.first = __reduce_min_sync(0xffffffffu, first) & ((1 << a.bshift) - 1);
-        const int token = (b << a.bshift) & ((1 << a.shift) - 1), page = (b << a.bshift) >> a.shift;
-        Place to;
-        to.block = (is_v ? a.v_pages : a.k_pages) + page * a.p.page_stride + head * a.p.head_stride + token * a.p.token_stride;
-        to.scale = (is_v ? a.v_scales : a.k_scales) + scale_at(page, head, token, a.p.Hkv, a.shift, a.bshift);
-        if (type == FADKV_F32) quantise<float, D, FORMAT>(a, (const float*)x + head * D, stride, to, run, lane, buf);
-        else if (type == FADKV_F16) quantise<__half, D, FORMAT>(a, (const __half*)x + head * D, stride, to, run, lane, buf);
-        else quantise<__nv_bfloat16, D, FORMAT>(a, (const __nv_bfloat16*)x + head * D, stride, to, run, lane, buf);
+            run.first = __reduce_min_sync(0xffffffffu, first) & ((1 << a.bshift) - 1);
+            const int token = (b << a.bshift) & ((1 << a.shift) - 1), page = (b << a.bshift) >> a.shift;
+            Place to;
+            to.block = (is_v ? a.v_pages : a.k_pages) + page * a.p.page_stride + head * a.p.head_stride + token * a.p.token_stride;
+            to.scale = (is_v ? a.v_scales : a.k_scales) + scale_at(page, head, token, a.p.Hkv, a.shift, a.bshift);
+            uint32_t* maxima = s_maxima[runs++ & 1];
+            if (type == FADKV_F32) quantise<float, D, FORMAT>(a, (const float*)x + head * D, stride, to, run, team, warp, buf, maxima);
+            else if (type == FADKV_F16) quantise<__half, D, FORMAT>(a, (const __half*)x + head * D, stride, to, run, team, warp, buf, maxima);
+            else quantise<__nv_bfloat16, D, FORMAT>(a, (const __nv_bfloat16*)x + head * D, stride, to, run, team, warp, buf, maxima);
+        }
     }
 }
 
@@ -259,12 +294,17 @@ template <int D, int FORMAT>
 cudaError_t launch_t(const Append8Args& a, cudaStream_t st)
 {
     const long long columns = 2ll * a.p.Hkv;
-    const long long want = a.p.T * columns / (152 * 24);
-    const int each = (int)std::max(1ll, std::min(want, a.p.block > 16 ? 31ll : 16ll));
-    const long long warps = (a.p.T + each - 1) / each * columns;
+    // A block of tokens that does not fit a warp's buffer is four warps' work (24000 tokens of 8 heads of 128 in blocks of 128, in
+    // 16 bits: KKK us, 68 a warp a block), where there are rows for whole ones.
+    const int size = a.p.k_dtype == FADKV_F32 || a.p.v_dtype == FADKV_F32 ? 4 : 2;
+    const int team = a.p.block * D * size > kHeldBytes && a.p.T > kWindow;
+    // Rows a warp (a team) looks for runs in: about a block, less where there are fewer rows than warps to be busy.
+    const long long want = a.p.T * columns / (152 * (team ? 6 : 24)), most = a.p.block <= 16 ? 16 : (a.p.block + 31) / 32 * kWindow;
+    const int each = (int)std::max(1ll, std::min(want, most));
+    const long long warps = (a.p.T + each - 1) / each * columns * (team ? kWarps : 1);
     if (warps > 0x7fffffffll) return cudaErrorInvalidValue;
     const unsigned grid = (unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32));
-    return launch_pdl(paged8_append_kernel<D, FORMAT>, dim3(grid), dim3(kThreads), 0, st, a, each);
+    return launch_pdl(paged8_append_kernel<D, FORMAT>, dim3(grid), dim3(kThreads), 0, st, a, each, team);
 }
 
 }  // namespace
