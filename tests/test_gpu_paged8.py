@@ -77,6 +77,7 @@ APPENDS = [
     ([11] * 40, [1] * 40, 4, 64, "bf16", "bf16", "i8", 16, 16, "token"),
     ([0, 9, 60], [900, 400, 700], 8, 128, "bf16", "f16", "e4m3", 32, 16, "head"),    # ranges of 16 rows a warp
     ([2, 0, 5], [2000, 3, 500], 4, 64, "f32", "f16", "i8", 64, 64, "head"),
+    ([30, 0], [3000, 700], 1, 128, "f16", "f32", "e4m3", 512, 256, "token"),         # four warps a block of tokens
 ]
 
 
@@ -153,6 +154,33 @@ def test_append_odd_values(fmt, dt):
         _append(x, x, _i32(slots), pools, "head")
         for got, want in zip(pools, codes):
             assert np.array_equal(V.decode(_codes(got, "head"), fmt), V.decode(want, fmt), equal_nan=True)
+        for got, want in zip(pools[2:], scales):
+            assert np.array_equal(got.cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("ps,block,d,dt", [(32, 32, 64, "f16"), (128, 128, 128, "bf16"), (256, 64, 128, "f32")])
+def test_append_in_any_order_within_a_block(ps, block, d, dt):
+    """Rows of one block in any order, some with values that are not finite (in a large block too)."""
+    rng = np.random.default_rng(block)
+    hkv, before, new, fmt = 2, [7, 40], [5 * block + 3, 60], "e4m3"
+    table, P = _tables(rng, [a + b for a, b in zip(before, new)], ps)
+    slots = np.array(_slots(table, before, new, ps))
+    blk = slots // block
+    cuts = [0] + (np.flatnonzero(blk[1:] != blk[:-1]) + 1).tolist() + [len(slots)]
+    for a, b in zip(cuts, cuts[1:]):
+        slots[a:b] = rng.permutation(slots[a:b])
+    x = torch.from_numpy(rng.standard_normal((len(slots), hkv, d)) * 3).to(TYPES[dt]).to(DEV)
+    x[block + 5, 1, 3], x[2 * block + 9, 0, 0], x[2 * block + 9, 0, d - 1] = float("nan"), float("inf"), float("-inf")
+    x[cuts[2]:cuts[3], 1] = float("inf")                # nothing finite in a whole block
+    for f in (fmt, "i8"):
+        codes = [_random_codes(rng, (P, ps, hkv, d), f) for _ in range(2)]
+        scales = [(2.0 ** rng.integers(-12, -3, (P, hkv, ps // block))).astype(np.float32) for _ in range(2)]
+        pools = [_to_pool(c, "head", f) for c in codes] + [torch.from_numpy(s.copy()).to(DEV) for s in scales]
+        for c, s in zip(codes, scales):
+            V.append(_np(x), slots.tolist(), c, s, ps, block, f)
+        _append(x, x, _i32(slots), pools, "head")
+        for got, want in zip(pools, codes):
+            assert np.array_equal(V.decode(_codes(got, "head"), f), V.decode(want, f), equal_nan=True)
         for got, want in zip(pools[2:], scales):
             assert np.array_equal(got.cpu().numpy(), want)
 
@@ -416,6 +444,25 @@ def test_attend_queries_of_any_size(dt):
         out, lse = _attend(q, pools, "token", table, [n] * 6, scale=scale)
         _check_attend((out[rows], lse[rows]), want, n, d, TYPES[dt])
         assert out[4:].isnan().all()
+
+
+@pytest.mark.parametrize("Hq", [4, 8, 16])
+def test_attend_small_codes(Hq):
+    """I8 codes of -2 .. 2 beside one large one a block: the keys enter the product as code + 128, so their sums are rounded at
+    that size: 2^-23 of sum |q| (|code| + 128) for each of the product's d / 16 steps and the sums of q, twice."""
+    rng = np.random.default_rng(13)
+    d, ps, n = 128, 16, 333
+    table, P = _tables(rng, [n], ps)
+    codes = [rng.integers(-2, 3, (P, ps, 1, d)).astype(np.int8) for _ in range(2)]
+    codes[0][:, 3, :, 7] = 127
+    codes = [c.view(np.uint8) for c in codes]
+    scales = [np.full((P, 1, 1), 0.25, np.float32), np.full((P, 1, 1), 2.0 ** -6, np.float32)]
+    q = torch.from_numpy(rng.standard_normal((1, Hq, d))).half().to(DEV)
+    pools = [_to_pool(c, "head", "i8") for c in codes] + [torch.from_numpy(s).to(DEV) for s in scales]
+    want = V.attend(_np(q), codes[0], codes[1], scales[0], scales[1], table, [n], 0, 0, d ** -0.5, "i8")
+    most = (np.abs(_np(q)) * (127 + 128)).sum(-1) * 0.25 * d ** -0.5
+    want[3] = want[3] + most * 2 * (d / 16 + d + 8) / (d + 8)   # (bounds() multiplies by (d + 8) 2^-23)
+    _check_attend(_attend(q, pools, "head", table, [n]), want, n, d, torch.float16)
 
 
 def test_attend_repeats_bit_for_bit_and_shares_a_workspace():
