@@ -9,10 +9,15 @@
 //
 // The new rows have to be read once and the codes written once: HBM for
 // prompts, latency for single tokens.  A warp takes one (block, head, keys or
-// values): its rows (up to 16 of 128 elements) stay in registers between the
-// maximum and the rounding, longer runs are read a second time, from L2.  The
-// runs of rows that share a block are found by the warps themselves, from the
-// slots: the warp whose rows a run begins in takes it.
+// values), and its rows wait in shared memory between the maximum and the
+// rounding (8 KB a warp, 24 warps a multiprocessor: enough in flight, and
+// few registers; kept in registers 28 us, read a second time from L2 35, for
+// the first case below); blocks too large for that are four warps' work.
+// The runs of rows that share a block are found by the warps themselves, from
+// the slots: the warp whose rows a run begins in takes it.  What is not finite is
+// looked at only where the maximum says so.  Three prompts of up to 8000 tokens
+// of 8 heads of 128, bfloat16 to I8: 22.0 us, 5.8 TB/s; 16 single tokens 2.1 us,
+// of which a launch is most.
 #include <algorithm>
 
 #include "paged8.cuh"
@@ -295,7 +300,7 @@ cudaError_t launch_t(const Append8Args& a, cudaStream_t st)
 {
     const long long columns = 2ll * a.p.Hkv;
     // A block of tokens that does not fit a warp's buffer is four warps' work (24000 tokens of 8 heads of 128 in blocks of 128, in
-    // 16 bits: KKK us, 68 a warp a block), where there are rows for whole ones.
+    // 16 bits: 29 us, 68 a warp a block), where there are rows for whole ones.
     const int size = a.p.k_dtype == FADKV_F32 || a.p.v_dtype == FADKV_F32 ? 4 : 2;
     const int team = a.p.block * D * size > kHeldBytes && a.p.T > kWindow;
     // Rows a warp (a team) looks for runs in: about a block, less where there are fewer rows than warps to be busy.

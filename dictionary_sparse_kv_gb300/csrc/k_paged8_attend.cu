@@ -18,14 +18,30 @@
 // or that the rows of the sums follow (values), so that two conversions and, for
 // the values, one byte permutation give two registers of a fragment.  Scales
 // enter behind the products, one of each kind for a 16-token tile, which lies in
-// one block.
+// one block of tokens.  The weights enter as two binary16 terms; up to four heads
+// leave half of a product's eight columns idle, which then take the second
+// terms (16 products a tile in place of 24).  Pages, places and scales are looked
+// up for 32 tiles at a time, a lane each.
 //
-// The work is cut as in the 16-bit kernel: one list of 64-token blocks, request
-// by request and KV head by KV head, an even share a CTA, or equal parts where
-// the lengths are about even; pieces go to the workspace and the CTA that
-// arrives last joins them in their order.  Blocks lie at multiples of 64 tokens
-// (a window's first one is partly seen), so that a tile is one page, one block
-// of scales and one run of bytes.
+// The work is one list of 64-token blocks, request by request and KV head by
+// KV head.  Blocks lie at multiples of 64 tokens (a window's first one is partly
+// seen), so that a warp's tile is one page, one block of scales and one run of
+// bytes.  Mostly a CTA takes one piece of one (request, KV head), of equal parts
+// no longer than they have to be, and joins where its tiles were; where there
+// are more (request, heads) than CTAs, an even share of the list.  Pieces go to
+// the workspace and the CTA that arrives last joins them in their order, so the
+// result does not depend on which one that was.
+//
+// 64 requests of up to 16384 tokens, 32 heads over 8 of 128: 166 us, 6.6 TB/s
+// (I8 the same; d = 64 5.9 TB/s, instructions; 16 heads a KV head 3.8 TB/s,
+// instruction latency).  16 of up to 4096 18.8 us: 2 until the lengths are cut, 3
+// until every warp has codes, 8 of codes at 6 TB/s, 3 of joins, and pieces that
+// end apart.  One of 777 tokens 7.1 us: the chain lengths -> table -> codes 2.3,
+// the joins 3.5.  Tiles by TMA, one box each of keys and values: 183 us where
+// this took 184 (an instruction count of three quarters did not show), and half
+// a microsecond more before the first tile.
+#include <algorithm>
+
 #include "paged8.cuh"
 
 namespace fadkv {
@@ -44,20 +60,22 @@ constexpr float kUp = 11.f;                        // 15 - kGrow: w is multiplie
 constexpr int kExtra = 3;                          // units that a piece costs beside its blocks
 constexpr int kSms = 152;
 
-// ONE: every CTA takes one piece, and joins where its tiles were.
-template <int D, bool ONE> struct Cfg {
-    static constexpr int PER_SM = D == 128 ? 3 : 4;
-    static constexpr int STAGES = D == 128 ? (ONE ? 4 : 3) : (ONE ? 6 : 4);
-    static constexpr int CTAS = PER_SM * kSms;
+// ONE: a CTA takes one piece, and joins where its tiles were.  WIDE: sixteen
+// heads a piece, whose sums want the registers of fewer CTAs.  (us, 16 requests of
+// up to 4096 tokens of 8 heads of 128, 113 of 1024 of two of 64: 18.8 and 15.7,
+// with a stage or two more 19.5 and 16.2; 64 of up to 16384 of eight of 64: 92, a
+// stage more 95; 64 of up to 32000 with 16 heads over one of 128: 62, with three
+// CTAs 71.)
+template <int D, bool ONE, bool WIDE> struct Cfg {
+    static constexpr int PER_SM = D == 128 ? (WIDE ? 2 : 3) : (WIDE ? 3 : 4);
+    static constexpr int STAGES = ONE && D == 64 ? 4 : 3;
     static constexpr int TILE_BYTES = kTile * D;
     static constexpr int WARP_BYTES = STAGES * 2 * TILE_BYTES;
     static constexpr int ROW = D + 8;                                  // floats of a result: d values, m, l; padding
     static constexpr int JOIN_BYTES = ONE ? kWarps * WARP_BYTES : D == 128 ? 24576 : 16384;   // results that are joined
     static constexpr int SMEM = kWarps * WARP_BYTES + (ONE ? 0 : JOIN_BYTES);
-    static_assert(kWarps * WARP_BYTES >= JOIN_BYTES, "join");
 };
-template <int D> constexpr int kCtas = Cfg<D, true>::CTAS;
-static_assert(kCtas<64> == Cfg<64, false>::CTAS && kCtas<128> == Cfg<128, false>::CTAS, "grid");
+template <int D, bool WIDE = false> constexpr int kCtas = Cfg<D, true, WIDE>::PER_SM * kSms;
 
 // Pieces that one CTA joins: more are joined in groups, as in the 16-bit kernel.
 constexpr int kAtOnce = 32, kGroup = 16;
@@ -65,8 +83,9 @@ constexpr int kCounters = 1024;
 static_assert(kCtas<64> <= kCounters && kCtas<128> <= kCounters, "counters");
 static_assert(3 * kCounters * sizeof(int) <= kHeadBytes - kDecodeHead, "workspace head");
 
-template <int D> constexpr bool kJoins = Cfg<D, false>::JOIN_BYTES >= (kAtOnce > 8 * kWarps ? kAtOnce : 8 * kWarps) * Cfg<D, false>::ROW * 4;
-static_assert(kJoins<64> && kJoins<128>, "join");
+template <int D> constexpr int kLeastJoin = (kAtOnce > 8 * kWarps ? kAtOnce : 8 * kWarps) * (D + 8) * 4;
+static_assert(Cfg<64, true, false>::JOIN_BYTES >= kLeastJoin<64> && Cfg<64, false, false>::JOIN_BYTES >= kLeastJoin<64> &&
+              Cfg<128, true, false>::JOIN_BYTES >= kLeastJoin<128> && Cfg<128, false, false>::JOIN_BYTES >= kLeastJoin<128>, "join");
 
 // A piece in the workspace: a row for each of its heads.
 __host__ __device__ constexpr size_t piece_floats(int d) { return (size_t)kMaxHeads * (d + 8); }
@@ -115,12 +134,12 @@ struct Work {
 // TILES of eight heads; 0: four heads, twice, for the two terms of their
 // weights, which one product then takes together.
 template <typename T, int D, int TILES, int FORMAT, bool ONE>
-__global__ void __launch_bounds__(kThreads, Cfg<D, ONE>::PER_SM)
+__global__ void __launch_bounds__(kThreads, Cfg<D, ONE, TILES == 2>::PER_SM)
 paged8_attend_kernel(const __grid_constant__ Paged8Args a)
 {
     constexpr bool TWO = TILES == 0;
     constexpr int NT = TWO ? 1 : TILES;
-    using C_ = Cfg<D, ONE>;
+    using C_ = Cfg<D, ONE, TILES == 2>;
     constexpr int STAGES = C_::STAGES, CPR = D / 16;                   // 16-byte chunks per row
     constexpr int KS = D / 16, ROW = C_::ROW;                          // 16-element steps; floats of a result
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -725,7 +744,7 @@ template <typename T, int D, int TILES, int FORMAT, bool ONE>
 cudaError_t launch_one(const Paged8Args& a, int grid, cudaStream_t st)
 {
     auto k = paged8_attend_kernel<T, D, TILES, FORMAT, ONE>;
-    const int smem = Cfg<D, ONE>::SMEM;
+    const int smem = Cfg<D, ONE, TILES == 2>::SMEM;
     const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(k, dim3((unsigned)grid), dim3(kThreads), smem, st, a);
@@ -740,7 +759,7 @@ cudaError_t launch_nt(const Paged8Args& a, cudaStream_t st)
     if (a.p.window > 0) most = most < (long long)a.p.window + a.p.sinks ? most : (long long)a.p.window + a.p.sinks;
     const long long sets = (long long)a.p.B * a.p.Hkv * ((a.grp + 8 * NT - 1) / (8 * NT));
     const long long units = ((most + kBlock - 1) / kBlock + 2) * sets;
-    const int grid = (int)(units < kCtas<D> ? units : kCtas<D>);
+    const int grid = (int)std::min(units, (long long)kCtas<D, TILES == 2>);
     // A piece a CTA, or even shares: where the (request, heads) are between half of the CTAs and all of them, few can be cut, and
     // long ones leave many CTAs waiting (us, requests of 24 heads over 8 of 128, in pieces and in shares: 40 of 300 tokens 10.0 and
     // 13.3, of 1500 27.1 and 27.2, of 6000 83 and 80; of up to 6000 51 and 45; 56 of up to 6000 77 and 61).  What the tables have

@@ -4,7 +4,11 @@
 // Codes are read and vectors written once: HBM.  The work is one list of
 // 16-token tiles, request by request, tile by tile and head by head; every CTA
 // takes an even contiguous share, its warps every fourth tile of it, keys and
-// values together (all their loads in flight at once).
+// values together.  A warp has the next tile's codes on their way while it
+// stores one, and has looked up the place of the one behind it.  8 requests of
+// up to 4096 tokens of 8 heads of 128 to binary16: 25 us, 5.3 TB/s (3 us of them
+// until the first codes arrive); 113 times the last 1024 tokens of two heads of
+// 64: 17.4 us (one tile in flight a warp: 18.8).
 #include "paged8.cuh"
 
 namespace fadkv {
