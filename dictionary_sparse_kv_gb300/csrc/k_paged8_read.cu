@@ -112,14 +112,46 @@ paged8_read_kernel(const __grid_constant__ Read8Args a)
     };
     const int sub = lane / LPR, l = lane % LPR;
     struct Codes { uint2 c[2][STEPS]; };
+    const long long from_step = RPW * a.p.token_stride, to_step = RPW * a.p.out_token_stride;
     auto load = [&](const Tile& t, Codes& x) {
-        const long long from = t.page * a.p.page_stride + t.head * a.p.head_stride + t.at * a.p.token_stride + l * 8;
+        if (t.page < 0) return;
+        const long long from = t.page * a.p.page_stride + t.head * a.p.head_stride + (t.at + sub) * a.p.token_stride + l * 8;
+        const uint8_t *k = a.k_pages + from, *v = a.v_pages + from;
+        if (t.lo <= 0 && t.hi >= kTile) {
 #pragma unroll
-        for (int j = 0; j < STEPS; ++j) {
-            const int i = j * RPW + sub;
-            const bool live = t.page >= 0 && i >= t.lo && i < t.hi;
-            x.c[0][j] = live ? __ldg(reinterpret_cast<const uint2*>(a.k_pages + from + i * a.p.token_stride)) : make_uint2(0u, 0u);
-            x.c[1][j] = live ? __ldg(reinterpret_cast<const uint2*>(a.v_pages + from + i * a.p.token_stride)) : make_uint2(0u, 0u);
+            for (int j = 0; j < STEPS; ++j, k += from_step, v += from_step) {
+                x.c[0][j] = __ldg(reinterpret_cast<const uint2*>(k));
+                x.c[1][j] = __ldg(reinterpret_cast<const uint2*>(v));
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < STEPS; ++j, k += from_step, v += from_step) {
+                const int i = j * RPW + sub;
+                const bool live = i >= t.lo && i < t.hi;
+                x.c[0][j] = live ? __ldg(reinterpret_cast<const uint2*>(k)) : make_uint2(0u, 0u);
+                x.c[1][j] = live ? __ldg(reinterpret_cast<const uint2*>(v)) : make_uint2(0u, 0u);
+            }
+        }
+    };
+    auto store = [&](const Tile& t, const Codes& x) {
+        if (t.page < 0) return;
+        const long long dst = t.to * a.p.out_page_stride + t.head * a.p.out_head_stride + (t.at + sub) * a.p.out_token_stride + l * 8;
+        const bool full = t.lo <= 0 && t.hi >= kTile;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            T* out = (T*)(kv ? a.v_out : a.k_out) + dst;
+            const float s = kv ? t.vs : t.ks;
+#pragma unroll
+            for (int j = 0; j < STEPS; ++j, out += to_step) {
+                const uint2 c = x.c[kv][j];
+                if (!full && (j * RPW + sub < t.lo || j * RPW + sub >= t.hi)) continue;
+                float y[8];
+                values<FORMAT>(c.x, y);
+                values<FORMAT>(c.y, y + 4);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] *= s;
+                store8(out, y);
+            }
         }
     };
     // a tile's codes are on their way while the one before it is stored, and the place of the one behind it is looked up
@@ -131,22 +163,7 @@ paged8_read_kernel(const __grid_constant__ Read8Args a)
     for (; u < u1; u += kWarps) {
         load(next, ahead);
         const Tile after = locate(u + 2 * kWarps);
-        if (t.page >= 0) {
-            const long long dst = t.to * a.p.out_page_stride + t.head * a.p.out_head_stride + t.at * a.p.out_token_stride + l * 8;
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-                for (int j = 0; j < STEPS; ++j) {
-                    const int i = j * RPW + sub;
-                    if (i < t.lo || i >= t.hi) continue;
-                    float y[8];
-                    values<FORMAT>(now.c[kv][j].x, y);
-                    values<FORMAT>(now.c[kv][j].y, y + 4);
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) y[x] *= kv ? t.vs : t.ks;
-                    store8((T*)(kv ? a.v_out : a.k_out) + dst + i * a.p.out_token_stride, y);
-                }
-        }
+        store(t, now);
         now = ahead;
         t = next;
         next = after;
