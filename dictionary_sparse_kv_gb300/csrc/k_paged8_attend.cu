@@ -660,7 +660,10 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
                 v += __shfl_xor_sync(0xffffffffu, v, 4);
                 v += __shfl_xor_sync(0xffffffffu, v, 8);
                 v += __shfl_xor_sync(0xffffffffu, v, 16);
-                const float f = v == 0.f ? 0.f : __fdividef(exp2_fast(Mg[n][i] == -INFINITY ? 0.f : Mr[n][i] - mr[n][i] - kUp), v);
+                // 2^(M - m) / l; for values so small that it is no number of the normal range, in two steps
+                const float e = Mg[n][i] == -INFINITY ? 0.f : Mr[n][i] - mr[n][i] - kUp;
+                const float f = v == 0.f ? 0.f : __fdividef(exp2_fast(e < -64.f ? e + 64.f : e), v);
+                const float g = e < -64.f ? 0x1p-64f : 1.f;
                 float* r = rows + (warp * 8 + 2 * (lane & 3) + i) * ROW;       // (f is 0 where nothing was seen)
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
@@ -669,7 +672,7 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
                         y.x += __shfl_xor_sync(0xffffffffu, y.x, 2);
                         y.y += __shfl_xor_sync(0xffffffffu, y.y, 2);
                     }
-                    *reinterpret_cast<float2*>(r + k * 16 + (lane >> 2) * 2) = make_float2(y.x * f, y.y * f);
+                    *reinterpret_cast<float2*>(r + k * 16 + (lane >> 2) * 2) = make_float2(y.x * f * g, y.y * f * g);
                 }
                 if (lane < 4) *reinterpret_cast<float2*>(r + D) = make_float2(mg[n][i] == -INFINITY ? -INFINITY : mr[n][i], v);
             }

@@ -87,7 +87,7 @@ def gather(pool, scales, row, length, fmt):
     return out, sc, ok
 
 
-def bounds(out, lse, pv, big, n, most, d, eps):
+def bounds(out, lse, pv, big, n, most, d, eps, least=2.0 ** -24):
     """Largest errors of out and lse that rounding allows.  As paged_util.bounds with 32-bit scores (their error is 2^-23 of
     `big` for each of d products, and eight more for the scales), and:
       - exponents are differences x - m, x + log2 sv - M and M - m, each rounded in 32 bits: 2^-24 of (1.45 big + 140) three
@@ -95,10 +95,10 @@ def bounds(out, lse, pv, big, n, most, d, eps):
       - the weights enter as two binary16 terms: 2^-22 of each; one that is below 2^-36 of the largest is lost, for each of n
         keys that much of the largest weight times value, `most`;
       - exponentials, sums and the joins' weights: 2^-19 of the sum.
-    out is rounded once."""
+    out is rounded once, to multiples of `least` at the low end (half of one; binary16's by default, with as much again)."""
     delta = (d + 8) * 2.0 ** -23 * big + 3 * 2.0 ** -24 * (1.45 * big + 140) + 2.0 ** -21
     rel = 2 * delta[..., None] + 2.0 ** -19 + 2.0 ** -22
-    e_out = eps / 2 * np.abs(out) * (1 + rel) + 2 * rel * pv + n * 2.0 ** -36 * most[..., None] + 2.0 ** -24
+    e_out = eps / 2 * np.abs(out) * (1 + rel) + 2 * rel * pv + n * 2.0 ** -36 * most[..., None] + least
     e_lse = 2 * delta + 2.0 ** -19 + np.where(np.isfinite(lse), np.abs(lse), 0) * 2.0 ** -22
     return e_out, e_lse
 

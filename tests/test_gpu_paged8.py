@@ -78,6 +78,8 @@ APPENDS = [
     ([0, 9, 60], [900, 400, 700], 8, 128, "bf16", "f16", "e4m3", 32, 16, "head"),    # ranges of 16 rows a warp
     ([2, 0, 5], [2000, 3, 500], 4, 64, "f32", "f16", "i8", 64, 64, "head"),
     ([30, 0], [3000, 700], 1, 128, "f16", "f32", "e4m3", 512, 256, "token"),         # four warps a block of tokens
+    ([40, 0], [14500, 900], 8, 64, "f16", "bf16", "i8", 64, 64, "head"),             # more rows a warp than it has lanes
+    ([3, 0], [7500, 300], 8, 128, "f16", "f16", "e4m3", 128, 128, "token"),          # the same, four warps a block
 ]
 
 
@@ -360,6 +362,21 @@ def test_attend_blocks_of_very_different_size():
     want[4][:] = 2.0 ** -12 * 448                       # the largest weight times value: e^-60 2^20 is far below
     got = _attend(q, pools, "head", table, [n])
     _check_attend(got, want, n, d, torch.float16)
+
+
+@pytest.mark.parametrize("power", [-126, -110, 100, 112])
+def test_attend_values_near_the_ends_of_their_range(power):
+    """Scales of the values near 2^-126 and 2^112: bfloat16 holds the result, and the references' difference is as large."""
+    rng = np.random.default_rng(14)
+    lens, d, ps = [40, 300, 1500], 128, 16
+    table, P, codes, scales = _attend_state(rng, lens, 1, d, "e4m3", ps, 16, "head")
+    scales[1][:] = 2.0 ** (power + rng.integers(0, 3, scales[1].shape))
+    q = torch.from_numpy(rng.standard_normal((3, 3, d))).bfloat16().to(DEV)
+    pools = [_to_pool(c, "head", "e4m3") for c in codes] + [torch.from_numpy(s).to(DEV) for s in scales]
+    want = V.attend(_np(q), codes[0], codes[1], scales[0], scales[1], table, lens, 0, 0, d ** -0.5, "e4m3")
+    out, lse = _attend(q, pools, "head", table, lens)
+    e_out, _ = V.bounds(*want[:4], 1500, want[4], d, 2.0 ** -7, least=2.0 ** -133)    # bfloat16's smallest step
+    assert (np.abs(_np(out) - want[0]) <= e_out).all(), (np.abs(_np(out) - want[0]) / e_out).max()
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "i8"])
