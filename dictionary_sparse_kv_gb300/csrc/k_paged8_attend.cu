@@ -103,16 +103,6 @@ __device__ __forceinline__ void cp16_all(uint32_t dst, const void* src)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-__device__ __forceinline__ int add_acq_rel(int* p, int v)
-{
-    int old;
-    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
-    return old;
-}
-
-// Bits 0 .. n-1 set (none for n <= 0, all for n >= 32).
-__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
-
 // The tokens that the query at position len - 1 sees, the first `first` ones
 // and those from `from` on, as a list of 64-token blocks: `sinks` ones from
 // token 0 on, then those from block `from_block` on; `count` in all.

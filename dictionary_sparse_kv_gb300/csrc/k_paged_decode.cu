@@ -90,13 +90,6 @@ struct Work {
     Seen seen;
 };
 
-__device__ __forceinline__ int add_acq_rel(int* p, int v)
-{
-    int old;
-    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
-    return old;
-}
-
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kDecThreads, dec_ctas(D) / 152)
 paged_decode_kernel(const __grid_constant__ PagedArgs a)

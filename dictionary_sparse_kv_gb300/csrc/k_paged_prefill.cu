@@ -230,9 +230,6 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return r;
 }
 
-// Bits 0 .. n-1 set (none for n <= 0, all for n >= 32).
-__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
-
 // The key tiles of an item: those of the window (or all), then those of the
 // first tokens, whose few keys would set a maximum that the next tile exceeds.
 struct Tiles {

@@ -190,6 +190,16 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     return r;
 }
 
+// Bits 0 .. n-1 set (none for n <= 0, all for n >= 32).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; }
+
+__device__ __forceinline__ int add_acq_rel(int* p, int v)
+{
+    int old;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
+    return old;
+}
+
 // Byte offset of 16-byte chunk c of row r in a tile of ROW-byte rows whose
 // chunks are swapped by row, so that eight rows at one chunk lie in eight
 // different bank groups.
