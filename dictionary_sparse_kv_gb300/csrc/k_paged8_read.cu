@@ -22,21 +22,29 @@ constexpr int kTile = 16;
 // CTAs a multiprocessor: what the registers of two tiles in flight allow.
 template <int D> constexpr int kPerSm = D == 128 ? 4 : 6;
 
+// SECTORS: the output pools lie on multiples of 32 bytes (the launcher looks), and so does every row of them, whose strides are
+// multiples of 32 bytes.
+template <bool SECTORS>
 __device__ __forceinline__ void store8(float* p, const float* y)
 {
-    // (32 bytes a lane in one instruction: a sector is written whole)
-    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]),
-                 "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7])
-                 : "memory");
+    if (SECTORS) {
+        // (32 bytes a lane in one instruction: a sector is written whole)
+        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]),
+                     "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<float4*>(p)[0] = make_float4(y[0], y[1], y[2], y[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(y[4], y[5], y[6], y[7]);
+    }
 }
-template <typename T>
+template <bool SECTORS, typename T>
 __device__ __forceinline__ void store8(T* p, const float* y)
 {
     *reinterpret_cast<uint4*>(p) = make_uint4(Num<T>::pack(y[0], y[1]), Num<T>::pack(y[2], y[3]), Num<T>::pack(y[4], y[5]),
                                               Num<T>::pack(y[6], y[7]));
 }
 
-template <typename T, int D, int FORMAT>
+template <typename T, int D, int FORMAT, bool SECTORS>
 __global__ void __launch_bounds__(kThreads, kPerSm<D>)
 paged8_read_kernel(const __grid_constant__ Read8Args a)
 {
@@ -150,7 +158,7 @@ paged8_read_kernel(const __grid_constant__ Read8Args a)
                 values<FORMAT>(c.y, y + 4);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) y[i] *= s;
-                store8(out, y);
+                store8<SECTORS>(out, y);
             }
         }
     };
@@ -170,21 +178,21 @@ paged8_read_kernel(const __grid_constant__ Read8Args a)
     }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool SECTORS>
 cudaError_t launch_t(const Read8Args& a, cudaStream_t st)
 {
     // an upper bound of the tiles: lengths are known on the device only
     const long long tiles = (((long long)a.p.max_pages << a.shift) / kTile) * a.p.B * a.p.Hkv;
     const long long ctas = 152 * kPerSm<D>;
     const unsigned grid = (unsigned)(tiles < ctas ? tiles : ctas);
-    return launch_pdl(a.p.format == FADKV_E4M3 ? paged8_read_kernel<T, D, FADKV_E4M3> : paged8_read_kernel<T, D, FADKV_I8>, dim3(grid),
-                      dim3(kThreads), 0, st, a);
+    return launch_pdl(a.p.format == FADKV_E4M3 ? paged8_read_kernel<T, D, FADKV_E4M3, SECTORS> : paged8_read_kernel<T, D, FADKV_I8, SECTORS>,
+                      dim3(grid), dim3(kThreads), 0, st, a);
 }
 
-template <typename T>
+template <typename T, bool SECTORS = false>
 cudaError_t launch_d(const Read8Args& a, cudaStream_t st)
 {
-    return a.p.d == 128 ? launch_t<T, 128>(a, st) : launch_t<T, 64>(a, st);
+    return a.p.d == 128 ? launch_t<T, 128, SECTORS>(a, st) : launch_t<T, 64, SECTORS>(a, st);
 }
 
 }  // namespace
@@ -192,7 +200,11 @@ cudaError_t launch_d(const Read8Args& a, cudaStream_t st)
 cudaError_t launch_paged8_read(const Read8Args& a, cudaStream_t st)
 {
     if (a.p.B <= 0 || a.p.num_pages <= 0 || a.p.out_pages <= 0) return cudaSuccess;
-    if (a.p.out_dtype == FADKV_F32) return launch_d<float>(a, st);
+    if (a.p.out_dtype == FADKV_F32) {
+        // 32-bit pools may lie 16 bytes off a sector
+        const bool sectors = (((uintptr_t)a.k_out | (uintptr_t)a.v_out) & 31u) == 0;
+        return sectors ? launch_d<float, true>(a, st) : launch_d<float>(a, st);
+    }
     if (a.p.out_dtype == FADKV_F16) return launch_d<__half>(a, st);
     return launch_d<__nv_bfloat16>(a, st);
 }
