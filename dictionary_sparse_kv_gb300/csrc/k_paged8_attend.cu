@@ -164,6 +164,7 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
     // each as keep its pieces at `most` blocks or fewer, the least that the grid has room for.  Where they are more, the
     // list is cut into even shares, each (request, heads) kExtra units longer than its blocks, which is what a piece costs.
     int cur_b, parts = 1, part = 0, seg = 0;                           // one: this CTA's piece
+    int C = 1;                                                         // shares: how many, no more than units, so that none is empty
     long long u = 0, u1 = 1, U = 0, base = 0;                          // shares: this CTA's units; all; the first of request cur_b
     // Each thread has the requests b0 .. b1-1: a lane each, the same in every warp, for up to 32; else over the block.
     const bool few = B <= 32;
@@ -268,8 +269,10 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
         } else {
             from = block_scan<kThreads>(mine, &U);
         }
-        u = U * blockIdx.x / grid;
-        u1 = U * (blockIdx.x + 1) / grid;
+        C = (int)min((long long)grid, U);
+        if ((int)blockIdx.x >= C) return;
+        u = U * blockIdx.x / C;
+        u1 = U * (blockIdx.x + 1) / C;
         if (few) {
             cur_b = __ffs(__ballot_sync(0xffffffffu, from + mine > u)) - 1;
             base = __shfl_sync(0xffffffffu, from, cur_b);
@@ -671,14 +674,14 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
             __syncthreads();                            // the rows are written again
         }
         if (!whole) {
-            // the CTAs that have its pieces; of shares, unit x is in share ((x + 1) grid - 1) / U
+            // the CTAs that have its pieces; of shares, unit x is in share ((x + 1) C - 1) / U
             int c0, c1;
             if (ONE) {
                 c0 = (int)blockIdx.x - part;
                 c1 = c0 + parts - 1;
             } else {
-                c0 = (int)(((done.unit0 + 1) * grid - 1) / U);
-                c1 = (int)(((done.unit0 + done.nb) * grid - 1) / U);
+                c0 = (int)(((done.unit0 + 1) * C - 1) / U);
+                c1 = (int)(((done.unit0 + done.nb) * C - 1) / U);
             }
             // whether this CTA is the last of n at a counter; the counter is back at zero then
             auto last_at = [&](int index, int n) {

@@ -1,10 +1,10 @@
 """The 8-bit paged cache and the prompts' attention at the calls that the documentation allows and the other tests do not make:
-output pools 16 bytes off a sector (needs a GPU)."""
+output pools 16 bytes off a sector, lengths far below what long tables have room for (needs a GPU)."""
 import numpy as np
 import pytest
 
 from tests import paged8_util as V
-from tests.test_gpu_paged8 import DEV, TYPES, _i32, _random_codes, _tables, _to_pool
+from tests.test_gpu_paged8 import DEV, TYPES, _attend_state, _check_attend, _i32, _np, _random_codes, _tables, _to_pool
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -52,3 +52,28 @@ def test_read_to_32_bits_16_bytes_off_a_sector(k_off, v_off, fmt, d, layout):
                 want[b * mp + j // ps, j % ps] = V.decode(c[page, j % ps], fmt).astype(np.float32) * s[page, :, j % ps // block][:, None]
         got = got.cpu().transpose(1, 2) if layout == "head" else got.cpu()
         assert torch.equal(got, torch.from_numpy(want))
+
+
+# --- attention of single tokens -----------------------------------------------------
+
+@pytest.mark.parametrize("length", [0, 1, 65, 100, 128, 300])
+@pytest.mark.parametrize("hkv,d", [(65, 64), (70, 128)])
+def test_attend_short_requests_in_very_long_tables(hkv, d, length):
+    """Tables of 2^31 tokens (units counted in 64 bits) and a request of a few blocks: fewer units than CTAs."""
+    from dictionary_sparse_kv_gb300 import fadkv as F
+    rng = np.random.default_rng(length)
+    ps, fmt = 1024, "e4m3"
+    table, P, codes, scales = _attend_state(rng, [length], hkv, d, fmt, ps, 128, "head")
+    pools = [_to_pool(c, "head", fmt) for c in codes] + [torch.from_numpy(s).to(DEV) for s in scales]
+    wide = torch.full((1, (1 << 21) - 5), -1, dtype=torch.int32, device=DEV)
+    wide[:, :table.shape[1]] = _i32(table)
+    q = torch.randn((1, hkv, d), generator=torch.Generator().manual_seed(7)).half().to(DEV)
+    out, lse = torch.empty_like(q), torch.empty((1, hkv), device=DEV)
+    p = F.paged8_params(q, out, pools[0], pools[2], "head", wide)
+    ws = torch.zeros(F.paged8_attend_workspace_bytes(p), dtype=torch.uint8, device=DEV)
+    want = V.attend(_np(q), codes[0], codes[1], scales[0], scales[1], table, [length], 0, 0, d ** -0.5, fmt)
+    for _ in range(3):                                  # the workspace is left fit for the next call
+        out.fill_(9), lse.fill_(9)
+        F.paged8_attend(p, *pools, wide, _i32([length]), q, out, lse, ws)
+        torch.cuda.synchronize()
+        _check_attend((out, lse), want, max(length, 1), d, torch.float16)
