@@ -348,6 +348,7 @@ paged8_attend_kernel(const __grid_constant__ Paged8Args a)
         if (f.seen) {
             const size_t at = scale_at(f.page, w.hk, token_of(w, t + lane) & ((1 << a.shift) - 1), a.p.Hkv, a.shift, a.bshift);
             f.ks = __ldg(a.k_scales + at);
+            f.ks = fmaf(f.ks, 0.f, f.ks);                              // an infinity as NaN: its score would be -inf, which nothing shows
             f.ls = __log2f(__ldg(a.v_scales + at));
         }
     };

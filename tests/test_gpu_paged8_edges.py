@@ -1,10 +1,11 @@
 """The 8-bit paged cache and the prompts' attention at the calls that the documentation allows and the other tests do not make:
-output pools 16 bytes off a sector, lengths far below what long tables have room for (needs a GPU)."""
+output pools 16 bytes off a sector, lengths far below what long tables have room for, scales that are not
+finite (needs a GPU)."""
 import numpy as np
 import pytest
 
 from tests import paged8_util as V
-from tests.test_gpu_paged8 import DEV, TYPES, _attend_state, _check_attend, _i32, _np, _random_codes, _tables, _to_pool
+from tests.test_gpu_paged8 import DEV, TYPES, _attend, _attend_state, _check_attend, _i32, _np, _random_codes, _tables, _to_pool
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -77,3 +78,32 @@ def test_attend_short_requests_in_very_long_tables(hkv, d, length):
         F.paged8_attend(p, *pools, wide, _i32([length]), q, out, lse, ws)
         torch.cuda.synchronize()
         _check_attend((out, lse), want, max(length, 1), d, torch.float16)
+
+
+@pytest.mark.parametrize("bad", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("fmt,d", [("e4m3", 64), ("i8", 64), ("e4m3", 128), ("i8", 128)])
+def test_attend_scales_that_are_not_finite(fmt, d, sign, bad):
+    """A seen block's scale that is not finite makes what it enters NaN, whatever the products' signs: of the keys, the rows and
+    lse of the heads that read it; of the values, the rows alone.  Nothing else changes."""
+    rng = np.random.default_rng(2)
+    lens, hkv, ps = [40, 300], 2, 16
+    table, P, codes, scales = _attend_state(rng, lens, hkv, d, fmt, ps, 16, "head")
+    positive = np.abs(V.decode(codes[0], fmt)) + 1
+    codes[0] = V.encode(positive.clip(1, 127), fmt)
+    q = sign * torch.rand((2, 2 * hkv, d), generator=torch.Generator().manual_seed(1)).add(0.5).half().to(DEV)
+    pools = [_to_pool(c, "head", fmt) for c in codes] + [torch.from_numpy(s.copy()).to(DEV) for s in scales]
+    out0, lse0 = _attend(q, pools, "head", table, lens)
+    assert out0.isfinite().all() and lse0.isfinite().all()
+    rows = torch.zeros((2, 2 * hkv), dtype=torch.bool, device=DEV)
+    rows[0, 2:] = True                                  # request 0, the heads over KV head 1
+    for which in (2, 3):                                # of the keys, of the values
+        was = pools[which][table[0, 1], 1, 0].clone()
+        pools[which][table[0, 1], 1, 0] = bad
+        out, lse = _attend(q, pools, "head", table, lens)
+        assert torch.equal(out.isnan(), rows[..., None].expand_as(out)) and torch.equal(out[~rows], out0[~rows])
+        if which == 2:
+            assert torch.equal(lse.isnan(), rows) and torch.equal(lse[~rows], lse0[~rows])
+        else:
+            assert torch.equal(lse, lse0)
+        pools[which][table[0, 1], 1, 0] = was
