@@ -1045,6 +1045,23 @@ struct PreShape {
     int split;                 // 0: items are not cut; else the tiles of an item that can hold rows
 };
 
+// Whether a call of B requests whose rows fill `items` items at least may cut them.  Cutting can pay only if they are fewer than
+// the multiprocessors, however the rows are spread over requests, and if there can be keys for two pieces.  How many pieces
+// there are is decided on the device.  (What fewer requests and items, more rows and keys take from a yes is never a no.)
+bool may_cut(const fadkv_paged_params& p, bool rows, int B, long long items)
+{
+    long long most = (long long)p.max_pages * p.page_size;
+    if (p.window > 0) most = most < (long long)p.window + p.sinks + 2 * kKeys ? most : (long long)p.window + p.sinks + 2 * kKeys;
+    if (B > 256 || items > kPreCtas || most < 2 * kLeastTiles * kKeys) return false;
+    if (!rows) return true;
+    // Prompts: T bounds the keys, mostly from far above, so the longest prompt is taken for twice the mean.  Cutting saves
+    // its key tiles' time (1.2 us each) but for items / 152 of it, and the pieces and their join cost some 10 us (8 heads over
+    // 1 of 128, 1500 tokens in 47 items: 21.2 us cut and 21.7 whole; 8 over 2, 1100 in 36: 23.5 and 20.2; 24 over 8, 1100
+    // in 112: 33 and 19; one head, 4000 in 16: 18 and 50).
+    const long long keys = std::min(std::min(most, (long long)p.T), 2ll * p.T / std::max(B, 1));
+    return 3 * items <= kPreCtas && keys / kKeys * (kPreCtas - items) >= 1300;
+}
+
 PreShape pre_shape(const fadkv_paged_params& p, bool rows)
 {
     PreShape s;
@@ -1054,20 +1071,7 @@ PreShape pre_shape(const fadkv_paged_params& p, bool rows)
     s.tq = kRows / s.gch;
     const long long heads = (long long)p.Hkv * s.chunks, tiles = p.T / (2 * s.tq);
     s.items = (tiles + (p.B < p.T ? p.B : p.T)) * heads;           // one more a request than its rows fill
-    // Cutting can pay only if the rows fill fewer items than there are multiprocessors, however they are spread over
-    // requests, and if there can be keys for two pieces.  How many pieces there are is decided on the device.
-    long long most = (long long)p.max_pages * p.page_size;
-    if (p.window > 0) most = most < (long long)p.window + p.sinks + 2 * kKeys ? most : (long long)p.window + p.sinks + 2 * kKeys;
-    bool cut = p.B <= 256 && (tiles + 1) * heads <= kPreCtas && most >= 2 * kLeastTiles * kKeys;
-    if (rows && cut) {
-        // Prompts: T bounds the keys, mostly from far above, so the longest prompt is taken for twice the mean.  Cutting saves
-        // its key tiles' time (1.2 us each) but for items / 152 of it, and the pieces and their join cost some 10 us (8 heads over
-        // 1 of 128, 1500 tokens in 47 items: 21.2 us cut and 21.7 whole; 8 over 2, 1100 in 36: 23.5 and 20.2; 24 over 8, 1100
-        // in 112: 33 and 19; one head, 4000 in 16: 18 and 50).
-        const long long keys = std::min(std::min(most, (long long)p.T), 2ll * p.T / std::max(p.B, 1)), items = (tiles + 1) * heads;
-        cut = 3 * items <= kPreCtas && keys / kKeys * (kPreCtas - items) >= 1300;
-    }
-    s.split = !cut ? 0 : (p.T <= s.tq ? 1 : 2);
+    s.split = !may_cut(p, rows, p.B, (tiles + 1) * heads) ? 0 : (p.T <= s.tq ? 1 : 2);
     return s;
 }
 
@@ -1107,6 +1111,13 @@ cudaError_t launch_t(const PagedArgs& a, cudaStream_t st, bool rows)
 size_t paged_prefill_workspace(const fadkv_paged_params& p, bool rows)
 {
     return kHeadBytes + (size_t)kSplitSlots * pre_shape(p, rows).split * slot_floats(p.d) * sizeof(float);
+}
+
+size_t paged_prefill_workspace_most(const fadkv_paged_params& p, bool rows)
+{
+    const PreShape s = pre_shape(p, rows);
+    const bool cut = p.B > 0 && may_cut(p, rows, 1, (long long)p.Hkv * s.chunks);
+    return kHeadBytes + (size_t)kSplitSlots * (!cut ? 0 : p.T <= s.tq ? 1 : 2) * slot_floats(p.d) * sizeof(float);
 }
 
 cudaError_t launch_paged_prefill(const PagedArgs& a, cudaStream_t st, bool rows)

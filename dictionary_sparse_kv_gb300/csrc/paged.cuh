@@ -65,7 +65,10 @@ size_t paged_attend_workspace(const fadkv_paged_params& p);
 cudaError_t launch_paged_attend(const PagedArgs& a, cudaStream_t st);
 // With `rows` set, keys and values are rows like the queries: a.k and a.v
 // rows, their pages the multiples of a.p.page_size (128) of a request's own.
+// The workspace that this call needs, and what a call of no more requests, rows and pages can need (few rows are cut, many are
+// not, so that the first alone does not grow with them).
 size_t paged_prefill_workspace(const fadkv_paged_params& p, bool rows = false);
+size_t paged_prefill_workspace_most(const fadkv_paged_params& p, bool rows = false);
 cudaError_t launch_paged_prefill(const PagedArgs& a, cudaStream_t st, bool rows = false);
 
 namespace paged {

@@ -307,7 +307,7 @@ fadkv_status fadkv_paged_prefill_workspace_bytes(const fadkv_paged_params* p, si
     const fadkv_status st = check_paged(p);
     if (st != FADKV_OK) return st;
     if (!bytes) return FADKV_ERR_INVALID_ARG;
-    *bytes = paged_prefill_workspace(*p);
+    *bytes = paged_prefill_workspace_most(*p);
     return FADKV_OK;
 }
 
@@ -526,7 +526,7 @@ fadkv_status fadkv_prompt_attend_workspace_bytes(const fadkv_prompt_params* p, s
     const fadkv_status st = check_prompt(p);
     if (st != FADKV_OK) return st;
     if (!bytes) return FADKV_ERR_INVALID_ARG;
-    *bytes = paged_prefill_workspace(prompt_shape(*p), true);
+    *bytes = paged_prefill_workspace_most(prompt_shape(*p), true);
     return FADKV_OK;
 }
 

@@ -633,6 +633,10 @@ fadkv_status fadkv_paged_status(void* workspace, uint64_t* host_out, int32_t cle
    now on, in the whole process (0 = the default, 200 ms).  Host-only. */
 fadkv_status fadkv_debug_paged_wait_limit(uint64_t limit_ns);
 
+/* Device workspace fadkv_paged_prefill needs (host-only; writes *bytes): enough
+   for every call of no more requests, rows and pages a request that is alike
+   otherwise, so that a workspace for the longest step serves the others too.
+   Errors: INVALID_ARG, UNSUPPORTED. */
 fadkv_status fadkv_paged_prefill_workspace_bytes(const fadkv_paged_params* params, size_t* bytes);
 
 /* ---------------------------------------------------------------------------
@@ -790,7 +794,8 @@ fadkv_status fadkv_prompt_attend(const fadkv_prompt_params* params, const void* 
                                  const int32_t* starts, const int32_t* positions, void* out, float* lse,
                                  void* workspace, size_t workspace_bytes, void* stream);
 
-/* Device workspace fadkv_prompt_attend needs (host-only; writes *bytes).
+/* Device workspace fadkv_prompt_attend needs (host-only; writes *bytes): enough
+   for every call of no more prompts and rows that is alike otherwise.
    Errors: INVALID_ARG, UNSUPPORTED. */
 fadkv_status fadkv_prompt_attend_workspace_bytes(const fadkv_prompt_params* params, size_t* bytes);
 
