@@ -578,7 +578,7 @@ def _pool8(pages, layout, scales, v_pages, v_scales):
         raise ValueError("an 8-bit pool is of float8_e4m3fn or int8")
     hkv, ps, *strides = _pool(pages, layout)
     _check_pools(pages, v_pages)
-    if scales.dim() != 3 or scales.shape[2] < 1 or ps % scales.shape[2]:
+    if scales is None or scales.dim() != 3 or scales.shape[2] < 1 or ps % scales.shape[2]:
         raise ValueError("scales are [pages][Hkv][page size / block]")
     shape = (pages.shape[0], hkv, scales.shape[2])
     _check_dense("scales", scales, shape, torch.float32)
@@ -594,7 +594,7 @@ def _check_rows(*rows):
 
 def _check_table(table, shape=None):
     import torch
-    if table.dim() != 2 or table.dtype != torch.int32 or not table.is_contiguous() or (shape and tuple(table.shape) != tuple(shape)):
+    if table is None or table.dim() != 2 or table.dtype != torch.int32 or not table.is_contiguous() or (shape and tuple(table.shape) != tuple(shape)):
         raise ValueError("block tables are contiguous [B][max_pages] int32")
 
 
