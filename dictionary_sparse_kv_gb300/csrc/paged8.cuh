@@ -78,7 +78,6 @@ __device__ __forceinline__ void prefetch_tables(const int32_t* lengths, const in
 template <int FORMAT> struct Code;
 
 template <> struct Code<FADKV_E4M3> {
-    static constexpr float kMost = 448.f;
     // bytes 0, 1 and bytes 2, 3
     static __device__ __forceinline__ void halves(uint32_t x, uint32_t& a, uint32_t& b)
     {
@@ -114,7 +113,6 @@ template <> struct Code<FADKV_E4M3> {
 };
 
 template <> struct Code<FADKV_I8> {
-    static constexpr float kMost = 127.f;
     static __device__ __forceinline__ uint32_t centred(uint32_t x)      // 1024 + 128 + code, less 1152
     {
         const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&x), __half2half2(__ushort_as_half(0x6480)));
