@@ -63,8 +63,10 @@ def test_attend_short_requests_in_very_long_tables(hkv, d, length):
     """Tables of 2^31 tokens (units counted in 64 bits) and a request of a few blocks: fewer units than CTAs."""
     from dictionary_sparse_kv_gb300 import fadkv as F
     rng = np.random.default_rng(length)
-    ps, fmt = 1024, "e4m3"
-    table, P, codes, scales = _attend_state(rng, [length], hkv, d, fmt, ps, 128, "head")
+    ps, fmt, P = 1024, "i8", 2
+    table = np.array([[1, -1]], np.int32)
+    codes = [rng.integers(-127, 128, (P, ps, hkv, d), np.int8).view(np.uint8) for _ in range(2)]
+    scales = [np.exp(rng.normal(-4.6, 1, (P, hkv, 8))).astype(np.float32) for _ in range(2)]
     pools = [_to_pool(c, "head", fmt) for c in codes] + [torch.from_numpy(s).to(DEV) for s in scales]
     wide = torch.full((1, (1 << 21) - 5), -1, dtype=torch.int32, device=DEV)
     wide[:, :table.shape[1]] = _i32(table)
