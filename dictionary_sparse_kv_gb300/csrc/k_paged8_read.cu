@@ -23,7 +23,8 @@ constexpr int kTile = 16;
 template <int D> constexpr int kPerSm = D == 128 ? 4 : 6;
 
 // SECTORS: the output pools lie on multiples of 32 bytes (the launcher looks), and so does every row of them, whose strides are
-// multiples of 32 bytes.
+// multiples of 32 bytes.  (16 requests of up to 4096 tokens of 8 heads of 128 to 32 bits: 58 us; two 16-byte stores, a sector's
+// halves apart, 74.)
 template <bool SECTORS>
 __device__ __forceinline__ void store8(float* p, const float* y)
 {

@@ -29,6 +29,13 @@
 // (with m the maximum 32768 keys 17.5 below one whose value is 0 came out as
 // 0).  bfloat16 has the exponents of 32 bits, and m is the maximum there.
 //
+// p is rounded once to the type of v (half a step at most, 2^-8 of it in bfloat16,
+// 2^-11 in binary16), as tensor cores that bound the kernel take it; l is the sum of the
+// unrounded ones.  The roundings are independent, so that out's error, which the
+// rounding of out itself sets (2-norm over 2-norm 1.65e-3 in bfloat16, 2.1e-4 in
+// binary16), comes to 1.1 (300 keys) to 1.35 (6000) times that: 2.15e-3, 2.8e-4.  A
+// second term would be half as many products again.
+//
 // K and V pages come by TMA, one box a page and 64-element half, through one
 // ring of stages; pages outside the pool and pages that no row sees are asked
 // for outside the map and arrive as zeros.  Keys that a row does not see are
@@ -53,7 +60,7 @@
 // Packed prompts (ROWS) are the same with keys and values as rows of their own:
 // a key tile is one box a half, rows behind the prompt's last one are masked
 // and cleared as those of a page are.  4 prompts of up to 6000 tokens, 32 heads
-// over 8 of 128 in bfloat16: 385 to 425 us by the power limit, 1.5 to 1.6
+// over 8 of 128 in bfloat16: 385 to 433 us by the power limit, 1.45 to 1.6
 // PFLOP/s; a part of the exponentials as polynomials on the other pipes cost more
 // than it saved at either d (5 of 16 pairs at d = 64: 69.5 -> 74 us for prompts with
 // a window; 2 of 16 at 128: 385 -> 430): the special-function units do not bound it.

@@ -718,7 +718,8 @@ typedef struct {
                  request b are read
      out_table   [B][max_pages] int32 or null: the output page that takes page
                  i of request b; null: page b * max_pages + i
-     k_out, v_out  output pools, 16-byte aligned
+     k_out, v_out  output pools, 16-byte aligned (of 32 bits: 32-byte aligned
+                 ones are written faster)
    Tokens on pages outside [0, num_pages), or for output pages outside
    [0, out_pages), are skipped; what is not read back is left as it is.
    Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
@@ -748,7 +749,9 @@ typedef struct {
    and one workspace (of the largest size) may serve these calls in turn.
    Scores, softmax and sums in 32 bits; bfloat16 queries enter the product with
    the codes as binary16 values, scaled by a power of two for each head (exact
-   but for elements below 2^-28 of the head's largest); the probabilities,
+   but for elements below 2^-28 of the head's largest); I8 keys enter it as
+   code + 128, put right by the sum of the query, so that a score is rounded as
+   that of codes of that size, small ones too; the probabilities,
    times the scales of the values, enter the product with the codes as two
    binary16 terms (22 bits; one below 2^-36 of the largest is lost).  A seen
    code that is NaN, or a scale that is not finite, makes what it enters NaN;
